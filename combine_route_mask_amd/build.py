@@ -14,7 +14,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libmoe_ep.so")
-SOURCES = ["exchange.hip", "agrs.hip", "api.cpp"]
+SOURCES = ["exchange.hip", "agrs.hip", "api.cpp", "experts.hip", "norm_quant.hip", "matmul_int8.hip",
+           "experts_api.cpp"]
 # reference kernels of the benchmark (measurement only; the exchange never calls them)
 CEILINGS_LIB = os.path.join(HERE, "libmoe_ep_ceilings.so")
 CEILINGS_SOURCES = ["ceilings.hip"]

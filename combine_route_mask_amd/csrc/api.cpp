@@ -10,6 +10,7 @@
 #include <string>
 #include <unordered_set>
 
+#include "experts_internal.h"
 #include "moe_ep.h"
 #include "moe_ep_internal.h"
 
@@ -25,15 +26,9 @@ struct moe_ep_handle {
     int32_t n[MOE_EP_MAX_RANKS];      // token counts of the last dispatch
 };
 
-namespace {
+namespace moe_ep {
 
-thread_local std::string g_err;
-
-// Handles created and not yet destroyed.  Looking a pointer up here (rather
-// than reading through it) keeps destroy idempotent and lets every entry
-// point reject stale handles without touching freed memory.
-std::mutex g_handles_mu;
-std::unordered_set<const moe_ep_handle *> g_handles;
+static thread_local std::string g_err;
 
 int fail(int code, const std::string &msg)
 {
@@ -46,6 +41,16 @@ int ok()
     g_err.clear();
     return MOE_EP_OK;
 }
+
+} // namespace moe_ep
+
+namespace {
+
+// Handles created and not yet destroyed.  Looking a pointer up here (rather
+// than reading through it) keeps destroy idempotent and lets every entry
+// point reject stale handles without touching freed memory.
+std::mutex g_handles_mu;
+std::unordered_set<const moe_ep_handle *> g_handles;
 
 int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
 

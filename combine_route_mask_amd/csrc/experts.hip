@@ -1,0 +1,722 @@
+// gfx950 kernels of the expert sort (rows to expert order), its way back
+// with weights, and the gradients.  All of them move rows and do little
+// else, so HBM bounds the large ones and the launches the small ones.
+//
+// The order is a stable counting sort by expert id: place(p) = number of
+// counted pairs with a smaller id, plus those with the same id before p.
+// Every place is an integer sum, so no atomic's order reaches a result.
+#include "experts_internal.h"
+#include "rows.h"
+
+namespace moe_ep {
+namespace {
+
+// Local expert of id on rank r, or -1 (unsigned compare covers both ends).
+__device__ __forceinline__ int local_expert(int32_t id, int r, int epr)
+{
+    const uint32_t e = (uint32_t)id - (uint32_t)(r * epr);
+    return e < (uint32_t)epr ? (int)e : -1;
+}
+
+__device__ __forceinline__ const int32_t *rank_ids(const moe_ep_sort_args &a, int r)
+{
+    return reinterpret_cast<const int32_t *>(reinterpret_cast<const uint8_t *>(a.ids) +
+                                             (int64_t)r * a.ids_rank_stride);
+}
+
+// ---------------------------------------------------------------------------
+// Rows of one slot to their places.  `pos` holds in lane base + j the place
+// of pair j (or -1); every wave of the workgroup holds the same.
+// ---------------------------------------------------------------------------
+
+// Copies n bytes to each of the slot's places, in words of type W.
+template <typename W, int BS>
+__device__ __forceinline__ void copy_small(const uint8_t *src, uint8_t *dst, int64_t n, int pos, int base,
+                                           uint64_t pairs)
+{
+    for (int64_t i = threadIdx.x; i < n / (int64_t)sizeof(W); i += BS) {
+        const W v = reinterpret_cast<const W *>(src)[i];
+        for (uint64_t m = pairs; m; m &= m - 1) {
+            const int64_t p = __builtin_amdgcn_readlane(pos, base + __builtin_ctzll(m));
+            reinterpret_cast<W *>(dst + p * n)[i] = v;
+        }
+    }
+}
+
+template <int BS>
+__device__ __forceinline__ void copy_scale_row(const moe_ep_sort_args &a, int r, int q, int pos, int base,
+                                               uint64_t pairs)
+{
+    const int64_t n = a.scale_row_bytes;
+    const uint8_t *src = static_cast<const uint8_t *>(a.scales) + (int64_t)r * a.scales_rank_stride + q * n;
+    uint8_t *dst = static_cast<uint8_t *>(a.out_scales);
+    const uint64_t align = (uint64_t)(uintptr_t)a.scales | (uint64_t)a.scales_rank_stride | (uint64_t)n |
+                           (uint64_t)(uintptr_t)dst;
+    if ((align & 15) == 0)
+        copy_small<u32x4, BS>(src, dst, n, pos, base, pairs);
+    else if ((align & 3) == 0)
+        copy_small<uint32_t, BS>(src, dst, n, pos, base, pairs);
+    else
+        copy_small<uint8_t, BS>(src, dst, n, pos, base, pairs);
+}
+
+// Largest magnitude over the workgroup; `red` holds a word for each wave.
+template <int BS>
+__device__ __forceinline__ uint32_t block_max(uint32_t top, uint32_t *red)
+{
+    top = wave_max(top);
+    if (BS > 64) {
+        __syncthreads(); // the last use of red is over
+        if ((threadIdx.x & 63) == 0)
+            red[threadIdx.x >> 6] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < BS / 64; ++w)
+            top = top > red[w] ? top : red[w];
+    }
+    return top;
+}
+
+// One slot's row as int8 codes to its places, by the whole workgroup.  A
+// thread keeps its first two 16-element units in registers between the
+// amax and the codes (rows of up to 32 * BS elements are read once); longer
+// rows are read again from the cache.
+template <typename T, int BS>
+__device__ __forceinline__ void quantize_slot(const moe_ep_sort_args &a, const uint8_t *row, int pos, int base,
+                                              uint64_t pairs, uint32_t *red)
+{
+    constexpr int kHeld = 2;
+    const int n = (int)(a.row_bytes / RowType<T>::kBytes), units = n / 16;
+    float f[kHeld][16];
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+        const int i = threadIdx.x + u * BS;
+        if (i < units) {
+            load_elements<T, 16>(row + (int64_t)i * 16 * RowType<T>::kBytes, f[u]);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                top = max(top, magnitude(f[u][e]));
+        }
+    }
+    for (int i = threadIdx.x + kHeld * BS; i < units; i += BS) {
+        float g[16];
+        load_elements<T, 16>(row + (int64_t)i * 16 * RowType<T>::kBytes, g);
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            top = max(top, magnitude(g[e]));
+    }
+    const Int8Row rule(block_max<BS>(top, red));
+    uint8_t *out = static_cast<uint8_t *>(a.out_rows);
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+        const int i = threadIdx.x + u * BS;
+        if (i < units) {
+            const u32x4 v = rule.codes16(f[u]);
+            for (uint64_t m = pairs; m; m &= m - 1)
+                *reinterpret_cast<u32x4 *>(out + (int64_t)__builtin_amdgcn_readlane(pos, base + __builtin_ctzll(m)) * n + 16 * i) = v;
+        }
+    }
+    for (int i = threadIdx.x + kHeld * BS; i < units; i += BS) {
+        float g[16];
+        load_elements<T, 16>(row + (int64_t)i * 16 * RowType<T>::kBytes, g);
+        const u32x4 v = rule.codes16(g);
+        for (uint64_t m = pairs; m; m &= m - 1)
+            *reinterpret_cast<u32x4 *>(out + (int64_t)__builtin_amdgcn_readlane(pos, base + __builtin_ctzll(m)) * n + 16 * i) = v;
+    }
+    if (threadIdx.x == 0)
+        for (uint64_t m = pairs; m; m &= m - 1)
+            static_cast<float *>(a.out_scales)[__builtin_amdgcn_readlane(pos, base + __builtin_ctzll(m))] = rule.scale;
+}
+
+// The k bits of a slot's pairs in a wave's ballot.
+__device__ __forceinline__ uint64_t slot_pairs(uint64_t ballot, int i, int k)
+{
+    const uint64_t all = k == 64 ? ~0ull : (1ull << k) - 1;
+    return (ballot >> (i * k)) & all;
+}
+
+// ---------------------------------------------------------------------------
+// Small sorts: one launch.  Each workgroup places its slot's k pairs by
+// counting over all pairs (at most 2048, eight a thread), which takes less
+// than a second launch would; the last workgroup writes counts and offsets.
+// ---------------------------------------------------------------------------
+
+constexpr int kDirectBlock = 256;
+
+template <typename T, bool QUANT>
+__global__ __launch_bounds__(kDirectBlock) void sort_direct_kernel(moe_ep_sort_args a, int nchunk)
+{
+    constexpr int BS = kDirectBlock;
+    const int S = a.slots, k = a.top_k, epr = a.experts_per_rank, per_rank = S * k;
+    const int npairs = a.ranks * per_rank, nslots = a.ranks * S, lane = threadIdx.x & 63;
+    __shared__ int32_t lds[kSortDirectExperts];
+    __shared__ uint32_t red[BS / 64];
+
+    if ((int)blockIdx.x == nslots * nchunk) { // counts and offsets
+        const int E = a.ranks * epr;
+        for (int e = threadIdx.x; e < E; e += BS)
+            lds[e] = 0;
+        __syncthreads();
+        for (int p = threadIdx.x; p < npairs; p += BS) {
+            const int r = p / per_rank;
+            const int e = local_expert(rank_ids(a, r)[p - r * per_rank], r, epr);
+            if (e >= 0)
+                atomicAdd(&lds[r * epr + e], 1);
+        }
+        __syncthreads();
+        if (threadIdx.x < 64) {
+            const int per = (E + 63) / 64, lo = min(E, lane * per), hi = min(E, lo + per);
+            int sum = 0;
+            for (int e = lo; e < hi; ++e)
+                sum += lds[e];
+            int before = sum;
+            for (int m = 1; m < 64; m <<= 1) {
+                const int y = __shfl_up(before, m);
+                before += lane >= m ? y : 0;
+            }
+            before -= sum;
+            for (int e = lo; e < hi; ++e) {
+                a.counts[e] = lds[e];
+                a.offsets[e] = (int32_t)min((int64_t)before, a.capacity);
+                before += lds[e];
+            }
+            if (lane == 63)
+                a.offsets[E] = (int32_t)min((int64_t)before, a.capacity);
+        }
+        return;
+    }
+    const int slot = blockIdx.x / nchunk, c = blockIdx.x % nchunk;
+    const int r = slot / S, q = slot % S;
+    const uint8_t *row = static_cast<const uint8_t *>(a.rows) + (int64_t)r * a.rows_rank_stride + q * a.row_bytes;
+    // the row's loads go out before the places are known
+    const int64_t at = ((int64_t)c * BS + threadIdx.x) * 16;
+    u32x4 v = {0, 0, 0, 0};
+    if (!QUANT && at < a.row_bytes)
+        v = load16_nt(row + at);
+
+    const int mine = slot * k; // first pair of the slot
+    int key = -1;              // lane j: global expert of pair j
+    if (lane < k) {
+        const int e = local_expert(rank_ids(a, r)[q * k + lane], r, epr);
+        key = e < 0 ? -1 : r * epr + e;
+    }
+    if (threadIdx.x < 64)
+        lds[threadIdx.x] = 0;
+    __syncthreads();
+    const uint64_t counted = __ballot(key >= 0);
+    int before = 0; // lane j: pairs ahead of pair j among this wave's
+    if (counted) {
+        for (int p0 = 0; p0 < npairs; p0 += BS) {
+            const int p = p0 + threadIdx.x;
+            int other = 0x7FFFFFFF;
+            if (p < npairs) {
+                const int rp = p / per_rank;
+                const int e = local_expert(rank_ids(a, rp)[p - rp * per_rank], rp, epr);
+                other = e < 0 ? other : rp * epr + e;
+            }
+            for (uint64_t m = counted; m; m &= m - 1) {
+                const int j = __builtin_ctzll(m);
+                const int kj = __builtin_amdgcn_readlane(key, j);
+                const int n = __popcll(__ballot(other < kj || (other == kj && p < mine + j)));
+                before += lane == j ? n : 0;
+            }
+        }
+        if (lane < k)
+            atomicAdd(&lds[lane], before);
+    }
+    __syncthreads();
+    int pos = key >= 0 ? lds[lane] : -1;
+    pos = pos < a.capacity ? pos : -1;
+    if (c == 0 && (int)threadIdx.x < k)
+        a.position[(int64_t)mine + lane] = pos;
+    const uint64_t pairs = __ballot(pos >= 0);
+    if (!pairs)
+        return;
+    if (QUANT) {
+        quantize_slot<T, BS>(a, row, pos, 0, pairs, red);
+        return;
+    }
+    if (at < a.row_bytes) {
+        uint8_t *out = static_cast<uint8_t *>(a.out_rows) + at;
+        for (uint64_t m = pairs; m; m &= m - 1)
+            *reinterpret_cast<u32x4 *>(out + (int64_t)__builtin_amdgcn_readlane(pos, __builtin_ctzll(m)) * a.row_bytes) = v;
+    }
+    if (c == 0 && a.scale_row_bytes)
+        copy_scale_row<BS>(a, r, q, pos, 0, pairs);
+}
+
+// ---------------------------------------------------------------------------
+// Large sorts: counts by tile, one scan, places by tile, then the rows.
+// ---------------------------------------------------------------------------
+
+constexpr int kTileBlock = 256;
+
+// ws[(r * epr + e) * tiles + t]: pairs of expert e in tile t of rank r.
+__global__ __launch_bounds__(kTileBlock) void sort_count_kernel(moe_ep_sort_args a, int tiles)
+{
+    extern __shared__ int32_t hist[];
+    const int r = blockIdx.x / tiles, t = blockIdx.x % tiles, epr = a.experts_per_rank;
+    for (int e = threadIdx.x; e < epr; e += kTileBlock)
+        hist[e] = 0;
+    __syncthreads();
+    const int per = sort_tile_slots(a.top_k) * a.top_k;
+    const int64_t lo = (int64_t)t * per, hi = min(lo + per, (int64_t)a.slots * a.top_k);
+    const int32_t *ids = rank_ids(a, r);
+    for (int64_t p = lo + threadIdx.x; p < hi; p += kTileBlock) {
+        const int e = local_expert(ids[p], r, epr);
+        if (e >= 0)
+            atomicAdd(&hist[e], 1);
+    }
+    __syncthreads();
+    int32_t *ws = static_cast<int32_t *>(a.workspace);
+    for (int e = threadIdx.x; e < epr; e += kTileBlock)
+        ws[((int64_t)r * epr + e) * tiles + t] = hist[e];
+}
+
+constexpr int kScanBlock = 1024;
+
+// Exclusive prefix of ws in place (expert-major, so that an expert's first
+// entry becomes its first place), offsets and counts.  One workgroup: the
+// table has one entry for each 2048 pairs and expert.
+__global__ __launch_bounds__(kScanBlock) void sort_scan_kernel(moe_ep_sort_args a, int tiles)
+{
+    __shared__ int32_t first[MOE_EP_MAX_SORT_EXPERTS + 1];
+    __shared__ int32_t sums[kScanBlock / 64];
+    const int E = a.ranks * a.experts_per_rank, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n = (int64_t)E * tiles;
+    int32_t *ws = static_cast<int32_t *>(a.workspace);
+    const int64_t per = (n + kScanBlock - 1) / kScanBlock;
+    const int64_t lo = min(n, (int64_t)threadIdx.x * per), hi = min(n, lo + per);
+    int sum = 0;
+    for (int64_t i = lo; i < hi; ++i)
+        sum += ws[i];
+    int before = sum;
+    for (int m = 1; m < 64; m <<= 1) {
+        const int y = __shfl_up(before, m);
+        before += lane >= m ? y : 0;
+    }
+    if (lane == 63)
+        sums[wave] = before;
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < kScanBlock / 64; ++w) {
+        if (w == wave)
+            before += total;
+        total += sums[w];
+    }
+    before -= sum;
+    for (int64_t i = lo; i < hi; ++i) {
+        const int c = ws[i];
+        if (i % tiles == 0)
+            first[i / tiles] = before;
+        ws[i] = before;
+        before += c;
+    }
+    if (threadIdx.x == 0)
+        first[E] = total;
+    __syncthreads();
+    for (int e = threadIdx.x; e <= E; e += kScanBlock) {
+        a.offsets[e] = (int32_t)min((int64_t)first[e], a.capacity);
+        if (e < E)
+            a.counts[e] = first[e + 1] - first[e];
+    }
+}
+
+// Places of a tile's pairs.  Each wave takes a quarter of the tile in
+// order; pairs of 64 consecutive lanes with the same expert find each other
+// by ballots over the bits of the expert number.
+__global__ __launch_bounds__(kTileBlock) void sort_place_kernel(moe_ep_sort_args a, int tiles, int bits)
+{
+    extern __shared__ int32_t next[]; // [waves][epr]
+    constexpr int kWaves = kTileBlock / 64;
+    const int r = blockIdx.x / tiles, t = blockIdx.x % tiles, epr = a.experts_per_rank;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int e = threadIdx.x; e < kWaves * epr; e += kTileBlock)
+        next[e] = 0;
+    __syncthreads();
+    const int per = sort_tile_slots(a.top_k) * a.top_k;
+    const int64_t lo = (int64_t)t * per, hi = min(lo + per, (int64_t)a.slots * a.top_k);
+    const int share = ((per + kWaves - 1) / kWaves + 63) & ~63;
+    const int64_t wlo = min(hi, lo + (int64_t)wave * share), whi = min(hi, wlo + share);
+    const int32_t *ids = rank_ids(a, r);
+    int32_t *mine = next + wave * epr;
+    for (int64_t p = wlo + lane; p < whi; p += 64) {
+        const int e = local_expert(ids[p], r, epr);
+        if (e >= 0)
+            atomicAdd(&mine[e], 1);
+    }
+    __syncthreads();
+    const int32_t *ws = static_cast<const int32_t *>(a.workspace);
+    for (int e = threadIdx.x; e < epr; e += kTileBlock) {
+        int before = ws[((int64_t)r * epr + e) * tiles + t];
+        for (int w = 0; w < kWaves; ++w) {
+            const int c = next[w * epr + e];
+            next[w * epr + e] = before;
+            before += c;
+        }
+    }
+    __syncthreads();
+    int32_t *position = a.position + (int64_t)r * a.slots * a.top_k;
+    for (int64_t p0 = wlo; p0 < whi; p0 += 64) {
+        const int64_t p = p0 + lane;
+        const int e = p < whi ? local_expert(ids[p], r, epr) : -1;
+        uint64_t peers = __ballot(e >= 0);
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t m = __ballot((e >> b) & 1);
+            peers &= ((e >> b) & 1) ? m : ~m;
+        }
+        int place = -1;
+        if (e >= 0) {
+            const int leader = __builtin_ctzll(peers);
+            int start = 0;
+            if (lane == leader)
+                start = atomicAdd(&mine[e], __popcll(peers));
+            start = __shfl(start, leader);
+            place = start + __popcll(peers & ((1ull << lane) - 1));
+        }
+        if (p < whi)
+            position[p] = place < a.capacity ? place : -1;
+    }
+}
+
+constexpr int kGatherBlock = 256;
+constexpr int kGatherVectors = 2;
+
+// Rows to their places: item (group of g slots, chunk of the row).
+template <typename T, bool QUANT>
+__global__ __launch_bounds__(kGatherBlock) void sort_gather_kernel(moe_ep_sort_args a, int g, uint32_t nchunk,
+                                                                   uint32_t items)
+{
+    constexpr int BS = kGatherBlock, VPT = kGatherVectors;
+    __shared__ uint32_t red[BS / 64];
+    const int64_t nslots = (int64_t)a.ranks * a.slots;
+    const int k = a.top_k, lane = threadIdx.x & 63;
+    for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t s0 = (int64_t)(item / nchunk) * g;
+    const int c = (int)(item % nchunk), ns = (int)min((int64_t)g, nslots - s0);
+    const int pos = lane < ns * k ? a.position[s0 * k + lane] : -1;
+    const uint64_t ballot = __ballot(pos >= 0);
+    for (int i = 0; i < ns; ++i) {
+        const uint64_t pairs = slot_pairs(ballot, i, k);
+        if (!pairs)
+            continue;
+        const uint32_t slot = (uint32_t)(s0 + i);
+        const int r = (int)(slot / (uint32_t)a.slots), q = (int)(slot % (uint32_t)a.slots);
+        const uint8_t *row =
+            static_cast<const uint8_t *>(a.rows) + (int64_t)r * a.rows_rank_stride + (int64_t)q * a.row_bytes;
+        if (QUANT) {
+            quantize_slot<T, BS>(a, row, pos, i * k, pairs, red);
+            continue;
+        }
+        u32x4 v[VPT];
+        int64_t at[VPT];
+#pragma unroll
+        for (int u = 0; u < VPT; ++u) {
+            at[u] = (((int64_t)c * VPT + u) * BS + threadIdx.x) * 16;
+            if (at[u] < a.row_bytes)
+                v[u] = load16_nt(row + at[u]);
+        }
+        for (uint64_t m = pairs; m; m &= m - 1) {
+            uint8_t *out = static_cast<uint8_t *>(a.out_rows) +
+                           (int64_t)__builtin_amdgcn_readlane(pos, i * k + __builtin_ctzll(m)) * a.row_bytes;
+#pragma unroll
+            for (int u = 0; u < VPT; ++u)
+                if (at[u] < a.row_bytes)
+                    store16_nt(out + at[u], v[u]);
+        }
+        if (c == 0 && a.scale_row_bytes)
+            copy_scale_row<BS>(a, r, q, pos, i * k, pairs);
+    }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Back: sum of a slot's rows, weighted or not.
+// ---------------------------------------------------------------------------
+
+constexpr int kUnsortBlock = 128;
+constexpr int kUnsortRows = 8; // rows of a slot in flight
+
+// Item (group of g slots, chunk of 128 vectors): one output vector a lane.
+template <typename T, bool WEIGHTS>
+__global__ __launch_bounds__(kUnsortBlock) void unsort_kernel(moe_ep_unsort_args a, int g, uint32_t nchunk,
+                                                              uint32_t items)
+{
+    constexpr int BS = kUnsortBlock, G = kUnsortRows, N = RowType<T>::kPer;
+    const int64_t nslots = (int64_t)a.ranks * a.slots, row_bytes = (int64_t)a.hidden_size * RowType<T>::kBytes;
+    const int k = a.top_k, lane = threadIdx.x & 63;
+    for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t s0 = (int64_t)(item / nchunk) * g;
+    const int ns = (int)min((int64_t)g, nslots - s0);
+    const int64_t at = ((int64_t)(item % nchunk) * BS + threadIdx.x) * 16;
+    int pos = -1;
+    float w = 1.0f;
+    if (lane < ns * k) {
+        pos = a.position[s0 * k + lane];
+        if (WEIGHTS) {
+            const uint32_t slot = (uint32_t)s0 + (uint32_t)lane / (uint32_t)k, S = (uint32_t)a.slots;
+            w = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(a.weights) +
+                                                (int64_t)(slot / S) * a.weights_rank_stride)[(int64_t)(slot % S) * k + lane % k];
+        }
+    }
+    const uint64_t ballot = __ballot(pos >= 0 && pos < a.num_rows);
+    const uint8_t *rows = static_cast<const uint8_t *>(a.rows) + at;
+    for (int i = 0; i < ns; ++i) {
+        uint64_t pairs = slot_pairs(ballot, i, k);
+        if (!pairs && a.keep_empty)
+            continue;
+        float acc[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            acc[e] = 0.0f;
+        while (pairs) {
+            u32x4 v[G];
+            float wj[G];
+            uint64_t m = pairs;
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+                if (m) {
+                    const int j = i * k + __builtin_ctzll(m);
+                    m &= m - 1;
+                    wj[u] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), j));
+                    if (at < row_bytes)
+                        v[u] = load16_nt(rows + (int64_t)__builtin_amdgcn_readlane(pos, j) * row_bytes);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < G; ++u) {
+                if (pairs) {
+                    pairs &= pairs - 1;
+                    float f[N];
+                    RowType<T>::unpack(v[u], f);
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+                        acc[e] = WEIGHTS ? fmaf(wj[u], f[e], acc[e]) : acc[e] + f[e];
+                }
+            }
+        }
+        if (at < row_bytes) {
+            const uint32_t slot = (uint32_t)(s0 + i), S = (uint32_t)a.slots;
+            store16_nt(static_cast<uint8_t *>(a.out) + (int64_t)(slot / S) * a.out_rank_stride +
+                           (int64_t)(slot % S) * row_bytes + at,
+                       RowType<T>::pack(acc));
+        }
+    }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the weighted way back.
+// ---------------------------------------------------------------------------
+
+constexpr int kGradBlock = 256;
+constexpr int kGradVectors = 4;
+
+// One workgroup for a group of g slots.  The slot's grad_out row is held in
+// registers (256 * 4 vectors at a time) while each of its k rows passes once:
+// read for the dot product, written scaled.  The k dot products are summed
+// over lanes, then waves, in an order that the shape fixes.
+template <typename T>
+__global__ __launch_bounds__(kGradBlock) void unsort_grad_kernel(moe_ep_unsort_grad_args a, int g,
+                                                                 uint32_t items)
+{
+    constexpr int BS = kGradBlock, VPT = kGradVectors, N = RowType<T>::kPer, kWaves = BS / 64;
+    __shared__ float dots[kWaves][64];
+    const int64_t nslots = (int64_t)a.ranks * a.slots, row_bytes = (int64_t)a.hidden_size * RowType<T>::kBytes;
+    const int k = a.top_k, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int64_t s0 = (int64_t)item * g;
+    const int ns = (int)min((int64_t)g, nslots - s0);
+    int pos = -1;
+    float w = 1.0f;
+    if (lane < ns * k) {
+        pos = a.position[s0 * k + lane];
+        if (a.weights) {
+            const uint32_t slot = (uint32_t)s0 + (uint32_t)lane / (uint32_t)k, S = (uint32_t)a.slots;
+            w = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(a.weights) +
+                                                (int64_t)(slot / S) * a.weights_rank_stride)[(int64_t)(slot % S) * k + lane % k];
+        }
+    }
+    const uint64_t ballot = __ballot(pos >= 0 && pos < a.num_rows);
+    dots[wave][lane] = 0.0f;
+    for (int i = 0; i < ns; ++i) {
+        const uint64_t pairs = slot_pairs(ballot, i, k);
+        if (!pairs)
+            continue;
+        const uint32_t slot = (uint32_t)(s0 + i), S = (uint32_t)a.slots;
+        const uint8_t *go = static_cast<const uint8_t *>(a.grad_out) + (int64_t)(slot / S) * a.grad_out_rank_stride +
+                            (int64_t)(slot % S) * row_bytes;
+        for (int64_t c0 = threadIdx.x; c0 * 16 - threadIdx.x * 16 < row_bytes; c0 += BS * VPT) {
+            float f[VPT][N];
+#pragma unroll
+            for (int u = 0; u < VPT; ++u) {
+                const int64_t at = (c0 + u * BS) * 16;
+                u32x4 v = {0, 0, 0, 0};
+                if (at < row_bytes)
+                    v = load16_nt(go + at);
+                RowType<T>::unpack(v, f[u]);
+            }
+            for (uint64_t m = pairs; m; m &= m - 1) {
+                const int j = i * k + __builtin_ctzll(m);
+                const int64_t row = (int64_t)__builtin_amdgcn_readlane(pos, j) * row_bytes;
+                if (a.grad_weights) {
+                    u32x4 v[VPT];
+#pragma unroll
+                    for (int u = 0; u < VPT; ++u) {
+                        const int64_t at = (c0 + u * BS) * 16;
+                        v[u] = u32x4{0, 0, 0, 0};
+                        if (at < row_bytes)
+                            v[u] = load16_nt(static_cast<const uint8_t *>(a.rows) + row + at);
+                    }
+                    float dot = 0.0f;
+#pragma unroll
+                    for (int u = 0; u < VPT; ++u) {
+                        float x[N];
+                        RowType<T>::unpack(v[u], x);
+#pragma unroll
+                        for (int e = 0; e < N; ++e)
+                            dot = fmaf(x[e], f[u][e], dot);
+                    }
+                    dot = wave_sum(dot);
+                    if (lane == j)
+                        dots[wave][j] += dot;
+                }
+                if (a.grad_rows) {
+                    const float wj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), j));
+#pragma unroll
+                    for (int u = 0; u < VPT; ++u) {
+                        const int64_t at = (c0 + u * BS) * 16;
+                        if (at < row_bytes) {
+                            float y[N];
+#pragma unroll
+                            for (int e = 0; e < N; ++e)
+                                y[e] = wj * f[u][e];
+                            store16_nt(static_cast<uint8_t *>(a.grad_rows) + row + at, RowType<T>::pack(y));
+                        }
+                    }
+                }
+            }
+        }
+    }
+    if (a.grad_weights) {
+        __syncthreads();
+        if ((int)threadIdx.x < ns * k) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kWaves; ++v)
+                sum += dots[v][lane];
+            a.grad_weights[s0 * k + lane] = sum;
+        }
+        __syncthreads(); // before the next item clears the sums
+    }
+    }
+}
+
+// Slots of one workgroup: several where most slots hold no row (the receive
+// regions of many ranks), so that the launch is not mostly empty
+// workgroups; a wave's 64 lanes hold their places.
+inline int slots_per_group(int64_t nslots, int64_t nrows, int k)
+{
+    int g = 1;
+    while (g * 2 * k <= 64 && g * nrows < nslots)
+        g *= 2;
+    return g;
+}
+
+// Workgroups of a launch over `items`: one each, up to a number whose
+// threads a 32-bit grid still counts.
+inline dim3 grid_of(int64_t items)
+{
+    const int64_t cap = 1 << 22;
+    return dim3((unsigned)(items < cap ? items : cap));
+}
+
+} // namespace
+
+hipError_t launch_expert_sort(const moe_ep_sort_args &a, hipStream_t s)
+{
+    const int64_t nslots = (int64_t)a.ranks * a.slots, nvec = a.row_bytes / 16;
+    const int E = a.ranks * a.experts_per_rank;
+    if (sort_is_direct(a.ranks, a.slots, a.top_k, E)) {
+        const int nchunk = a.quantize ? 1 : (int)((nvec + kDirectBlock - 1) / kDirectBlock);
+        const dim3 grid((unsigned)(nslots * nchunk + 1));
+        if (!a.quantize)
+            hipLaunchKernelGGL((sort_direct_kernel<Bf16, false>), grid, dim3(kDirectBlock), 0, s, a, nchunk);
+        else if (a.row_type == MOE_EP_BF16_ROWS)
+            hipLaunchKernelGGL((sort_direct_kernel<Bf16, true>), grid, dim3(kDirectBlock), 0, s, a, nchunk);
+        else
+            hipLaunchKernelGGL((sort_direct_kernel<Fp32, true>), grid, dim3(kDirectBlock), 0, s, a, nchunk);
+        return hipGetLastError();
+    }
+    const int tiles = (int)sort_tiles(a.slots, a.top_k), epr = a.experts_per_rank;
+    int bits = 0;
+    while ((1 << bits) < epr)
+        ++bits;
+    if (a.slots) {
+        hipLaunchKernelGGL(sort_count_kernel, dim3(a.ranks * tiles), dim3(kTileBlock), epr * 4, s, a, tiles);
+        if (hipError_t e = hipGetLastError())
+            return e;
+    }
+    hipLaunchKernelGGL(sort_scan_kernel, dim3(1), dim3(kScanBlock), 0, s, a, tiles);
+    if (hipError_t e = hipGetLastError())
+        return e;
+    if (!a.slots)
+        return hipSuccess;
+    hipLaunchKernelGGL(sort_place_kernel, dim3(a.ranks * tiles), dim3(kTileBlock), (kTileBlock / 64) * epr * 4, s, a,
+                       tiles, bits);
+    if (hipError_t e = hipGetLastError())
+        return e;
+    if (!a.capacity)
+        return hipSuccess;
+    const int g = slots_per_group(nslots, a.capacity, a.top_k);
+    const uint32_t nchunk =
+        a.quantize ? 1 : (uint32_t)((nvec + kGatherBlock * kGatherVectors - 1) / (kGatherBlock * kGatherVectors));
+    const int64_t items = (nslots + g - 1) / g * nchunk;
+    if (items > INT32_MAX)
+        return hipErrorInvalidValue;
+    const dim3 grid = grid_of(items);
+    if (!a.quantize)
+        hipLaunchKernelGGL((sort_gather_kernel<Bf16, false>), grid, dim3(kGatherBlock), 0, s, a, g, nchunk, (uint32_t)items);
+    else if (a.row_type == MOE_EP_BF16_ROWS)
+        hipLaunchKernelGGL((sort_gather_kernel<Bf16, true>), grid, dim3(kGatherBlock), 0, s, a, g, nchunk, (uint32_t)items);
+    else
+        hipLaunchKernelGGL((sort_gather_kernel<Fp32, true>), grid, dim3(kGatherBlock), 0, s, a, g, nchunk, (uint32_t)items);
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_unsort(const moe_ep_unsort_args &a, hipStream_t s)
+{
+    const bool bf16 = a.row_type == MOE_EP_BF16_ROWS;
+    const int64_t nslots = (int64_t)a.ranks * a.slots, nvec = (int64_t)a.hidden_size * (bf16 ? 2 : 4) / 16;
+    const int g = slots_per_group(nslots, a.num_rows, a.top_k);
+    const uint32_t nchunk = (uint32_t)((nvec + kUnsortBlock - 1) / kUnsortBlock);
+    const int64_t items = (nslots + g - 1) / g * nchunk;
+    if (items > INT32_MAX)
+        return hipErrorInvalidValue;
+    const dim3 grid = grid_of(items), block(kUnsortBlock);
+    if (bf16 && a.weights)
+        hipLaunchKernelGGL((unsort_kernel<Bf16, true>), grid, block, 0, s, a, g, nchunk, (uint32_t)items);
+    else if (bf16)
+        hipLaunchKernelGGL((unsort_kernel<Bf16, false>), grid, block, 0, s, a, g, nchunk, (uint32_t)items);
+    else if (a.weights)
+        hipLaunchKernelGGL((unsort_kernel<Fp32, true>), grid, block, 0, s, a, g, nchunk, (uint32_t)items);
+    else
+        hipLaunchKernelGGL((unsort_kernel<Fp32, false>), grid, block, 0, s, a, g, nchunk, (uint32_t)items);
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_unsort_backward(const moe_ep_unsort_grad_args &a, hipStream_t s)
+{
+    const int64_t nslots = (int64_t)a.ranks * a.slots;
+    const int g = slots_per_group(nslots, a.num_rows, a.top_k);
+    const int64_t items = (nslots + g - 1) / g;
+    const dim3 grid = grid_of(items), block(kGradBlock);
+    if (a.row_type == MOE_EP_BF16_ROWS)
+        hipLaunchKernelGGL(unsort_grad_kernel<Bf16>, grid, block, 0, s, a, g, (uint32_t)items);
+    else
+        hipLaunchKernelGGL(unsort_grad_kernel<Fp32>, grid, block, 0, s, a, g, (uint32_t)items);
+    return hipGetLastError();
+}
+
+} // namespace moe_ep

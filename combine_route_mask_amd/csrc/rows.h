@@ -1,0 +1,143 @@
+// Row elements of the expert layer's kernels: 16-byte vectors of bf16 or
+// fp32 to floats and back, wave and workgroup reductions, and the int8 row
+// scale.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "formats.h"
+#include "memory_ops.h"
+
+namespace moe_ep {
+
+struct Bf16 {};
+struct Fp32 {};
+
+template <typename T>
+struct RowType;
+
+template <>
+struct RowType<Bf16> {
+    static constexpr int kPer = 8;   // elements of a 16-byte vector
+    static constexpr int kBytes = 2;
+    static __device__ __forceinline__ void unpack(u32x4 v, float *f)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            unpack_bf16x2(v[i], f[2 * i], f[2 * i + 1]);
+    }
+    static __device__ __forceinline__ u32x4 pack(const float *f)
+    {
+        u32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+        return v;
+    }
+};
+
+template <>
+struct RowType<Fp32> {
+    static constexpr int kPer = 4;
+    static constexpr int kBytes = 4;
+    static __device__ __forceinline__ void unpack(u32x4 v, float *f)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            f[i] = __uint_as_float(v[i]);
+    }
+    static __device__ __forceinline__ u32x4 pack(const float *f)
+    {
+        u32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = __float_as_uint(f[i]);
+        return v;
+    }
+};
+
+// N elements (a multiple of kPer) from / to a 16-byte aligned address.
+template <typename T, int N>
+__device__ __forceinline__ void load_elements(const uint8_t *p, float *f)
+{
+    u32x4 v[N / RowType<T>::kPer];
+#pragma unroll
+    for (int i = 0; i < N / RowType<T>::kPer; ++i)
+        v[i] = load16_nt(p + 16 * i);
+#pragma unroll
+    for (int i = 0; i < N / RowType<T>::kPer; ++i)
+        RowType<T>::unpack(v[i], f + i * RowType<T>::kPer);
+}
+
+__device__ __forceinline__ void store16_nt(void *p, u32x4 v)
+{
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(p));
+}
+
+__device__ __forceinline__ float wave_sum(float x)
+{
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1)
+        x += __shfl_xor(x, m);
+    return x;
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t x)
+{
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const uint32_t y = (uint32_t)__shfl_xor((int)x, m);
+        x = x > y ? x : y;
+    }
+    return x;
+}
+
+// Magnitude of x as an ordered integer: infinities and NaN are the largest.
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+constexpr uint32_t kInfinity = 0x7F800000u;
+
+// The int8 rule of a row whose largest magnitude is `top`: scale = top / 127,
+// code = round(x / scale) to nearest even.  The code is taken as
+// round(x * (127 / top)), two roundings of 2^-24 away from x / scale, so it
+// differs only within 127 * 2^-22 of a tie.  A tiny row is brought up by a
+// power of two first, so that 127 / top stays finite.
+struct Int8Row {
+    float scale, up, inv;
+    __device__ __forceinline__ explicit Int8Row(uint32_t top)
+    {
+        if (top >= kInfinity) {
+            scale = __uint_as_float(0x7FC00000u);
+            up = inv = 0.0f;
+        } else if (top == 0) {
+            scale = up = inv = 0.0f;
+        } else {
+            const float t = __uint_as_float(top);
+            scale = t / 127.0f;
+            up = t < 0x1p-100f ? 0x1p+64f : 1.0f;
+            inv = 127.0f / (t * up);
+        }
+    }
+    // NaN * 0 and infinity * 0 convert to 0.
+    __device__ __forceinline__ int code(float x) const
+    {
+        const float c = rintf((x * up) * inv);
+        return c == c ? (int)c : 0;
+    }
+    __device__ __forceinline__ uint32_t codes4(const float *f) const
+    {
+        return (uint32_t)(code(f[0]) & 0xFF) | ((uint32_t)(code(f[1]) & 0xFF) << 8) |
+               ((uint32_t)(code(f[2]) & 0xFF) << 16) | ((uint32_t)(code(f[3]) & 0xFF) << 24);
+    }
+    __device__ __forceinline__ u32x4 codes16(const float *f) const
+    {
+        u32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = codes4(f + 4 * i);
+        return v;
+    }
+};
+
+} // namespace moe_ep

@@ -38,7 +38,9 @@ _COMBINE_NAMES = {"bf16": COMBINE_BF16, "fp8": COMBINE_FP8}
 # Every symbol include/moe_ep.h declares.
 EXPORTS = ("moe_ep_is_supported", "moe_ep_workspace_bytes", "moe_ep_create", "moe_ep_dispatch",
            "moe_ep_combine", "moe_ep_combine_noalloc", "moe_ep_destroy", "moe_ep_allgatherv",
-           "moe_ep_reduce_scatterv", "moe_ep_last_error")
+           "moe_ep_reduce_scatterv", "moe_ep_expert_sort_workspace_bytes", "moe_ep_expert_sort",
+           "moe_ep_expert_unsort", "moe_ep_expert_unsort_backward", "moe_ep_expert_matmul",
+           "moe_ep_silu_mul_quantize", "moe_ep_add_rms_norm", "moe_ep_last_error")
 STATIC_SCRATCH_BYTES = 64 << 20  # MOE_EP_STATIC_SCRATCH_BYTES
 
 
@@ -102,6 +104,13 @@ def _load(path: str = LIB_PATH):
     L.moe_ep_allgatherv.restype = C.c_int
     L.moe_ep_reduce_scatterv.argtypes = [i32, C.POINTER(i32), i32, vp, i64, vp, i64, vp]
     L.moe_ep_reduce_scatterv.restype = C.c_int
+    L.moe_ep_expert_sort_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.moe_ep_expert_sort_workspace_bytes.restype = i64
+    # the expert layer's calls take one packed argument block each (experts.py)
+    for name in ("moe_ep_expert_sort", "moe_ep_expert_unsort", "moe_ep_expert_unsort_backward",
+                 "moe_ep_expert_matmul", "moe_ep_silu_mul_quantize", "moe_ep_add_rms_norm"):
+        getattr(L, name).argtypes = [C.c_char_p, vp]
+        getattr(L, name).restype = C.c_int
     L.moe_ep_last_error.argtypes = []
     L.moe_ep_last_error.restype = C.c_char_p
     return L
@@ -261,6 +270,7 @@ class MoeEpExchange:
                                      device=device)
         self.handle = moe_ep_create(self.params, self.workspace.data_ptr(), self.size_per_rank)
         self.views: Optional[DispatchViews] = None
+        self.most_pairs = 0  # expert rows of the last dispatch, at most
 
     @property
     def P(self):
@@ -339,6 +349,8 @@ class MoeEpExchange:
                             T, stream, active_rank_mask, extra_payload, eplb_local_stats)
         self.views = v
         k = self.params.top_k
+        self.most_pairs = k * sum(int(n) for r, n in enumerate(num_tokens)
+                                  if active_rank_mask is None or (int(active_rank_mask) >> r) & 1)
         out = {
             "tokens_per_rank": v.tokens_per_rank,
             "payload": self._plane(v.payload_offset, v.payload_row_bytes, T),
@@ -361,6 +373,26 @@ class MoeEpExchange:
             out["eplb_gathered_stats"] = base.as_strided((P, P * n * 4), (self.size_per_rank, 1),
                                                          v.eplb_offset).view(torch.int32).view(P, P, n)
         return out
+
+    def expert_sort(self, recv, quantize: bool = False, capacity: Optional[int] = None, out=None,
+                    out_scales=None, stream=None):
+        """The received rows of the last dispatch (``recv``, its result) in
+        expert order, all ranks' experts after one another: see
+        ``experts.expert_sort``.  The capacity defaults to the step's tokens
+        times top_k, which holds every pair.  ``quantize`` (BF16 payloads)
+        makes int8 rows with one scale each."""
+        import torch
+        from . import experts
+        _need(self.views is not None, "expert_sort before any dispatch")
+        rows = recv["payload"]
+        if self.params.dispatch_format == FMT_BF16:
+            rows = rows.view(torch.bfloat16)
+        else:
+            _need(not quantize, "quantize needs a BF16 payload")
+        return experts.expert_sort(recv["ids"], rows, self.params.num_experts // self.P,
+                                   scales=recv["scales"],
+                                   capacity=self.most_pairs if capacity is None else capacity,
+                                   quantize=quantize, out=out, out_scales=out_scales, stream=stream)
 
     def combine_landing(self):
         """FP8 combine landing planes of the last step: codes

@@ -275,6 +275,222 @@ int moe_ep_reduce_scatterv(int32_t ep_size, const int32_t *sizes, int32_t hidden
                            const void *in, int64_t in_rank_stride, void *out,
                            int64_t out_rank_stride, void *stream);
 
+/* ---------------------------------------------------------------------
+ * The expert layer between a dispatch and its combine, and the norm that
+ * makes the next layer's payload.  These calls need no handle and keep no
+ * state: the caller owns every buffer, launches go to the caller's stream
+ * without host synchronisation, nothing is allocated, and a call may be
+ * captured into a HIP graph.  Buffers belong to the current HIP device.
+ * Calls whose output, workspace or index buffers overlap must be ordered by
+ * the caller; calls on buffers of their own may run at the same time.
+ * Every call takes one argument block, all pointers device pointers.
+ * --------------------------------------------------------------------- */
+
+#define MOE_EP_BF16_ROWS 0 /* element types of the expert layer's rows   */
+#define MOE_EP_FP32_ROWS 1
+
+#define MOE_EP_MAX_SORT_EXPERTS 4096 /* ranks * experts_per_rank          */
+
+/*
+ * Expert sort: rows to expert order.  Slot q of rank r holds one row and
+ * top_k global expert ids (the planes that a dispatch leaves in rank r's
+ * region; with ranks = 1 simply a batch of tokens).  A pair (r, q, j) counts
+ * when its id lies on its rank: r*e <= id < (r+1)*e, e = experts_per_rank;
+ * other ids (other ranks' experts, the invalid id, anything out of range)
+ * are passed over.  Counted pairs are placed by ascending (id, q, j): the
+ * order depends on the ids alone.
+ *  position  [R][S][k]: a pair's place, -1 where it has none
+ *  counts    [R*e]: pairs of each expert
+ *  offsets   [R*e + 1]: exclusive prefix of counts, clamped to capacity;
+ *            expert x's rows are offsets[x] .. offsets[x+1] - 1
+ *  out_rows, out_scales: row position[r][q][j] is a copy of the row and
+ *            scale row of (r, q); rows from offsets[R*e] on are left alone.
+ * Pairs from place `capacity` on are dropped (position -1, not in offsets;
+ * counts still holds them), so no row is written past the capacity.
+ * capacity >= sum over ranks of num_tokens * k never drops one after a
+ * dispatch.  An id that a row carries twice gives two pairs.
+ * quantize = 1: rows are row_type elements, row_bytes of them, and out_rows
+ * holds int8 codes with out_scales one fp32 scale a row: scale = amax / 127,
+ * code = row / scale rounded to nearest even (scale 0 and codes 0 for a row
+ * of zeros; scale NaN and codes 0 for a row with a NaN or an infinity).
+ * row_bytes: a multiple of 16 up to 2^24, with quantize also of 16 elements;
+ * scale_row_bytes: any size up to 2^24.  workspace: moe_ep_expert_sort_workspace_bytes(),
+ * 16-byte aligned, for this call alone.
+ * Limits: ranks 1..64, slots >= 0, top_k 1..64, ranks*experts_per_rank in
+ * 1..4096, ranks*slots*top_k and capacity below 2^31.
+ */
+typedef struct moe_ep_sort_args {
+    const int32_t *ids;          /* [R][S][k]                                */
+    int64_t ids_rank_stride;     /* bytes from rank to rank                  */
+    const void *rows;            /* [R][S][row_bytes]                        */
+    int64_t rows_rank_stride;
+    int64_t row_bytes;
+    const void *scales;          /* [R][S][scale_row_bytes] or NULL          */
+    int64_t scales_rank_stride;
+    int64_t scale_row_bytes;
+    void *out_rows;              /* [capacity][row_bytes], int8 [capacity][H] */
+    void *out_scales;            /* [capacity][scale_row_bytes], fp32 [capacity] */
+    int32_t *position;
+    int32_t *offsets;
+    int32_t *counts;
+    void *workspace;
+    int64_t workspace_bytes;
+    int64_t capacity;
+    int32_t ranks;
+    int32_t slots;
+    int32_t top_k;
+    int32_t experts_per_rank;
+    int32_t quantize;            /* 0: copy, 1: int8 codes and scales        */
+    int32_t row_type;            /* MOE_EP_*_ROWS, read when quantize = 1    */
+} moe_ep_sort_args;
+
+/* Bytes of workspace an expert sort of this shape needs (0: none; -1: bad
+ * shape, see moe_ep_last_error).  Host-only. */
+int64_t moe_ep_expert_sort_workspace_bytes(int32_t ranks, int32_t slots, int32_t top_k,
+                                           int32_t experts_per_rank);
+
+int moe_ep_expert_sort(const moe_ep_sort_args *args, void *stream);
+
+/*
+ * Expert unsort: out[r][q] = sum over j of weights[r][q][j] *
+ * rows[position[r][q][j]] (weights NULL: 1), fp32 from +0 in ascending j,
+ * rounded once to row_type.  Pairs with a position outside [0, num_rows)
+ * add nothing; a slot without any is filled with zeros (keep_empty = 0) or
+ * left alone (keep_empty = 1: what a combine never reads).  With weights
+ * NULL it is the gradient of the expert sort.  hidden_size elements a row, a
+ * multiple of 16 bytes up to 2^24; `out` may not overlap `rows`.
+ */
+typedef struct moe_ep_unsort_args {
+    const int32_t *position;     /* [R][S][k], contiguous                    */
+    const void *rows;            /* [num_rows][H]                            */
+    const float *weights;        /* [R][S][k] or NULL                        */
+    int64_t weights_rank_stride; /* bytes                                    */
+    void *out;                   /* [R][S][H]                                */
+    int64_t out_rank_stride;     /* bytes                                    */
+    int64_t num_rows;
+    int32_t ranks;
+    int32_t slots;
+    int32_t top_k;
+    int32_t hidden_size;
+    int32_t row_type;
+    int32_t keep_empty;
+} moe_ep_unsort_args;
+
+int moe_ep_expert_unsort(const moe_ep_unsort_args *args, void *stream);
+
+/*
+ * Gradient of the expert unsort, for grad_out [R][S][H]:
+ *  grad_rows[position[r][q][j]] = weights[r][q][j] * grad_out[r][q],
+ *            rounded once (rows that no pair names are left alone); or NULL
+ *  grad_weights[r][q][j] = sum over h of rows[position[r][q][j]][h] *
+ *            grad_out[r][q][h] in fp32, in an order that the shape alone
+ *            fixes, 0 for a pair without a row; or NULL
+ * A place may appear in `position` once, as the sort makes it.
+ */
+typedef struct moe_ep_unsort_grad_args {
+    const int32_t *position;     /* [R][S][k], contiguous                    */
+    const void *grad_out;        /* [R][S][H]                                */
+    int64_t grad_out_rank_stride;
+    const void *rows;            /* [num_rows][H], needed for grad_weights   */
+    const float *weights;        /* [R][S][k] or NULL                        */
+    int64_t weights_rank_stride;
+    void *grad_rows;             /* [num_rows][H] or NULL                    */
+    float *grad_weights;         /* [R][S][k], contiguous, or NULL           */
+    int64_t num_rows;
+    int32_t ranks;
+    int32_t slots;
+    int32_t top_k;
+    int32_t hidden_size;
+    int32_t row_type;
+    int32_t reserved;            /* 0                                        */
+} moe_ep_unsort_grad_args;
+
+int moe_ep_expert_unsort_backward(const moe_ep_unsort_grad_args *args, void *stream);
+
+/*
+ * Product of int8 rows with each expert's int8 weights:
+ *  out[m][n] = x_scales[m] * w_scales[e][n] * sum over k of x[m][k] * w[e][n][k]
+ * for the rows offsets[e] <= m < offsets[e+1] of every expert e, the sum
+ * exact in int32, the scaling in fp32, one rounding to out_type.  offsets
+ * [E + 1] ascends and is read on the device, each entry taken as at most
+ * num_rows; rows outside every expert's range are left alone.  offsets NULL:
+ * a dense product, num_experts = 1 and every row.  k a multiple of 16 and at
+ * most 131056 (|sum| < 2^31 also at -128 * -128); n >= 1; x and w 16-byte
+ * aligned and contiguous.
+ */
+typedef struct moe_ep_matmul_args {
+    const int8_t *x;             /* [num_rows][k]                            */
+    const float *x_scales;       /* [num_rows]                               */
+    const int8_t *w;             /* [E][n][k]                                */
+    const float *w_scales;       /* [E][n]                                   */
+    const int32_t *offsets;      /* [E + 1] or NULL                          */
+    void *out;                   /* [num_rows][n]                            */
+    int64_t num_rows;
+    int32_t num_experts;
+    int32_t n;
+    int32_t k;
+    int32_t out_type;            /* MOE_EP_*_ROWS                            */
+} moe_ep_matmul_args;
+
+int moe_ep_expert_matmul(const moe_ep_matmul_args *args, void *stream);
+
+/*
+ * Gated activation between the two expert products: for the first
+ * min(*num_valid, num_rows) rows (num_valid NULL: all; offsets + E of the
+ * sort), a = silu(x[:, :I]) * x[:, I:] in fp32, as int8 codes and one scale
+ * a row (as the quantising sort's); other rows are left alone.  I a multiple
+ * of 16, at most 32768.
+ */
+typedef struct moe_ep_silu_args {
+    const void *x;               /* [num_rows][2 * I] row_type               */
+    const int32_t *num_valid;    /* one device int32, or NULL                */
+    int8_t *out;                 /* [num_rows][I]                            */
+    float *out_scales;           /* [num_rows]                               */
+    int64_t num_rows;
+    int32_t inter_size;          /* I                                        */
+    int32_t row_type;
+} moe_ep_silu_args;
+
+int moe_ep_silu_mul_quantize(const moe_ep_silu_args *args, void *stream);
+
+#define MOE_EP_NORM_INT8 0        /* int8 codes, one fp32 scale a row         */
+#define MOE_EP_NORM_MXFP8 1       /* the MXFP8 payload: e4m3, e8m0 a 32-block */
+#define MOE_EP_NORM_DEEPSEEK_FP8 2 /* the DeepSeekFp8 payload: e4m3, fp32 a 128-block */
+
+/*
+ * Root-mean-square norm with the residual's addition and an 8-bit output:
+ *  s = x + residual (residual NULL: x), residual_out = s rounded to row_type,
+ *  y = s / sqrt(mean(s^2) + eps) * weight, from the unrounded s, all in fp32,
+ *  out / scales = y in `format`:
+ *   INT8: scale = amax(y) / 127, as the quantising sort's rows
+ *   MXFP8: scale 2^(b - 127), the smallest power of two that keeps the
+ *    block's magnitudes within 448 (b = 0 for a block of zeros; the FP8
+ *    combine's rule: nothing saturates), code = y / scale to nearest even; a
+ *    block with a NaN or an infinity in y has b = 255 and codes 0x7F
+ *   DEEPSEEK_FP8: scale = amax / 448 (0 and codes 0 for a block of zeros;
+ *    NaN and codes 0x7F for one with a NaN or an infinity)
+ * A row in which s holds a NaN or an infinity, or whose sum of squares passes
+ * fp32, has y = NaN throughout; a row of zeros with eps = 0 too.
+ * H a multiple of 16 (INT8), 32, 128, at most 32768.  residual_out may be
+ * residual or x itself; NULL: not written.
+ */
+typedef struct moe_ep_norm_args {
+    const void *x;               /* [num_rows][H] row_type                   */
+    const void *residual;        /* [num_rows][H] row_type or NULL           */
+    const void *weight;          /* [H] row_type                             */
+    void *residual_out;          /* [num_rows][H] row_type or NULL           */
+    void *out;                   /* [num_rows][H] bytes                      */
+    void *scales;                /* fp32 [num_rows], [num_rows][H/32] bytes,
+                                    fp32 [num_rows][H/128]                   */
+    int64_t num_rows;
+    int32_t hidden_size;
+    int32_t row_type;
+    int32_t format;              /* MOE_EP_NORM_*                            */
+    float eps;                   /* >= 0                                     */
+} moe_ep_norm_args;
+
+int moe_ep_add_rms_norm(const moe_ep_norm_args *args, void *stream);
+
 /* Message of the calling thread's last failed call ("" if none). */
 const char *moe_ep_last_error(void);
 
