@@ -16,53 +16,90 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 struct Tile {
-    int expert;
+    int expert;          // -1: no such tile
     int64_t first, last; // rows of the tile: first <= m < last
+    int n;               // channel tile
 };
 
-// The tile number `index` of all experts' row tiles of BM rows, found by
-// each wave from the offsets; expert -1 when there are fewer tiles.
-template <int BM>
-__device__ __forceinline__ Tile find_tile(const moe_ep_matmul_args &a, int64_t index)
+__device__ __forceinline__ int prefix_sum(int x, int lane)
 {
-    Tile t = {-1, 0, 0};
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const int y = __shfl_up(x, m);
+        x += lane >= m ? y : 0;
+    }
+    return x;
+}
+
+// Rows [lo, hi) of expert e, within the num_rows there are.
+__device__ __forceinline__ void expert_rows(const moe_ep_matmul_args &a, int e, int &lo, int &hi)
+{
+    lo = hi = 0;
+    if (e < a.num_experts) {
+        lo = min(max(a.offsets[e], 0), (int)a.num_rows);
+        hi = min(max(a.offsets[e + 1], lo), (int)a.num_rows);
+    }
+}
+
+// The workgroup's tile: BM rows of one expert and one of its `ntiles`
+// channel tiles, found by each wave from the offsets (the host does not know
+// them).  Tiles are numbered by expert, channel tile, row tile, so that
+// neighbours share their weights, and each of the eight XCDs (workgroup
+// number modulo 8) takes a run of them, so that the sharing is in one L2.
+template <int BM>
+__device__ __forceinline__ Tile find_tile(const moe_ep_matmul_args &a, int ntiles)
+{
+    Tile t = {-1, 0, 0, 0};
+    const int lane = threadIdx.x & 63;
     if (!a.offsets) {
-        if (index * BM < a.num_rows) {
+        const int tiles = (int)((a.num_rows + BM - 1) / BM), total = tiles * ntiles, per = (total + 7) / 8;
+        const int at = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+        if ((int)(blockIdx.x >> 3) < per && at < total) {
             t.expert = 0;
-            t.first = index * BM;
+            t.n = at / tiles;
+            t.first = (int64_t)(at % tiles) * BM;
             t.last = min(a.num_rows, t.first + BM);
         }
         return t;
     }
-    const int lane = threadIdx.x & 63;
-    const int M = (int)a.num_rows;
-    int before = 0; // tiles of the experts so far
-    for (int e0 = 0; e0 < a.num_experts; e0 += 64) {
-        const int e = e0 + lane;
-        int lo = 0, hi = 0;
-        if (e < a.num_experts) {
-            lo = min(max(a.offsets[e], 0), M);
-            hi = min(max(a.offsets[e + 1], lo), M);
-        }
-        const int n = (hi - lo + BM - 1) / BM;
-        int sum = n;
-#pragma unroll
-        for (int m = 1; m < 64; m <<= 1) {
-            const int y = __shfl_up(sum, m);
-            sum += lane >= m ? y : 0;
-        }
-        const int start = before + sum - n;
-        const uint64_t hit = __ballot(index >= start && index < start + n);
-        if (hit) {
-            const int l = __builtin_ctzll(hit);
-            const int s = __builtin_amdgcn_readlane(start, l);
-            t.expert = e0 + l;
-            t.first = (int64_t)__builtin_amdgcn_readlane(lo, l) + (index - s) * BM;
-            t.last = min((int64_t)__builtin_amdgcn_readlane(hi, l), t.first + BM);
-            return t;
-        }
-        before += __builtin_amdgcn_readlane(sum, 63);
+    // lane l sums the experts l * share ..; then the lane that holds the
+    // tile is looked into, one expert a lane
+    const int share = (a.num_experts + 63) / 64;
+    int lo = 0, hi = 0, n = 0;
+    for (int i = 0; i < share; ++i) {
+        expert_rows(a, lane * share + i, lo, hi);
+        n += (hi - lo + BM - 1) / BM;
     }
+    int sum = prefix_sum(n, lane);
+    const int total = __builtin_amdgcn_readlane(sum, 63) * ntiles, per = (total + 7) / 8;
+    const int at = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || at >= total)
+        return t;
+    int start = (sum - n) * ntiles;
+    uint64_t hit = __ballot(at >= start && at < start + n * ntiles);
+    if (!hit) // offsets that do not ascend: no tile, and nothing out of range
+        return t;
+    int l = __builtin_ctzll(hit), base = 0;
+    if (share > 1) {
+        start = __builtin_amdgcn_readlane(start, l);
+        base = l * share;
+        lo = hi = 0;
+        if (lane < share)
+            expert_rows(a, base + lane, lo, hi);
+        n = (hi - lo + BM - 1) / BM;
+        start += (prefix_sum(n, lane) - n) * ntiles;
+        hit = __ballot(at >= start && at < start + n * ntiles);
+        if (!hit)
+            return t;
+        l = __builtin_ctzll(hit);
+    }
+    const int tiles = __builtin_amdgcn_readlane(n, l), here = at - __builtin_amdgcn_readlane(start, l);
+    t.n = here / tiles;
+    if (t.n >= ntiles)
+        return t;
+    t.expert = base + l;
+    t.first = (int64_t)__builtin_amdgcn_readlane(lo, l) + (int64_t)(here % tiles) * BM;
+    t.last = min((int64_t)__builtin_amdgcn_readlane(hi, l), t.first + BM);
     return t;
 }
 
@@ -73,6 +110,15 @@ inline int64_t most_tiles(const moe_ep_matmul_args &a, int64_t bm)
     const int64_t full = a.num_rows / bm;
     return a.offsets ? full + (a.num_rows < a.num_experts ? a.num_rows : a.num_experts)
                      : (a.num_rows + bm - 1) / bm;
+}
+
+// One workgroup a tile, in eight runs of the same length; false when there
+// are more than a grid of 32-bit thread numbers holds.
+inline bool tile_grid(int64_t tiles, int threads, dim3 &grid)
+{
+    tiles = (tiles + 7) / 8 * 8;
+    grid = dim3((unsigned)tiles);
+    return tiles * threads <= INT32_MAX;
 }
 
 // Four consecutive channels of token m, scaled and rounded.
@@ -123,14 +169,14 @@ constexpr int kSkinnyWaves = 4;
 // waves take a quarter of k each, straight from memory into the MFMA's
 // registers, and add their int32 sums in LDS.
 template <typename T, int NT, int MT>
-__global__ __launch_bounds__(kSkinnyWaves * 64) void matmul_skinny_kernel(moe_ep_matmul_args a, uint32_t ntiles)
+__global__ __launch_bounds__(kSkinnyWaves * 64) void matmul_skinny_kernel(moe_ep_matmul_args a, int ntiles)
 {
     constexpr int W = kSkinnyWaves, U = 4;
     __shared__ i32x4 part[W - 1][NT * MT][64];
-    const Tile t = find_tile<16 * MT>(a, blockIdx.x / ntiles);
+    const Tile t = find_tile<16 * MT>(a, ntiles);
     if (t.expert < 0)
         return;
-    const int n0 = (int)(blockIdx.x % ntiles) * 16 * NT;
+    const int n0 = t.n * 16 * NT;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, k16 = (lane >> 4) * 16;
     const int8_t *wp[NT], *xp[MT];
 #pragma unroll
@@ -202,14 +248,127 @@ __global__ __launch_bounds__(kSkinnyWaves * 64) void matmul_skinny_kernel(moe_ep
 template <int NT, int MT>
 hipError_t skinny_launch(const moe_ep_matmul_args &a, hipStream_t s)
 {
-    const int64_t ntiles = (a.n + 16 * NT - 1) / (16 * NT), items = most_tiles(a, 16 * MT) * ntiles;
-    if (items > (1 << 23))
+    const int64_t ntiles = (a.n + 16 * NT - 1) / (16 * NT);
+    dim3 grid;
+    if (!tile_grid(most_tiles(a, 16 * MT) * ntiles, kSkinnyWaves * 64, grid))
         return hipErrorInvalidValue;
-    const dim3 grid((unsigned)items), block(kSkinnyWaves * 64);
+    const dim3 block(kSkinnyWaves * 64);
     if (a.out_type == MOE_EP_BF16_ROWS)
-        hipLaunchKernelGGL((matmul_skinny_kernel<Bf16, NT, MT>), grid, block, 0, s, a, (uint32_t)ntiles);
+        hipLaunchKernelGGL((matmul_skinny_kernel<Bf16, NT, MT>), grid, block, 0, s, a, (int)ntiles);
     else
-        hipLaunchKernelGGL((matmul_skinny_kernel<Fp32, NT, MT>), grid, block, 0, s, a, (uint32_t)ntiles);
+        hipLaunchKernelGGL((matmul_skinny_kernel<Fp32, NT, MT>), grid, block, 0, s, a, (int)ntiles);
+    return hipGetLastError();
+}
+
+// Many rows an expert: the matrix cores bound the call.  A workgroup of four
+// waves takes 256 channels and 128 rows, 128 bytes of k at a time: the next
+// 48 KB travel to registers while the MFMAs work on the 48 KB in LDS.  A wave
+// holds 128 x 64 of the result (128 registers), so it reads 24 KB of LDS for
+// 64 MFMAs; two workgroups share a CU, and one multiplies while the other
+// turns its LDS over.
+//
+// LDS rows are 128 bytes, all on the same banks: chunk c of row r lies at
+// place c ^ (r & 7), so that 8 rows' reads of one chunk cover all banks.
+constexpr int kTileN = 256, kTileM = 128, kTileK = 128, kTileThreads = 256;
+
+template <typename T>
+__global__ __launch_bounds__(kTileThreads, 2) void matmul_tile_kernel(moe_ep_matmul_args a, int ntiles)
+{
+    constexpr int LN = kTileN / 32, LM = kTileM / 32; // 16-byte loads of a thread
+    constexpr int WN = 8, WM = 4;                     // 16 x 16 results of a wave
+    __shared__ __align__(16) uint8_t lds[(kTileN + kTileM) * kTileK];
+    const Tile t = find_tile<kTileM>(a, ntiles);
+    if (t.expert < 0)
+        return;
+    const int n0 = t.n * kTileN;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int chunk = tid & 7, row = tid >> 3;
+
+    // channels and rows past the last read the last's and are not stored
+    const int8_t *wp = a.w + ((int64_t)t.expert * a.n + n0) * a.k;
+    const int8_t *xp = a.x + t.first * a.k;
+    const int nlast = min(kTileN, a.n - n0) - 1, mlast = (int)(t.last - t.first) - 1;
+    uint32_t wo[LN], xo[LM];
+#pragma unroll
+    for (int i = 0; i < LN; ++i)
+        wo[i] = (uint32_t)min(row + 32 * i, nlast) * (uint32_t)a.k + chunk * 16;
+#pragma unroll
+    for (int i = 0; i < LM; ++i)
+        xo[i] = (uint32_t)min(row + 32 * i, mlast) * (uint32_t)a.k + chunk * 16;
+    uint8_t *put = lds + row * kTileK + ((chunk ^ (row & 7)) * 16);
+
+    i32x4 wv[LN], xv[LM];
+    auto load = [&](int k) {
+        const bool in = k + chunk * 16 < a.k; // zeros past the end add nothing
+#pragma unroll
+        for (int i = 0; i < LN; ++i) {
+            wv[i] = i32x4{0, 0, 0, 0};
+            if (in)
+                wv[i] = *reinterpret_cast<const i32x4 *>(wp + k + wo[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < LM; ++i) {
+            xv[i] = i32x4{0, 0, 0, 0};
+            if (in)
+                xv[i] = *reinterpret_cast<const i32x4 *>(xp + k + xo[i]);
+        }
+    };
+    const int wn = (wave & 1) * 128, wm = (wave >> 1) * 64, l16 = lane & 15, l4 = lane >> 4;
+    i32x4 acc[WN][WM] = {};
+    load(0);
+    for (int k = 0; k < a.k; k += kTileK) {
+        __syncthreads(); // the last step's reads are over
+#pragma unroll
+        for (int i = 0; i < LN; ++i)
+            *reinterpret_cast<i32x4 *>(put + i * 32 * kTileK) = wv[i];
+#pragma unroll
+        for (int i = 0; i < LM; ++i)
+            *reinterpret_cast<i32x4 *>(put + (kTileN + i * 32) * kTileK) = xv[i];
+        __syncthreads();
+        if (k + kTileK < a.k)
+            load(k + kTileK);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int at = ((h * 4 + l4) ^ (l16 & 7)) * 16 + l16 * kTileK;
+            i32x4 xf[WM];
+#pragma unroll
+            for (int j = 0; j < WM; ++j)
+                xf[j] = *reinterpret_cast<const i32x4 *>(lds + (kTileN + wm + 16 * j) * kTileK + at);
+#pragma unroll
+            for (int i = 0; i < WN; ++i) {
+                const i32x4 wf = *reinterpret_cast<const i32x4 *>(lds + (wn + 16 * i) * kTileK + at);
+#pragma unroll
+                for (int j = 0; j < WM; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf, xf[j], acc[i][j], 0, 0, 0);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < WM; ++j) {
+        const int64_t m = t.first + wm + 16 * j + l16;
+        if (m < t.last) {
+            const float sx = a.x_scales[m];
+#pragma unroll
+            for (int i = 0; i < WN; ++i) {
+                const int n = n0 + wn + 16 * i + l4 * 4;
+                float sw[4];
+                channel_scales(a, t.expert, n, sw);
+                store_channels<T>(a, m, n, acc[i][j], sx, sw);
+            }
+        }
+    }
+}
+
+hipError_t tile_launch(const moe_ep_matmul_args &a, hipStream_t s)
+{
+    const int64_t ntiles = (a.n + kTileN - 1) / kTileN;
+    dim3 grid;
+    if (!tile_grid(most_tiles(a, kTileM) * ntiles, kTileThreads, grid))
+        return hipErrorInvalidValue;
+    if (a.out_type == MOE_EP_BF16_ROWS)
+        hipLaunchKernelGGL((matmul_tile_kernel<Bf16>), grid, dim3(kTileThreads), 0, s, a, (int)ntiles);
+    else
+        hipLaunchKernelGGL((matmul_tile_kernel<Fp32>), grid, dim3(kTileThreads), 0, s, a, (int)ntiles);
     return hipGetLastError();
 }
 
@@ -217,7 +376,8 @@ hipError_t skinny_launch(const moe_ep_matmul_args &a, hipStream_t s)
 
 hipError_t launch_expert_matmul(const moe_ep_matmul_args &a, hipStream_t s)
 {
-    return skinny_launch<4, 2>(a, s);
+    const int64_t average = a.num_rows / a.num_experts;
+    return average >= 48 ? tile_launch(a, s) : skinny_launch<4, 2>(a, s);
 }
 
 } // namespace moe_ep

@@ -99,30 +99,30 @@ __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(
 constexpr uint32_t kInfinity = 0x7F800000u;
 
 // The int8 rule of a row whose largest magnitude is `top`: scale = top / 127,
-// code = round(x / scale) to nearest even.  The code is taken as
-// round(x * (127 / top)), two roundings of 2^-24 away from x / scale, so it
-// differs only within 127 * 2^-22 of a tie.  A tiny row is brought up by a
-// power of two first, so that 127 / top stays finite.
+// code = x / scale to nearest even, taken as the correctly rounded quotient
+// 127 x / top.  Ties are common (bf16 rows are ratios of 8-bit integers) and
+// this form keeps them exact, where a product with 127 / top would fall to
+// either side.  A huge row is brought down by a power of two first, so that
+// 127 x stays finite.
 struct Int8Row {
-    float scale, up, inv;
-    __device__ __forceinline__ explicit Int8Row(uint32_t top)
+    float scale, by, top;
+    __device__ __forceinline__ explicit Int8Row(uint32_t bits)
     {
-        if (top >= kInfinity) {
-            scale = __uint_as_float(0x7FC00000u);
-            up = inv = 0.0f;
-        } else if (top == 0) {
-            scale = up = inv = 0.0f;
+        top = __uint_as_float(bits);
+        if (bits == 0 || bits >= kInfinity) {
+            scale = bits ? __uint_as_float(0x7FC00000u) : 0.0f;
+            by = 0.0f;
+            top = 1.0f;
         } else {
-            const float t = __uint_as_float(top);
-            scale = t / 127.0f;
-            up = t < 0x1p-100f ? 0x1p+64f : 1.0f;
-            inv = 127.0f / (t * up);
+            scale = top / 127.0f;
+            by = top > 0x1p+100f ? 127.0f * 0x1p-20f : 127.0f;
+            top = top > 0x1p+100f ? top * 0x1p-20f : top;
         }
     }
     // NaN * 0 and infinity * 0 convert to 0.
     __device__ __forceinline__ int code(float x) const
     {
-        const float c = rintf((x * up) * inv);
+        const float c = rintf((x * by) / top);
         return c == c ? (int)c : 0;
     }
     __device__ __forceinline__ uint32_t codes4(const float *f) const
