@@ -34,6 +34,11 @@ __device__ __forceinline__ int prefix_sum(int x, int lane)
 // Rows [lo, hi) of expert e, within the num_rows there are.
 __device__ __forceinline__ void expert_rows(const moe_ep_matmul_args &a, int e, int &lo, int &hi)
 {
+    if (!a.offsets) {
+        lo = 0;
+        hi = e == 0 ? (int)a.num_rows : 0;
+        return;
+    }
     lo = hi = 0;
     if (e < a.num_experts) {
         lo = min(max(a.offsets[e], 0), (int)a.num_rows);
@@ -41,7 +46,7 @@ __device__ __forceinline__ void expert_rows(const moe_ep_matmul_args &a, int e, 
     }
 }
 
-// The workgroup's tile: BM rows of one expert and one of its `ntiles`
+// The workgroup's tile: up to BM rows of one expert and one of its `ntiles`
 // channel tiles, found by each wave from the offsets (the host does not know
 // them).  Tiles are numbered by expert, channel tile, row tile, so that
 // neighbours share their weights, and each of the eight XCDs (workgroup
@@ -50,18 +55,7 @@ template <int BM>
 __device__ __forceinline__ Tile find_tile(const moe_ep_matmul_args &a, int ntiles)
 {
     Tile t = {-1, 0, 0, 0};
-    const int lane = threadIdx.x & 63;
-    if (!a.offsets) {
-        const int tiles = (int)((a.num_rows + BM - 1) / BM), total = tiles * ntiles, per = (total + 7) / 8;
-        const int at = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-        if ((int)(blockIdx.x >> 3) < per && at < total) {
-            t.expert = 0;
-            t.n = at / tiles;
-            t.first = (int64_t)(at % tiles) * BM;
-            t.last = min(a.num_rows, t.first + BM);
-        }
-        return t;
-    }
+    const int lane = threadIdx.x & 63, slot = blockIdx.x >> 3;
     // lane l sums the experts l * share ..; then the lane that holds the
     // tile is looked into, one expert a lane
     const int share = (a.num_experts + 63) / 64;
@@ -70,10 +64,10 @@ __device__ __forceinline__ Tile find_tile(const moe_ep_matmul_args &a, int ntile
         expert_rows(a, lane * share + i, lo, hi);
         n += (hi - lo + BM - 1) / BM;
     }
-    int sum = prefix_sum(n, lane);
+    const int sum = prefix_sum(n, lane);
     const int total = __builtin_amdgcn_readlane(sum, 63) * ntiles, per = (total + 7) / 8;
-    const int at = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-    if ((int)(blockIdx.x >> 3) >= per || at >= total)
+    const int at = (int)(blockIdx.x & 7) * per + slot;
+    if (slot >= per || at >= total)
         return t;
     int start = (sum - n) * ntiles;
     uint64_t hit = __ballot(at >= start && at < start + n * ntiles);
@@ -121,263 +115,428 @@ inline bool tile_grid(int64_t tiles, int threads, dim3 &grid)
     return tiles * threads <= INT32_MAX;
 }
 
-// Four consecutive channels of token m, scaled and rounded.
 template <typename T>
-__device__ __forceinline__ void store_channels(const moe_ep_matmul_args &a, int64_t m, int n, const i32x4 &sum,
-                                               float sx, const float *sw)
+__device__ __forceinline__ void store_element(void *p, float y)
 {
-    float f[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        f[i] = (float)sum[i] * (sx * sw[i]);
-    const int64_t at = m * a.n + n;
-    if (RowType<T>::kBytes == 2) {
-        uint16_t *out = static_cast<uint16_t *>(a.out) + at;
-        if (n + 4 <= a.n && (a.n & 3) == 0 && ((uintptr_t)a.out & 7) == 0) {
-            *reinterpret_cast<u32x2 *>(out) = u32x2{pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3])};
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n + i < a.n)
-                out[i] = (uint16_t)f32_to_bf16_rne(f[i]);
-    } else {
-        float *out = static_cast<float *>(a.out) + at;
-        if (n + 4 <= a.n && (a.n & 3) == 0 && ((uintptr_t)a.out & 15) == 0) {
-            *reinterpret_cast<u32x4 *>(out) = RowType<Fp32>::pack(f);
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (n + i < a.n)
-                out[i] = f[i];
-    }
-}
-
-__device__ __forceinline__ void channel_scales(const moe_ep_matmul_args &a, int e, int n, float *sw)
-{
-    const float *s = a.w_scales + (int64_t)e * a.n;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        sw[i] = n + i < a.n ? s[n + i] : 0.0f;
+    if (RowType<T>::kBytes == 2)
+        *static_cast<uint16_t *>(p) = (uint16_t)f32_to_bf16_rne(y);
+    else
+        *static_cast<float *>(p) = y;
 }
 
 constexpr int kSkinnyWaves = 4;
 
-// Few rows an expert: the weights stream from HBM once and bound the call.
-// A workgroup takes 16 * NT channels of one expert and 16 * MT rows; its
-// waves take a quarter of k each, straight from memory into the MFMA's
-// registers, and add their int32 sums in LDS.
-template <typename T, int NT, int MT>
+// One row tile and few channels: a workgroup takes 16 channels of one expert
+// and 16 rows; each of its waves takes a quarter of k, straight from memory
+// into the MFMA's registers, four steps of 64 bytes in flight, and the int32
+// sums meet in LDS.
+template <typename T>
 __global__ __launch_bounds__(kSkinnyWaves * 64) void matmul_skinny_kernel(moe_ep_matmul_args a, int ntiles)
 {
     constexpr int W = kSkinnyWaves, U = 4;
-    __shared__ i32x4 part[W - 1][NT * MT][64];
-    const Tile t = find_tile<16 * MT>(a, ntiles);
+    __shared__ i32x4 part[W - 1][64];
+    const Tile t = find_tile<16>(a, ntiles);
     if (t.expert < 0)
         return;
-    const int n0 = t.n * 16 * NT;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, k16 = (lane >> 4) * 16;
-    const int8_t *wp[NT], *xp[MT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) // channels past the last read the last's weights and are not stored
-        wp[i] = a.w + ((int64_t)t.expert * a.n + min(n0 + 16 * i + l16, a.n - 1)) * a.k + k16;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-        xp[i] = a.x + min(t.first + 16 * i + l16, t.last - 1) * a.k + k16;
-    i32x4 acc[NT][MT] = {};
+    // channels and rows past the last read the last's and are not stored
+    const int8_t *wp = a.w + ((int64_t)t.expert * a.n + min(t.n * 16 + l16, a.n - 1)) * a.k + k16;
+    const int8_t *xp = a.x + min(t.first + l16, t.last - 1) * a.k + k16;
+    i32x4 acc = {0, 0, 0, 0};
     const int steps = (a.k + 63) / 64, share = (steps + W - 1) / W;
     const int lo = wave * share, hi = min(steps, lo + share);
     for (int s0 = lo; s0 < hi; s0 += U) {
-        i32x4 wv[U][NT], xv[U][MT];
+        i32x4 wv[U], xv[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int k = (s0 + u) * 64;
-            const bool in = s0 + u < hi && k + k16 < a.k; // zeros past the end add nothing
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                wv[u][i] = i32x4{0, 0, 0, 0};
-                if (in)
-                    wv[u][i] = __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(wp[i] + k));
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                xv[u][i] = i32x4{0, 0, 0, 0};
-                if (in)
-                    xv[u][i] = *reinterpret_cast<const i32x4 *>(xp[i] + k);
+            wv[u] = xv[u] = i32x4{0, 0, 0, 0};
+            if (s0 + u < hi && k + k16 < a.k) { // zeros past the end add nothing
+                wv[u] = __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(wp + k));
+                xv[u] = *reinterpret_cast<const i32x4 *>(xp + k);
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int j = 0; j < MT; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u][i], xv[u][j], acc[i][j], 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u], xv[u], acc, 0, 0, 0);
     }
-    if (wave) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < MT; ++j)
-                part[wave - 1][i * MT + j][lane] = acc[i][j];
-    }
-    __syncthreads();
     if (wave)
+        part[wave - 1][lane] = acc;
+    __syncthreads();
+    const int64_t m = t.first + l16;
+    if (wave || m >= t.last)
         return;
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-        const int64_t m = t.first + 16 * j + l16;
-        const bool stored = m < t.last;
-        const float sx = stored ? a.x_scales[m] : 0.0f;
+    for (int w = 0; w < W - 1; ++w)
+        acc += part[w][lane];
+    const float *scales = a.w_scales + (int64_t)t.expert * a.n;
+    const float sx = a.x_scales[m];
+    const int n = t.n * 16 + (lane >> 4) * 4;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const int n = n0 + 16 * i + (lane >> 4) * 4;
-            float sw[4];
-            channel_scales(a, t.expert, n, sw);
-            i32x4 sum = acc[i][j];
-#pragma unroll
-            for (int w = 0; w < W - 1; ++w)
-                sum += part[w][i * MT + j][lane];
-            if (stored)
-                store_channels<T>(a, m, n, sum, sx, sw);
-        }
-    }
+    for (int e = 0; e < 4; ++e)
+        if (n + e < a.n)
+            store_element<T>(static_cast<uint8_t *>(a.out) + (m * a.n + n + e) * RowType<T>::kBytes,
+                             (float)acc[e] * (sx * scales[n + e]));
 }
 
-template <int NT, int MT>
 hipError_t skinny_launch(const moe_ep_matmul_args &a, hipStream_t s)
 {
-    const int64_t ntiles = (a.n + 16 * NT - 1) / (16 * NT);
+    const int64_t ntiles = (a.n + 15) / 16;
     dim3 grid;
-    if (!tile_grid(most_tiles(a, 16 * MT) * ntiles, kSkinnyWaves * 64, grid))
+    if (!tile_grid(most_tiles(a, 16) * ntiles, kSkinnyWaves * 64, grid))
         return hipErrorInvalidValue;
     const dim3 block(kSkinnyWaves * 64);
     if (a.out_type == MOE_EP_BF16_ROWS)
-        hipLaunchKernelGGL((matmul_skinny_kernel<Bf16, NT, MT>), grid, block, 0, s, a, (int)ntiles);
+        hipLaunchKernelGGL(matmul_skinny_kernel<Bf16>, grid, block, 0, s, a, (int)ntiles);
     else
-        hipLaunchKernelGGL((matmul_skinny_kernel<Fp32, NT, MT>), grid, block, 0, s, a, (int)ntiles);
+        hipLaunchKernelGGL(matmul_skinny_kernel<Fp32>, grid, block, 0, s, a, (int)ntiles);
     return hipGetLastError();
 }
 
-// Many rows an expert: the matrix cores bound the call.  A workgroup of four
-// waves takes 256 channels and 128 rows, 128 bytes of k at a time: the next
-// 48 KB travel to registers while the MFMAs work on the 48 KB in LDS.  A wave
-// holds 128 x 64 of the result (128 registers), so it reads 24 KB of LDS for
-// 64 MFMAs; two workgroups share a CU, and one multiplies while the other
-// turns its LDS over.
-//
-// LDS rows are 128 bytes, all on the same banks: chunk c of row r lies at
-// place c ^ (r & 7), so that 8 rows' reads of one chunk cover all banks.
-constexpr int kTileN = 256, kTileM = 128, kTileK = 128, kTileThreads = 256;
+// Many rows an expert: the matrix cores bound the call.  A workgroup takes
+// BN channels and BM rows, 128 bytes of k at a time, through STAGES of LDS:
+// the next stages' rows go from memory straight into LDS while this one's
+// are multiplied.  NW x MW waves, each FN x FM results of 16 x 16.
+constexpr int kTileK = 128;
 
-template <typename T>
-__global__ __launch_bounds__(kTileThreads, 2) void matmul_tile_kernel(moe_ep_matmul_args a, int ntiles)
+template <int NW_, int MW_, int FN_, int FM_, int STAGES_>
+struct TileShape {
+    static constexpr int NW = NW_, MW = MW_, FN = FN_, FM = FM_, STAGES = STAGES_, W = NW * MW;
+    static constexpr int BN = NW * FN * 16, BM = MW * FM * 16, THREADS = 64 * W;
+    static constexpr int LN = BN / (8 * W), LM = BM / (8 * W); // loads of a thread and stage; a wave's covers 8 rows
+    static constexpr int BYTES = (BN + BM) * kTileK;
+};
+
+// 16 bytes a lane from base + offset + k into LDS: lane l's to `to` + 16 l.
+// (The buffer form: a global load into LDS makes every later LDS wait wait
+// for all reads.)
+__device__ __forceinline__ void load_lds(const int8_t *base, uint32_t offset, int k, uint8_t *to)
 {
-    constexpr int LN = kTileN / 32, LM = kTileM / 32; // 16-byte loads of a thread
-    constexpr int WN = 8, WM = 4;                     // 16 x 16 results of a wave
-    __shared__ __align__(16) uint8_t lds[(kTileN + kTileM) * kTileK];
-    const Tile t = find_tile<kTileM>(a, ntiles);
-    if (t.expert < 0)
-        return;
-    const int n0 = t.n * kTileN;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int chunk = tid & 7, row = tid >> 3;
+#if defined(__HIP_DEVICE_COMPILE__) // the host compiler does not know the resource type
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(base), 0, 0x7FFFFFFF, 0x00027000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void *)to, 16, offset, k, 0, 0);
+#endif
+}
 
-    // channels and rows past the last read the last's and are not stored
-    const int8_t *wp = a.w + ((int64_t)t.expert * a.n + n0) * a.k;
-    const int8_t *xp = a.x + t.first * a.k;
-    const int nlast = min(kTileN, a.n - n0) - 1, mlast = (int)(t.last - t.first) - 1;
-    uint32_t wo[LN], xo[LM];
-#pragma unroll
-    for (int i = 0; i < LN; ++i)
-        wo[i] = (uint32_t)min(row + 32 * i, nlast) * (uint32_t)a.k + chunk * 16;
-#pragma unroll
-    for (int i = 0; i < LM; ++i)
-        xo[i] = (uint32_t)min(row + 32 * i, mlast) * (uint32_t)a.k + chunk * 16;
-    uint8_t *put = lds + row * kTileK + ((chunk ^ (row & 7)) * 16);
+// Waits until at most N of the wave's loads are on their way and all its LDS
+// reads are back, then for the other waves.
+template <int N>
+__device__ __forceinline__ void wait_barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
 
-    i32x4 wv[LN], xv[LM];
-    auto load = [&](int k) {
-        const bool in = k + chunk * 16 < a.k; // zeros past the end add nothing
+// A workgroup's operands: where a thread's rows start, and where the wave's
+// first fragments lie in a stage.
+template <typename S>
+struct Operands {
+    const int8_t *wp, *xp;
+    uint32_t wo[S::LN], xo[S::LM];
+    int wave;
+    uint32_t wat[2], xat[2];
+};
+
+template <typename S>
+struct Fragments {
+    i32x4 x[2][S::FM], w[2 * S::FN];
+};
+
+template <typename S>
+__device__ __forceinline__ void read_x(const uint8_t *stage, const Operands<S> &o, Fragments<S> &f, int h, int j)
+{
+    f.x[h][j] = *reinterpret_cast<const i32x4 *>(stage + o.xat[h] + 16 * j * kTileK);
+}
+
+template <typename S>
+__device__ __forceinline__ void read_w(const uint8_t *stage, const Operands<S> &o, Fragments<S> &f, int i)
+{
+    f.w[i] = *reinterpret_cast<const i32x4 *>(stage + o.wat[i / S::FN] + 16 * (i % S::FN) * kTileK);
+}
+
+template <typename S>
+__device__ __forceinline__ void load_part(uint8_t *stage, const Operands<S> &o, int i, int k)
+{
+    if (i < S::LN)
+        load_lds(o.wp, o.wo[i], k, stage + (i * S::W + o.wave) * 1024);
+    else
+        load_lds(o.xp, o.xo[i - S::LN], k, stage + S::BN * kTileK + ((i - S::LN) * S::W + o.wave) * 1024);
+}
+
+constexpr int kAhead = 2; // weight fragments are read this many products before they are used
+
+// The products of stage `cur`, groups of FM.  The first kAhead fragments are
+// in registers already; the last groups run behind the barrier and read the
+// first of `next`, so that neither LDS nor the barrier leaves the matrix
+// cores idle for long.  `fill` (the stage read last, or `next` where there
+// are two) takes the loads for STAGES - 1 steps on.  The stages are distinct
+// objects to the compiler, so that a read of one does not wait for loads into
+// another; wait_barrier() does, for those that have to have arrived.
+template <typename S, typename ACC>
+__device__ __forceinline__ void tile_step(const uint8_t *__restrict__ cur, const uint8_t *__restrict__ next,
+                                          uint8_t *__restrict__ fill, int k, const Operands<S> &o, Fragments<S> &f,
+                                          ACC &acc, Fragments<S> &g)
+{
+    constexpr int G = 2 * S::FN, L = S::LN + S::LM, PER = (2 * L + G - 1) / G, FIRST = S::FN - S::FM - kAhead + 1;
 #pragma unroll
-        for (int i = 0; i < LN; ++i) {
-            wv[i] = i32x4{0, 0, 0, 0};
-            if (in)
-                wv[i] = *reinterpret_cast<const i32x4 *>(wp + k + wo[i]);
+    for (int i = 0; i < G; ++i) {
+#pragma unroll
+        for (int u = PER * i; u < PER * i + PER; ++u)
+            if (u < L)
+                load_part<S>(fill, o, u, k);
+        if (i + kAhead < G)
+            read_w<S>(cur, o, f, i + kAhead);
+#pragma unroll
+        for (int j = 0; j < S::FM; ++j) // the second half's rows, spread before its first product
+            if (i == (FIRST + j > 0 ? FIRST + j : 0))
+                read_x<S>(cur, o, f, 1, j);
+        if (i == G - kAhead)
+            wait_barrier<(S::STAGES - 2) * L>(); // this stage is read, the next one has arrived
+        __builtin_amdgcn_sched_barrier(0);
+        if (i >= G - kAhead) {
+            read_w<S>(next, o, g, i - (G - kAhead));
+#pragma unroll
+            for (int j = 0; j < S::FM; ++j)
+                if (j % kAhead == i - (G - kAhead))
+                    read_x<S>(next, o, g, 0, j);
         }
 #pragma unroll
-        for (int i = 0; i < LM; ++i) {
-            xv[i] = i32x4{0, 0, 0, 0};
-            if (in)
-                xv[i] = *reinterpret_cast<const i32x4 *>(xp + k + xo[i]);
+        for (int j = 0; j < S::FM; ++j)
+            acc[i % S::FN][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w[i], f.x[i / S::FN][j], acc[i % S::FN][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    // the fragments read ahead
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        f.w[i] = g.w[i];
+#pragma unroll
+    for (int j = 0; j < S::FM; ++j)
+        f.x[0][j] = g.x[0][j];
+}
+
+template <typename T, typename S>
+__device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const Tile &t, uint8_t *lds)
+{
+    constexpr int FN = S::FN, FM = S::FM;
+    const int n0 = t.n * S::BN;
+    const int lane = threadIdx.x & 63, l16 = lane & 15, l4 = lane >> 4;
+    Operands<S> o;
+    o.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    o.wp = a.w + ((int64_t)t.expert * a.n + n0) * a.k;
+    o.xp = a.x + t.first * a.k;
+    // LDS rows are 128 bytes, all on the same banks: chunk c of row r lies at
+    // place c ^ (r & 7), so that 8 rows' reads of one chunk cover all banks.
+    // Within a wave's 16 FN channels LDS row 16 i + r holds channel
+    // 4 FN (r / 4) + 4 i + r % 4: a lane's results then are 4 FN channels in
+    // a row.  Channels and rows past the last read the last's and are not
+    // stored.
+    const int sub = lane / 8;
+    const uint32_t chunk = (uint32_t)((lane % 8) ^ sub) * 16;
+    const int nlast = min(S::BN, a.n - n0) - 1, mlast = (int)(t.last - t.first) - 1;
+#pragma unroll
+    for (int i = 0; i < S::LN; ++i) {
+        const int row = (i * S::W + o.wave) * 8 + sub, r = row & 15;
+        const int n = row / (16 * FN) * (16 * FN) + 4 * FN * (r >> 2) + 4 * (row / 16 % FN) + (r & 3);
+        o.wo[i] = (uint32_t)min(n, nlast) * (uint32_t)a.k + chunk;
+    }
+#pragma unroll
+    for (int i = 0; i < S::LM; ++i)
+        o.xo[i] = (uint32_t)min((i * S::W + o.wave) * 8 + sub, mlast) * (uint32_t)a.k + chunk;
+    const int wn = (o.wave % S::NW) * FN * 16, wm = (o.wave / S::NW) * FM * 16;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t place = (uint32_t)(((h * 4 + l4) ^ (l16 & 7)) * 16 + l16 * kTileK);
+        o.wat[h] = place + wn * kTileK;
+        o.xat[h] = place + (S::BN + wm) * kTileK;
+    }
+    i32x4 acc[FN][FM] = {};
+    Fragments<S> f, g;
+    const int whole = a.k / kTileK;
+    uint8_t *cur = lds;
+    if (whole) {
+        // k starts elsewhere in each channel tile and goes round: rows a
+        // power of two apart would otherwise have all workgroups read the
+        // same few memory channels at a time (64 rows, 32 experts, N = K =
+        // 4096: 106 us all from k = 0, 79 us)
+        const int start = (int)((uint32_t)(t.expert * ((a.n + S::BN - 1) / S::BN) + t.n) % (uint32_t)whole);
+        constexpr int L = S::LN + S::LM;
+#pragma unroll
+        for (int st = 0; st < S::STAGES - 1; ++st)
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                load_part<S>(lds + st * S::BYTES, o, i, (start + st) % whole * kTileK);
+        wait_barrier<(S::STAGES - 2) * L>();
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+            read_x<S>(cur, o, f, 0, j);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            read_w<S>(cur, o, f, i);
+        uint8_t *next = lds + S::BYTES, *fill = lds + (S::STAGES - 1) * S::BYTES;
+        int at = (start + S::STAGES - 1) % whole;
+        // the loads behind the last whole step are not read
+        for (int i = 0; i < whole; ++i) {
+            tile_step<S>(cur, next, fill, at * kTileK, o, f, acc, g);
+            at = at + 1 == whole ? 0 : at + 1;
+            fill = cur;
+            cur = next;
+            next = next == lds + (S::STAGES - 1) * S::BYTES ? lds : next + S::BYTES;
         }
-    };
-    const int wn = (wave & 1) * 128, wm = (wave >> 1) * 64, l16 = lane & 15, l4 = lane >> 4;
-    i32x4 acc[WN][WM] = {};
-    load(0);
-    for (int k = 0; k < a.k; k += kTileK) {
-        __syncthreads(); // the last step's reads are over
+        wait_barrier<0>(); // nothing is on its way into LDS
+    }
+    if (whole * kTileK < a.k) {
+        // the rest of k, through registers, zeros past its end
+        const int k = whole * kTileK;
+        const bool in = k + (int)chunk < a.k;
+        uint8_t *put = lds + lane * 16;
 #pragma unroll
-        for (int i = 0; i < LN; ++i)
-            *reinterpret_cast<i32x4 *>(put + i * 32 * kTileK) = wv[i];
+        for (int i = 0; i < S::LN; ++i) {
+            i32x4 v = {0, 0, 0, 0};
+            if (in)
+                v = *reinterpret_cast<const i32x4 *>(o.wp + k + o.wo[i]);
+            *reinterpret_cast<i32x4 *>(put + (i * S::W + o.wave) * 1024) = v;
+        }
 #pragma unroll
-        for (int i = 0; i < LM; ++i)
-            *reinterpret_cast<i32x4 *>(put + (kTileN + i * 32) * kTileK) = xv[i];
+        for (int i = 0; i < S::LM; ++i) {
+            i32x4 v = {0, 0, 0, 0};
+            if (in)
+                v = *reinterpret_cast<const i32x4 *>(o.xp + k + o.xo[i]);
+            *reinterpret_cast<i32x4 *>(put + S::BN * kTileK + (i * S::W + o.wave) * 1024) = v;
+        }
         __syncthreads();
-        if (k + kTileK < a.k)
-            load(k + kTileK);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int at = ((h * 4 + l4) ^ (l16 & 7)) * 16 + l16 * kTileK;
-            i32x4 xf[WM];
 #pragma unroll
-            for (int j = 0; j < WM; ++j)
-                xf[j] = *reinterpret_cast<const i32x4 *>(lds + (kTileN + wm + 16 * j) * kTileK + at);
+            for (int j = 0; j < FM; ++j)
+                read_x<S>(lds, o, f, h, j);
 #pragma unroll
-            for (int i = 0; i < WN; ++i) {
-                const i32x4 wf = *reinterpret_cast<const i32x4 *>(lds + (wn + 16 * i) * kTileK + at);
+            for (int i = 0; i < FN; ++i) {
+                read_w<S>(lds, o, f, h * FN + i);
 #pragma unroll
-                for (int j = 0; j < WM; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf, xf[j], acc[i][j], 0, 0, 0);
+                for (int j = 0; j < FM; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w[h * FN + i], f.x[h][j], acc[i][j], 0, 0, 0);
             }
         }
     }
+    const float *scales = a.w_scales + (int64_t)t.expert * a.n;
+    constexpr int V = RowType<T>::kPer / 4; // results of 4 channels in a 16-byte store
+    // rows of whole vectors, all aligned
+    const bool vectors = a.n % RowType<T>::kPer == 0 && (((uintptr_t)a.out | (uintptr_t)a.w_scales) & 15) == 0;
+    float sx[FM];
 #pragma unroll
-    for (int j = 0; j < WM; ++j) {
+    for (int j = 0; j < FM; ++j) {
         const int64_t m = t.first + wm + 16 * j + l16;
-        if (m < t.last) {
-            const float sx = a.x_scales[m];
+        sx[j] = m < t.last ? a.x_scales[m] : 0.0f;
+    }
 #pragma unroll
-            for (int i = 0; i < WN; ++i) {
-                const int n = n0 + wn + 16 * i + l4 * 4;
-                float sw[4];
-                channel_scales(a, t.expert, n, sw);
-                store_channels<T>(a, m, n, acc[i][j], sx, sw);
+    for (int i = 0; i < FN; i += V) {
+        const int n = n0 + wn + 4 * FN * l4 + 4 * i;
+        float sw[4 * V];
+#pragma unroll
+        for (int e = 0; e < 4 * V; ++e)
+            sw[e] = n + e < a.n ? scales[n + e] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            const int64_t m = t.first + wm + 16 * j + l16;
+            float y[4 * V];
+#pragma unroll
+            for (int e = 0; e < 4 * V; ++e)
+                y[e] = (float)acc[i + e / 4][j][e % 4] * (sx[j] * sw[e]);
+            uint8_t *out = static_cast<uint8_t *>(a.out) + (m * a.n + n) * RowType<T>::kBytes;
+            if (vectors) {
+                if (m < t.last && n < a.n)
+                    *reinterpret_cast<u32x4 *>(out) = RowType<T>::pack(y);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4 * V; ++e)
+                    if (m < t.last && n + e < a.n)
+                        store_element<T>(out + e * RowType<T>::kBytes, y[e]);
             }
         }
     }
 }
 
+// The tile's rows choose among the shapes, smallest first: the last rows of
+// an expert do not pay for rows that are not there.
+template <typename T, typename S, typename... MORE>
+__device__ __forceinline__ void multiply_shaped(const moe_ep_matmul_args &a, const Tile &t, uint8_t *lds)
+{
+    if constexpr (sizeof...(MORE) == 0) {
+        multiply_tile<T, S>(a, t, lds);
+    } else {
+        if (t.last - t.first <= S::BM)
+            multiply_tile<T, S>(a, t, lds);
+        else
+            multiply_shaped<T, MORE...>(a, t, lds);
+    }
+}
+
+constexpr int largest(int x) { return x; }
+
+template <typename... MORE>
+constexpr int largest(int x, MORE... more)
+{
+    return x > largest(more...) ? x : largest(more...);
+}
+
+template <typename T, typename S, typename... MORE>
+__global__ __launch_bounds__(S::THREADS, 2) void matmul_tile_kernel(moe_ep_matmul_args a, int ntiles)
+{
+    __shared__ __align__(16) uint8_t lds[largest(S::STAGES * S::BYTES, (MORE::STAGES * MORE::BYTES)...)];
+    const Tile t = find_tile<largest(S::BM, MORE::BM...)>(a, ntiles);
+    if (t.expert < 0)
+        return;
+    multiply_shaped<T, S, MORE...>(a, t, lds);
+}
+
+template <typename S, typename... MORE>
 hipError_t tile_launch(const moe_ep_matmul_args &a, hipStream_t s)
 {
-    const int64_t ntiles = (a.n + kTileN - 1) / kTileN;
+    const int64_t ntiles = (a.n + S::BN - 1) / S::BN;
     dim3 grid;
-    if (!tile_grid(most_tiles(a, kTileM) * ntiles, kTileThreads, grid))
+    if (!tile_grid(most_tiles(a, largest(S::BM, MORE::BM...)) * ntiles, S::THREADS, grid))
         return hipErrorInvalidValue;
+    const dim3 block(S::THREADS);
     if (a.out_type == MOE_EP_BF16_ROWS)
-        hipLaunchKernelGGL((matmul_tile_kernel<Bf16>), grid, dim3(kTileThreads), 0, s, a, (int)ntiles);
+        hipLaunchKernelGGL((matmul_tile_kernel<Bf16, S, MORE...>), grid, block, 0, s, a, (int)ntiles);
     else
-        hipLaunchKernelGGL((matmul_tile_kernel<Fp32>), grid, dim3(kTileThreads), 0, s, a, (int)ntiles);
+        hipLaunchKernelGGL((matmul_tile_kernel<Fp32, S, MORE...>), grid, block, 0, s, a, (int)ntiles);
     return hipGetLastError();
 }
 
 } // namespace
 
+// The shape follows from the average rows of an expert and from how many
+// tiles there are for 256 CUs (times in us, E experts of N x K):
+//  - 256 x 256 (eight waves, one workgroup a CU) reads the least for its
+//    products, 32 bytes a clock and CU at full rate, and wins where there are
+//    two rounds of it and k is long enough for its first and last step:
+//    E 32, 4096 x 4096, 512 rows: 352 against 374 with 128 x 128; but
+//    256 rows 258 / 240, and k = 1024 (E 32, N 2048, 1024 rows) 147 / 114;
+//  - 128 x 128 (four waves, two workgroups a CU): E 32, 4096 x 4096, 96 rows
+//    142, with 64 x 64 157;
+//  - 64 x 64 (four waves, three workgroups a CU, three stages) keeps the most
+//    loads in flight, for few rows, where the weights' bytes count, and for
+//    few tiles: E 8, 4096 x 7168, 32 rows 38, with 128 x 128 42; E 1,
+//    2048 x 2048, 512 rows 9.8 / 14.9;
+//  - one row tile of 16 and too few channel tiles even for that: workgroups
+//    of 16 channels that split k, E 1, 7168 x 7168, 1 row 14.0 / 19.1.
 hipError_t launch_expert_matmul(const moe_ep_matmul_args &a, hipStream_t s)
 {
-    const int64_t average = a.num_rows / a.num_experts;
-    return average >= 48 ? tile_launch(a, s) : skinny_launch<4, 2>(a, s);
+    const int64_t average = (a.num_rows + a.num_experts - 1) / a.num_experts;
+    const auto tiles = [&](int64_t size) {
+        return a.num_experts * ((average + size - 1) / size) * ((a.n + size - 1) / size);
+    };
+    if (average <= 16 && tiles(64) < 256)
+        return skinny_launch(a, s);
+    if (average <= 48 || tiles(128) <= 256)
+        return tile_launch<TileShape<2, 2, 2, 2, 3>>(a, s);
+    if (a.k < 4096 || average < 512 || tiles(256) < 512)
+        return tile_launch<TileShape<2, 2, 4, 2, 2>, TileShape<2, 2, 4, 4, 2>>(a, s);
+    return tile_launch<TileShape<4, 2, 4, 2, 2>, TileShape<4, 2, 4, 4, 2>, TileShape<2, 4, 8, 4, 2>>(a, s);
 }
 
 } // namespace moe_ep

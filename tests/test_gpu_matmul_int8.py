@@ -68,7 +68,8 @@ CASES = [
     (500, 3, 2055, 2064, "ragged"), (1023, 1, 2055, 2064, "even"), (700, 4, 512, 4096, "one"),
     (2048, 8, 512, 1024, "even"), (2300, 8, 515, 1040, "ragged"), (5000, 2, 258, 16, "ragged"),
     (5000, 7, 300, 112, "ragged"), (4096, 16, 1024, 512, "ragged"), (1500, 4096, 8, 32, "ragged"),
-    (16, 1, 1024, 131056, "even"), (520, 1, 264, 16384, "even"),
+    (16, 1, 1024, 131056, "even"), (520, 1, 264, 16384, "even"), (2048, 8, 2055, 1040, "ragged"),
+    (2100, 4, 16400, 4112, "ragged"),
 ]
 
 
