@@ -63,16 +63,6 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x, uint32_t *red)
     return x;
 }
 
-// Largest magnitude over groups of 2^LOG consecutive lanes.
-template <int LOG>
-__device__ __forceinline__ uint32_t lanes_max(uint32_t x)
-{
-#pragma unroll
-    for (int b = 0; b < LOG; ++b)
-        x = max(x, (uint32_t)__shfl_xor((int)x, 1 << b));
-    return x;
-}
-
 __device__ __forceinline__ u32x2 int8_codes(const Int8Row &rule, const float *f)
 {
     return u32x2{rule.codes4(f), rule.codes4(f + 4)};
@@ -101,6 +91,16 @@ __global__ __launch_bounds__(BS) void add_rms_norm_kernel(moe_ep_norm_args a)
     __shared__ float sums[BS / 64];
     __shared__ uint32_t tops[BS / 64];
     const int H = a.hidden_size, units = H / kUnit;
+    constexpr int NV = kUnit / RowType<T>::kPer;
+    u32x4 weight[VPT][NV]; // read once, before the rows
+#pragma unroll
+    for (int u = 0; u < VPT; ++u)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            weight[u][v] = u32x4{0, 0, 0, 0};
+            if ((int)threadIdx.x + u * BS < units)
+                weight[u][v] = reinterpret_cast<const u32x4 *>(a.weight)[(threadIdx.x + u * BS) * NV + v];
+        }
     for (int64_t row = blockIdx.x; row < a.num_rows; row += gridDim.x) {
         const int64_t first = row * units;
         float f[VPT][kUnit];
@@ -139,9 +139,10 @@ __global__ __launch_bounds__(BS) void add_rms_norm_kernel(moe_ep_norm_args a)
 #pragma unroll
         for (int u = 0; u < VPT; ++u) {
             const int i = threadIdx.x + u * BS;
-            float w[kUnit] = {};
-            if (i < units)
-                load_elements<T, kUnit>(static_cast<const uint8_t *>(a.weight) + (int64_t)i * kUnit * RowType<T>::kBytes, w);
+            float w[kUnit];
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+                RowType<T>::unpack(weight[u][v], w + v * RowType<T>::kPer);
             top[u] = 0;
 #pragma unroll
             for (int e = 0; e < kUnit; ++e) {
@@ -167,7 +168,7 @@ __global__ __launch_bounds__(BS) void add_rms_norm_kernel(moe_ep_norm_args a)
 #pragma unroll
             for (int u = 0; u < VPT; ++u) {
                 const int i = threadIdx.x + u * BS;
-                const uint32_t t = lanes_max<kLog>(top[u]);
+                const uint32_t t = FMT == MOE_EP_NORM_MXFP8 ? max4(top[u]) : max16(top[u]);
                 if (i >= units)
                     continue;
                 const bool head = (threadIdx.x & ((1 << kLog) - 1)) == 0;
@@ -191,7 +192,7 @@ __global__ __launch_bounds__(BS) void add_rms_norm_kernel(moe_ep_norm_args a)
                         codes = kNanCodes;
                     if (head)
                         static_cast<float *>(a.scales)[(first + i) >> kLog] =
-                            t >= kInfinity ? __uint_as_float(0x7FC00000u) : m / 448.0f;
+                            t >= kInfinity ? __uint_as_float(0x7FC00000u) : m * (1.0f / 448.0f);
                 }
                 store_codes(a.out, first + i, codes);
             }
@@ -252,7 +253,13 @@ hipError_t norm_launch(const moe_ep_norm_args &a, hipStream_t s)
     return hipGetLastError();
 }
 
-// The smallest workgroup that holds the row at up to four units a thread.
+// Two units a thread keep more waves on a row than four: 32768 rows of 7168
+// bf16 to DeepSeekFp8 took 319 us with 512 threads of two units, 344 with 256
+// of four, 364 with 128 of seven, 334 with 1024 of one, and one row 4.1 / 5.8
+// / 8.5 / 3.6 us (before the lanes' maxima moved from LDS shuffles to DPP,
+// which took the 319 us to 278: 5.9 TB/s; MXFP8 269 us, int8 298).  One
+// workgroup a row: 2048 workgroups that loop over rows gained 4% there but
+// lost 6% on int8.
 template <typename T, int FMT>
 hipError_t norm_shape(const moe_ep_norm_args &a, hipStream_t s)
 {
@@ -266,7 +273,7 @@ hipError_t norm_shape(const moe_ep_norm_args &a, hipStream_t s)
     if (units <= 512)
         return norm_launch<T, FMT, 256, 2>(a, s);
     if (units <= 1024)
-        return norm_launch<T, FMT, 256, 4>(a, s);
+        return norm_launch<T, FMT, 512, 2>(a, s);
     if (units <= 2048)
         return norm_launch<T, FMT, 512, 4>(a, s);
     return norm_launch<T, FMT, 1024, 4>(a, s);
@@ -302,7 +309,7 @@ hipError_t silu_shape(const moe_ep_silu_args &a, hipStream_t s)
     if (units <= 512)
         return silu_launch<T, 256, 2>(a, s);
     if (units <= 1024)
-        return silu_launch<T, 256, 4>(a, s);
+        return silu_launch<T, 512, 2>(a, s);
     if (units <= 2048)
         return silu_launch<T, 512, 4>(a, s);
     return silu_launch<T, 1024, 4>(a, s);

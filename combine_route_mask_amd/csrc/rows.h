@@ -75,21 +75,54 @@ __device__ __forceinline__ void store16_nt(void *p, u32x4 v)
     __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(p));
 }
 
-__device__ __forceinline__ float wave_sum(float x)
+// The value of another lane of the same 16, without LDS: CTRL is a DPP
+// control (the lane with the lowest bit, or the second, turned over; the
+// mirror image within 8, or 16, lanes).
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppMirror8 = 0x141, kDppMirror16 = 0x140;
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x)
 {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1)
-        x += __shfl_xor(x, m);
-    return x;
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x)
+{
+    return __uint_as_float(dpp<CTRL>(__float_as_uint(x)));
+}
+
+// Largest value of each 4 or 16 consecutive lanes, in all of them.
+__device__ __forceinline__ uint32_t max4(uint32_t x)
+{
+    x = max(x, dpp<kDppXor1>(x));
+    return max(x, dpp<kDppXor2>(x));
+}
+
+__device__ __forceinline__ uint32_t max16(uint32_t x)
+{
+    x = max4(x);
+    x = max(x, dpp<kDppMirror8>(x));
+    return max(x, dpp<kDppMirror16>(x));
 }
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t x)
 {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const uint32_t y = (uint32_t)__shfl_xor((int)x, m);
-        x = x > y ? x : y;
-    }
+    x = max16(x);
+    x = max(x, (uint32_t)__shfl_xor((int)x, 16));
+    return max(x, (uint32_t)__shfl_xor((int)x, 32));
+}
+
+// Sum over the wave, the same in every lane (each step adds the same two
+// numbers on both sides).
+__device__ __forceinline__ float wave_sum(float x)
+{
+    x += dpp<kDppXor1>(x);
+    x += dpp<kDppXor2>(x);
+    x += dpp<kDppMirror8>(x);
+    x += dpp<kDppMirror16>(x);
+    x += __shfl_xor(x, 16);
+    x += __shfl_xor(x, 32);
     return x;
 }
 
