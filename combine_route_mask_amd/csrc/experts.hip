@@ -65,64 +65,61 @@ template <int BS>
 __device__ __forceinline__ uint32_t block_max(uint32_t top, uint32_t *red)
 {
     top = wave_max(top);
-    if (BS > 64) {
-        __syncthreads(); // the last use of red is over
-        if ((threadIdx.x & 63) == 0)
-            red[threadIdx.x >> 6] = top;
-        __syncthreads();
+    __syncthreads(); // the last use of red is over
+    if ((threadIdx.x & 63) == 0)
+        red[threadIdx.x >> 6] = top;
+    __syncthreads();
 #pragma unroll
-        for (int w = 0; w < BS / 64; ++w)
-            top = top > red[w] ? top : red[w];
-    }
+    for (int w = 0; w < BS / 64; ++w)
+        top = max(top, red[w]);
     return top;
 }
 
 // One slot's row as int8 codes to its places, by the whole workgroup.  A
 // thread keeps its first two 16-element units in registers between the
-// amax and the codes (rows of up to 32 * BS elements are read once); longer
-// rows are read again from the cache.
+// maximum and the codes, so a row of up to 32 * BS elements is read once;
+// the rest of a longer one is read again from the cache.  (A wave to a row
+// needs no barrier, but its lanes then take four times the codes in turn:
+// 8 ranks of 2048 slots, rows of 4096, 42 us against 27.)
 template <typename T, int BS>
 __device__ __forceinline__ void quantize_slot(const moe_ep_sort_args &a, const uint8_t *row, int pos, int base,
                                               uint64_t pairs, uint32_t *red)
 {
-    constexpr int kHeld = 2;
+    constexpr int kHeld = 2, B = 16 * RowType<T>::kBytes;
     const int n = (int)(a.row_bytes / RowType<T>::kBytes), units = n / 16;
-    float f[kHeld][16];
+    float f[kHeld][16], g[16];
     uint32_t top = 0;
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) {
         const int i = threadIdx.x + u * BS;
         if (i < units) {
-            load_elements<T, 16>(row + (int64_t)i * 16 * RowType<T>::kBytes, f[u]);
+            load_elements<T, 16>(row + (int64_t)i * B, f[u]);
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 top = max(top, magnitude(f[u][e]));
         }
     }
     for (int i = threadIdx.x + kHeld * BS; i < units; i += BS) {
-        float g[16];
-        load_elements<T, 16>(row + (int64_t)i * 16 * RowType<T>::kBytes, g);
+        load_elements<T, 16>(row + (int64_t)i * B, g);
 #pragma unroll
         for (int e = 0; e < 16; ++e)
             top = max(top, magnitude(g[e]));
     }
     const Int8Row rule(block_max<BS>(top, red));
-    uint8_t *out = static_cast<uint8_t *>(a.out_rows);
-#pragma unroll
-    for (int u = 0; u < kHeld; ++u) {
-        const int i = threadIdx.x + u * BS;
-        if (i < units) {
-            const u32x4 v = rule.codes16(f[u]);
-            for (uint64_t m = pairs; m; m &= m - 1)
-                *reinterpret_cast<u32x4 *>(out + (int64_t)__builtin_amdgcn_readlane(pos, base + __builtin_ctzll(m)) * n + 16 * i) = v;
-        }
-    }
-    for (int i = threadIdx.x + kHeld * BS; i < units; i += BS) {
-        float g[16];
-        load_elements<T, 16>(row + (int64_t)i * 16 * RowType<T>::kBytes, g);
-        const u32x4 v = rule.codes16(g);
+    const auto store = [&](int i, const float *x) {
+        const u32x4 codes = rule.codes16(x);
         for (uint64_t m = pairs; m; m &= m - 1)
-            *reinterpret_cast<u32x4 *>(out + (int64_t)__builtin_amdgcn_readlane(pos, base + __builtin_ctzll(m)) * n + 16 * i) = v;
+            *reinterpret_cast<u32x4 *>(
+                static_cast<uint8_t *>(a.out_rows) +
+                (int64_t)__builtin_amdgcn_readlane(pos, base + __builtin_ctzll(m)) * n + 16 * i) = codes;
+    };
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u)
+        if ((int)threadIdx.x + u * BS < units)
+            store(threadIdx.x + u * BS, f[u]);
+    for (int i = threadIdx.x + kHeld * BS; i < units; i += BS) {
+        load_elements<T, 16>(row + (int64_t)i * B, g);
+        store(i, g);
     }
     if (threadIdx.x == 0)
         for (uint64_t m = pairs; m; m &= m - 1)
@@ -323,68 +320,192 @@ __global__ __launch_bounds__(kScanBlock) void sort_scan_kernel(moe_ep_sort_args 
     }
 }
 
-// Places of a tile's pairs.  Each wave takes a quarter of the tile in
-// order; pairs of 64 consecutive lanes with the same expert find each other
-// by ballots over the bits of the expert number.
+// Places of a wave's 64 pairs, lane by lane (local experts e, -1 for none):
+// lanes with the same expert find each other by ballots over the bits of its
+// number, and the first of them takes all their places from next[e].
+__device__ __forceinline__ int place_pairs(int e, int bits, int lane, int32_t *next)
+{
+    uint64_t peers = __ballot(e >= 0);
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t m = __ballot((e >> b) & 1);
+        peers &= ((e >> b) & 1) ? m : ~m;
+    }
+    int place = -1;
+    if (e >= 0) {
+        const int leader = __builtin_ctzll(peers);
+        int start = 0;
+        if (lane == leader)
+            start = atomicAdd(&next[e], __popcll(peers));
+        start = __shfl(start, leader);
+        place = start + __popcll(peers & ((1ull << lane) - 1));
+    }
+    return place;
+}
+
+// Places of a tile's pairs: each wave takes a quarter of the tile in order.
 __global__ __launch_bounds__(kTileBlock) void sort_place_kernel(moe_ep_sort_args a, int tiles, int bits)
 {
     extern __shared__ int32_t next[]; // [waves][epr]
-    constexpr int kWaves = kTileBlock / 64;
+    constexpr int kWaves = kTileBlock / 64, IT = kSortTilePairs / kTileBlock;
     const int r = blockIdx.x / tiles, t = blockIdx.x % tiles, epr = a.experts_per_rank;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int e = threadIdx.x; e < kWaves * epr; e += kTileBlock)
-        next[e] = 0;
-    __syncthreads();
     const int per = sort_tile_slots(a.top_k) * a.top_k;
     const int64_t lo = (int64_t)t * per, hi = min(lo + per, (int64_t)a.slots * a.top_k);
-    const int share = ((per + kWaves - 1) / kWaves + 63) & ~63;
-    const int64_t wlo = min(hi, lo + (int64_t)wave * share), whi = min(hi, wlo + share);
+    const int64_t first = lo + wave * (IT * 64);
     const int32_t *ids = rank_ids(a, r);
-    int32_t *mine = next + wave * epr;
-    for (int64_t p = wlo + lane; p < whi; p += 64) {
-        const int e = local_expert(ids[p], r, epr);
-        if (e >= 0)
-            atomicAdd(&mine[e], 1);
+    int e[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int64_t p = first + i * 64 + lane;
+        e[i] = p < hi ? local_expert(ids[p], r, epr) : -1;
     }
+    for (int x = threadIdx.x; x < kWaves * epr; x += kTileBlock)
+        next[x] = 0;
+    __syncthreads();
+    int32_t *mine = next + wave * epr;
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+        if (e[i] >= 0)
+            atomicAdd(&mine[e[i]], 1);
     __syncthreads();
     const int32_t *ws = static_cast<const int32_t *>(a.workspace);
-    for (int e = threadIdx.x; e < epr; e += kTileBlock) {
-        int before = ws[((int64_t)r * epr + e) * tiles + t];
+    for (int x = threadIdx.x; x < epr; x += kTileBlock) {
+        int before = ws[((int64_t)r * epr + x) * tiles + t];
         for (int w = 0; w < kWaves; ++w) {
-            const int c = next[w * epr + e];
-            next[w * epr + e] = before;
+            const int c = next[w * epr + x];
+            next[w * epr + x] = before;
             before += c;
         }
     }
     __syncthreads();
     int32_t *position = a.position + (int64_t)r * a.slots * a.top_k;
-    for (int64_t p0 = wlo; p0 < whi; p0 += 64) {
-        const int64_t p = p0 + lane;
-        const int e = p < whi ? local_expert(ids[p], r, epr) : -1;
-        uint64_t peers = __ballot(e >= 0);
-        for (int b = 0; b < bits; ++b) {
-            const uint64_t m = __ballot((e >> b) & 1);
-            peers &= ((e >> b) & 1) ? m : ~m;
-        }
-        int place = -1;
-        if (e >= 0) {
-            const int leader = __builtin_ctzll(peers);
-            int start = 0;
-            if (lane == leader)
-                start = atomicAdd(&mine[e], __popcll(peers));
-            start = __shfl(start, leader);
-            place = start + __popcll(peers & ((1ull << lane) - 1));
-        }
-        if (p < whi)
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int place = place_pairs(e[i], bits, lane, mine);
+        const int64_t p = first + i * 64 + lane;
+        if (p < hi)
             position[p] = place < a.capacity ? place : -1;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Sorts in between: each rank's pairs fit one workgroup's registers, so one
+// launch of a workgroup a rank counts, scans and places them within the rank
+// (the gather adds the pairs of the ranks before).  Against the three
+// launches for large sorts: 8 ranks of 1024 slots, top_k 8, 17 us become
+// FIGURE us.
+// ---------------------------------------------------------------------------
+
+constexpr int kPlanBlock = 1024;
+constexpr int kPlanWaves = kPlanBlock / 64;
+
+// ws: totals [ranks], then places within the rank [ranks][slots * k].
+__global__ __launch_bounds__(kPlanBlock) void sort_plan_kernel(moe_ep_sort_args a, int bits)
+{
+    constexpr int IT = kSortPlanPairs / kPlanBlock;
+    extern __shared__ int32_t next[]; // [waves][epr], then [waves] sums
+    const int r = blockIdx.x, epr = a.experts_per_rank, pairs = a.slots * a.top_k;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int32_t *sums = next + kPlanWaves * epr, *mine = next + wave * epr;
+    const int32_t *ids = rank_ids(a, r);
+    const int share = ((pairs + kPlanWaves - 1) / kPlanWaves + 63) & ~63, first = wave * share;
+    int e[IT]; // wave w takes the pairs from w * share on, 64 at a time
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int p = first + i * 64 + lane;
+        e[i] = i * 64 < share && p < pairs ? local_expert(ids[p], r, epr) : -1;
+    }
+    for (int x = threadIdx.x; x < kPlanWaves * epr; x += kPlanBlock)
+        next[x] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+        if (e[i] >= 0)
+            atomicAdd(&mine[e[i]], 1);
+    __syncthreads();
+    // thread x: the pairs of expert x in each wave's share, then those of
+    // the experts before
+    int count = 0;
+    if ((int)threadIdx.x < epr)
+        for (int w = 0; w < kPlanWaves; ++w)
+            count += next[w * epr + threadIdx.x];
+    int before = count;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const int y = __shfl_up(before, m);
+        before += lane >= m ? y : 0;
+    }
+    if (lane == 63)
+        sums[wave] = before;
+    __syncthreads();
+    int total = 0;
+    for (int w = 0; w < kPlanWaves; ++w) {
+        if (w == wave)
+            before += total;
+        total += sums[w];
+    }
+    before -= count;
+    int32_t *ws = static_cast<int32_t *>(a.workspace);
+    if (threadIdx.x == 0)
+        ws[r] = total;
+    if ((int)threadIdx.x < epr) {
+        a.counts[r * epr + threadIdx.x] = count;
+        for (int w = 0; w < kPlanWaves; ++w) {
+            const int c = next[w * epr + threadIdx.x];
+            next[w * epr + threadIdx.x] = before;
+            before += c;
+        }
+    }
+    __syncthreads();
+    int32_t *places = ws + a.ranks + (int64_t)r * pairs;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        if (i * 64 < share) {
+            const int place = place_pairs(e[i], bits, lane, mine);
+            const int p = first + i * 64 + lane;
+            if (p < pairs)
+                places[p] = place;
+        }
     }
 }
 
 constexpr int kGatherBlock = 256;
 constexpr int kGatherVectors = 2;
 
-// Rows to their places: item (group of g slots, chunk of the row).
-template <typename T, bool QUANT>
+// Offsets from the counts, by one workgroup.
+__device__ __forceinline__ void write_offsets(const moe_ep_sort_args &a)
+{
+    __shared__ int32_t sums[kGatherBlock / 64];
+    const int E = a.ranks * a.experts_per_rank, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int per = (E + kGatherBlock - 1) / kGatherBlock, lo = min(E, (int)threadIdx.x * per), hi = min(E, lo + per);
+    int sum = 0;
+    for (int e = lo; e < hi; ++e)
+        sum += a.counts[e];
+    int before = sum;
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+        const int y = __shfl_up(before, m);
+        before += lane >= m ? y : 0;
+    }
+    if (lane == 63)
+        sums[wave] = before;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w)
+        before += sums[w];
+    before -= sum;
+    for (int e = lo; e < hi; ++e) {
+        a.offsets[e] = (int32_t)min((int64_t)before, a.capacity);
+        before += a.counts[e];
+        if (e == E - 1)
+            a.offsets[E] = (int32_t)min((int64_t)before, a.capacity);
+    }
+}
+
+// Rows to their places: item (group of g slots, chunk of the row; a quantised
+// row is one chunk).  PLANNED: the places are the plan's, within the rank; the
+// first chunk writes them out, and the workgroup behind the last item the
+// offsets.
+template <typename T, bool QUANT, bool PLANNED>
 __global__ __launch_bounds__(kGatherBlock) void sort_gather_kernel(moe_ep_sort_args a, int g, uint32_t nchunk,
                                                                    uint32_t items)
 {
@@ -392,42 +513,65 @@ __global__ __launch_bounds__(kGatherBlock) void sort_gather_kernel(moe_ep_sort_a
     __shared__ uint32_t red[BS / 64];
     const int64_t nslots = (int64_t)a.ranks * a.slots;
     const int k = a.top_k, lane = threadIdx.x & 63;
-    for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t s0 = (int64_t)(item / nchunk) * g;
-    const int c = (int)(item % nchunk), ns = (int)min((int64_t)g, nslots - s0);
-    const int pos = lane < ns * k ? a.position[s0 * k + lane] : -1;
-    const uint64_t ballot = __ballot(pos >= 0);
-    for (int i = 0; i < ns; ++i) {
-        const uint64_t pairs = slot_pairs(ballot, i, k);
-        if (!pairs)
-            continue;
-        const uint32_t slot = (uint32_t)(s0 + i);
-        const int r = (int)(slot / (uint32_t)a.slots), q = (int)(slot % (uint32_t)a.slots);
-        const uint8_t *row =
-            static_cast<const uint8_t *>(a.rows) + (int64_t)r * a.rows_rank_stride + (int64_t)q * a.row_bytes;
-        if (QUANT) {
-            quantize_slot<T, BS>(a, row, pos, i * k, pairs, red);
-            continue;
-        }
-        u32x4 v[VPT];
-        int64_t at[VPT];
-#pragma unroll
-        for (int u = 0; u < VPT; ++u) {
-            at[u] = (((int64_t)c * VPT + u) * BS + threadIdx.x) * 16;
-            if (at[u] < a.row_bytes)
-                v[u] = load16_nt(row + at[u]);
-        }
-        for (uint64_t m = pairs; m; m &= m - 1) {
-            uint8_t *out = static_cast<uint8_t *>(a.out_rows) +
-                           (int64_t)__builtin_amdgcn_readlane(pos, i * k + __builtin_ctzll(m)) * a.row_bytes;
-#pragma unroll
-            for (int u = 0; u < VPT; ++u)
-                if (at[u] < a.row_bytes)
-                    store16_nt(out + at[u], v[u]);
-        }
-        if (c == 0 && a.scale_row_bytes)
-            copy_scale_row<BS>(a, r, q, pos, i * k, pairs);
+    if (PLANNED && blockIdx.x == gridDim.x - 1) {
+        write_offsets(a);
+        return;
     }
+    const uint32_t step = PLANNED ? gridDim.x - 1 : gridDim.x;
+    const int32_t *plan = static_cast<const int32_t *>(a.workspace);
+    const int own = PLANNED && lane < a.ranks ? plan[lane] : 0; // lane x: pairs of rank x
+    for (uint32_t item = blockIdx.x; item < items; item += step) {
+        const int64_t s0 = (int64_t)(item / nchunk) * g;
+        const int c = (int)(item % nchunk), ns = (int)min((int64_t)g, nslots - s0);
+        int pos = -1;
+        if (lane < ns * k)
+            pos = PLANNED ? plan[a.ranks + s0 * k + lane] : a.position[s0 * k + lane];
+        if (PLANNED) {
+            // the pairs of the ranks before the first slot's, and of those
+            // that begin within the group
+            const int r0 = (int)((uint32_t)s0 / (uint32_t)a.slots);
+            const int r = (int)(((uint32_t)s0 + (uint32_t)lane / (uint32_t)k) / (uint32_t)a.slots);
+            int before = wave_add(lane < r0 ? own : 0);
+            const int r1 = (int)((uint32_t)(s0 + ns - 1) / (uint32_t)a.slots);
+            for (int x = r0; x < r1; ++x)
+                before += r > x ? __builtin_amdgcn_readlane(own, x) : 0;
+            pos = pos >= 0 ? pos + before : -1;
+            pos = pos < a.capacity ? pos : -1;
+            if ((int)threadIdx.x < ns * k && c == 0)
+                a.position[s0 * k + lane] = pos;
+        }
+        const uint64_t ballot = __ballot(pos >= 0);
+        for (int i = 0; i < ns; ++i) {
+            const uint64_t pairs = slot_pairs(ballot, i, k);
+            if (!pairs)
+                continue;
+            const uint32_t slot = (uint32_t)(s0 + i);
+            const int r = (int)(slot / (uint32_t)a.slots), q = (int)(slot % (uint32_t)a.slots);
+            const uint8_t *row =
+                static_cast<const uint8_t *>(a.rows) + (int64_t)r * a.rows_rank_stride + (int64_t)q * a.row_bytes;
+            if (QUANT) {
+                quantize_slot<T, BS>(a, row, pos, i * k, pairs, red);
+                continue;
+            }
+            u32x4 v[VPT];
+            int64_t at[VPT];
+#pragma unroll
+            for (int u = 0; u < VPT; ++u) {
+                at[u] = (((int64_t)c * VPT + u) * BS + threadIdx.x) * 16;
+                if (at[u] < a.row_bytes)
+                    v[u] = load16_nt(row + at[u]);
+            }
+            for (uint64_t m = pairs; m; m &= m - 1) {
+                uint8_t *out = static_cast<uint8_t *>(a.out_rows) +
+                               (int64_t)__builtin_amdgcn_readlane(pos, i * k + __builtin_ctzll(m)) * a.row_bytes;
+#pragma unroll
+                for (int u = 0; u < VPT; ++u)
+                    if (at[u] < a.row_bytes)
+                        store16_nt(out + at[u], v[u]);
+            }
+            if (c == 0 && a.scale_row_bytes)
+                copy_scale_row<BS>(a, r, q, pos, i * k, pairs);
+        }
     }
 }
 
@@ -436,73 +580,82 @@ __global__ __launch_bounds__(kGatherBlock) void sort_gather_kernel(moe_ep_sort_a
 // ---------------------------------------------------------------------------
 
 constexpr int kUnsortBlock = 128;
-constexpr int kUnsortRows = 8; // rows of a slot in flight
 
-// Item (group of g slots, chunk of 128 vectors): one output vector a lane.
-template <typename T, bool WEIGHTS>
+// Item (group of g slots, chunk of 128 * VPT vectors): VPT output vectors a
+// lane, G rows of a slot in flight.
+template <typename T, bool WEIGHTS, int VPT, int G>
 __global__ __launch_bounds__(kUnsortBlock) void unsort_kernel(moe_ep_unsort_args a, int g, uint32_t nchunk,
                                                               uint32_t items)
 {
-    constexpr int BS = kUnsortBlock, G = kUnsortRows, N = RowType<T>::kPer;
+    constexpr int BS = kUnsortBlock, N = RowType<T>::kPer;
     const int64_t nslots = (int64_t)a.ranks * a.slots, row_bytes = (int64_t)a.hidden_size * RowType<T>::kBytes;
     const int k = a.top_k, lane = threadIdx.x & 63;
     for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t s0 = (int64_t)(item / nchunk) * g;
-    const int ns = (int)min((int64_t)g, nslots - s0);
-    const int64_t at = ((int64_t)(item % nchunk) * BS + threadIdx.x) * 16;
-    int pos = -1;
-    float w = 1.0f;
-    if (lane < ns * k) {
-        pos = a.position[s0 * k + lane];
-        if (WEIGHTS) {
-            const uint32_t slot = (uint32_t)s0 + (uint32_t)lane / (uint32_t)k, S = (uint32_t)a.slots;
-            w = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(a.weights) +
-                                                (int64_t)(slot / S) * a.weights_rank_stride)[(int64_t)(slot % S) * k + lane % k];
-        }
-    }
-    const uint64_t ballot = __ballot(pos >= 0 && pos < a.num_rows);
-    const uint8_t *rows = static_cast<const uint8_t *>(a.rows) + at;
-    for (int i = 0; i < ns; ++i) {
-        uint64_t pairs = slot_pairs(ballot, i, k);
-        if (!pairs && a.keep_empty)
-            continue;
-        float acc[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-            acc[e] = 0.0f;
-        while (pairs) {
-            u32x4 v[G];
-            float wj[G];
-            uint64_t m = pairs;
-#pragma unroll
-            for (int u = 0; u < G; ++u) {
-                if (m) {
-                    const int j = i * k + __builtin_ctzll(m);
-                    m &= m - 1;
-                    wj[u] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), j));
-                    if (at < row_bytes)
-                        v[u] = load16_nt(rows + (int64_t)__builtin_amdgcn_readlane(pos, j) * row_bytes);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < G; ++u) {
-                if (pairs) {
-                    pairs &= pairs - 1;
-                    float f[N];
-                    RowType<T>::unpack(v[u], f);
-#pragma unroll
-                    for (int e = 0; e < N; ++e)
-                        acc[e] = WEIGHTS ? fmaf(wj[u], f[e], acc[e]) : acc[e] + f[e];
-                }
+        const int64_t s0 = (int64_t)(item / nchunk) * g;
+        const int ns = (int)min((int64_t)g, nslots - s0);
+        const int64_t at = ((int64_t)(item % nchunk) * BS * VPT + threadIdx.x) * 16;
+        int pos = -1;
+        float w = 1.0f;
+        if (lane < ns * k) {
+            pos = a.position[s0 * k + lane];
+            if (WEIGHTS) {
+                const uint32_t slot = (uint32_t)s0 + (uint32_t)lane / (uint32_t)k, S = (uint32_t)a.slots;
+                w = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(a.weights) +
+                                                    (int64_t)(slot / S) * a.weights_rank_stride)[(int64_t)(slot % S) * k + lane % k];
             }
         }
-        if (at < row_bytes) {
+        const uint64_t ballot = __ballot(pos >= 0 && pos < a.num_rows);
+        const uint8_t *rows = static_cast<const uint8_t *>(a.rows) + at;
+        for (int i = 0; i < ns; ++i) {
+            uint64_t pairs = slot_pairs(ballot, i, k);
+            if (!pairs && a.keep_empty)
+                continue;
+            float acc[VPT][N];
+#pragma unroll
+            for (int x = 0; x < VPT; ++x)
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    acc[x][e] = 0.0f;
+            while (pairs) {
+                u32x4 v[G][VPT];
+                float wj[G];
+                uint64_t m = pairs;
+#pragma unroll
+                for (int u = 0; u < G; ++u) {
+                    if (m) {
+                        const int j = i * k + __builtin_ctzll(m);
+                        m &= m - 1;
+                        wj[u] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), j));
+                        const int64_t row = (int64_t)__builtin_amdgcn_readlane(pos, j) * row_bytes;
+#pragma unroll
+                        for (int x = 0; x < VPT; ++x)
+                            if (at + x * BS * 16 < row_bytes)
+                                v[u][x] = load16_nt(rows + row + x * BS * 16);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < G; ++u) {
+                    if (pairs) {
+                        pairs &= pairs - 1;
+#pragma unroll
+                        for (int x = 0; x < VPT; ++x) {
+                            float f[N];
+                            RowType<T>::unpack(v[u][x], f);
+#pragma unroll
+                            for (int e = 0; e < N; ++e)
+                                acc[x][e] = WEIGHTS ? fmaf(wj[u], f[e], acc[x][e]) : acc[x][e] + f[e];
+                        }
+                    }
+                }
+            }
             const uint32_t slot = (uint32_t)(s0 + i), S = (uint32_t)a.slots;
-            store16_nt(static_cast<uint8_t *>(a.out) + (int64_t)(slot / S) * a.out_rank_stride +
-                           (int64_t)(slot % S) * row_bytes + at,
-                       RowType<T>::pack(acc));
+            uint8_t *out = static_cast<uint8_t *>(a.out) + (int64_t)(slot / S) * a.out_rank_stride +
+                           (int64_t)(slot % S) * row_bytes + at;
+#pragma unroll
+            for (int x = 0; x < VPT; ++x)
+                if (at + x * BS * 16 < row_bytes)
+                    store16_nt(out + x * BS * 16, RowType<T>::pack(acc[x]));
         }
-    }
     }
 }
 
@@ -649,61 +802,99 @@ hipError_t launch_expert_sort(const moe_ep_sort_args &a, hipStream_t s)
             hipLaunchKernelGGL((sort_direct_kernel<Fp32, true>), grid, dim3(kDirectBlock), 0, s, a, nchunk);
         return hipGetLastError();
     }
-    const int tiles = (int)sort_tiles(a.slots, a.top_k), epr = a.experts_per_rank;
+    const int epr = a.experts_per_rank;
     int bits = 0;
     while ((1 << bits) < epr)
         ++bits;
-    if (a.slots) {
-        hipLaunchKernelGGL(sort_count_kernel, dim3(a.ranks * tiles), dim3(kTileBlock), epr * 4, s, a, tiles);
+    const bool planned = sort_is_planned(a.slots, a.top_k, epr);
+    if (planned) {
+        const size_t lds = (size_t)(kPlanWaves * epr + kPlanWaves) * 4;
+        hipLaunchKernelGGL(sort_plan_kernel, dim3(a.ranks), dim3(kPlanBlock), lds, s, a, bits);
         if (hipError_t e = hipGetLastError())
             return e;
+    } else {
+        const int tiles = (int)sort_tiles(a.slots, a.top_k);
+        if (a.slots) {
+            hipLaunchKernelGGL(sort_count_kernel, dim3(a.ranks * tiles), dim3(kTileBlock), epr * 4, s, a, tiles);
+            if (hipError_t e = hipGetLastError())
+                return e;
+        }
+        hipLaunchKernelGGL(sort_scan_kernel, dim3(1), dim3(kScanBlock), 0, s, a, tiles);
+        if (hipError_t e = hipGetLastError())
+            return e;
+        if (!a.slots)
+            return hipSuccess;
+        hipLaunchKernelGGL(sort_place_kernel, dim3(a.ranks * tiles), dim3(kTileBlock), (kTileBlock / 64) * epr * 4, s,
+                           a, tiles, bits);
+        if (hipError_t e = hipGetLastError())
+            return e;
+        if (!a.capacity)
+            return hipSuccess;
     }
-    hipLaunchKernelGGL(sort_scan_kernel, dim3(1), dim3(kScanBlock), 0, s, a, tiles);
-    if (hipError_t e = hipGetLastError())
-        return e;
-    if (!a.slots)
-        return hipSuccess;
-    hipLaunchKernelGGL(sort_place_kernel, dim3(a.ranks * tiles), dim3(kTileBlock), (kTileBlock / 64) * epr * 4, s, a,
-                       tiles, bits);
-    if (hipError_t e = hipGetLastError())
-        return e;
-    if (!a.capacity)
-        return hipSuccess;
     const int g = slots_per_group(nslots, a.capacity, a.top_k);
+    const int64_t groups = (nslots + g - 1) / g;
     const uint32_t nchunk =
         a.quantize ? 1 : (uint32_t)((nvec + kGatherBlock * kGatherVectors - 1) / (kGatherBlock * kGatherVectors));
-    const int64_t items = (nslots + g - 1) / g * nchunk;
+    const int64_t items = groups * nchunk;
     if (items > INT32_MAX)
         return hipErrorInvalidValue;
-    const dim3 grid = grid_of(items);
-    if (!a.quantize)
-        hipLaunchKernelGGL((sort_gather_kernel<Bf16, false>), grid, dim3(kGatherBlock), 0, s, a, g, nchunk, (uint32_t)items);
-    else if (a.row_type == MOE_EP_BF16_ROWS)
-        hipLaunchKernelGGL((sort_gather_kernel<Bf16, true>), grid, dim3(kGatherBlock), 0, s, a, g, nchunk, (uint32_t)items);
-    else
-        hipLaunchKernelGGL((sort_gather_kernel<Fp32, true>), grid, dim3(kGatherBlock), 0, s, a, g, nchunk, (uint32_t)items);
+    dim3 grid = grid_of(items);
+    grid.x += planned;
+    const dim3 block(kGatherBlock);
+#define MOE_EP_GATHER(T, QUANT, PLANNED) \
+    hipLaunchKernelGGL((sort_gather_kernel<T, QUANT, PLANNED>), grid, block, 0, s, a, g, nchunk, (uint32_t)items)
+    const bool bf16 = a.row_type == MOE_EP_BF16_ROWS;
+    if (planned) {
+        if (!a.quantize)
+            MOE_EP_GATHER(Bf16, false, true);
+        else if (bf16)
+            MOE_EP_GATHER(Bf16, true, true);
+        else
+            MOE_EP_GATHER(Fp32, true, true);
+    } else {
+        if (!a.quantize)
+            MOE_EP_GATHER(Bf16, false, false);
+        else if (bf16)
+            MOE_EP_GATHER(Bf16, true, false);
+        else
+            MOE_EP_GATHER(Fp32, true, false);
+    }
+#undef MOE_EP_GATHER
     return hipGetLastError();
 }
 
-hipError_t launch_expert_unsort(const moe_ep_unsort_args &a, hipStream_t s)
+namespace {
+
+template <typename T, bool WEIGHTS, int VPT, int G>
+hipError_t unsort_launch(const moe_ep_unsort_args &a, hipStream_t s, int g)
 {
-    const bool bf16 = a.row_type == MOE_EP_BF16_ROWS;
-    const int64_t nslots = (int64_t)a.ranks * a.slots, nvec = (int64_t)a.hidden_size * (bf16 ? 2 : 4) / 16;
-    const int g = slots_per_group(nslots, a.num_rows, a.top_k);
-    const uint32_t nchunk = (uint32_t)((nvec + kUnsortBlock - 1) / kUnsortBlock);
+    const int64_t nslots = (int64_t)a.ranks * a.slots, nvec = (int64_t)a.hidden_size * RowType<T>::kBytes / 16;
+    const uint32_t nchunk = (uint32_t)((nvec + kUnsortBlock * VPT - 1) / (kUnsortBlock * VPT));
     const int64_t items = (nslots + g - 1) / g * nchunk;
     if (items > INT32_MAX)
         return hipErrorInvalidValue;
-    const dim3 grid = grid_of(items), block(kUnsortBlock);
-    if (bf16 && a.weights)
-        hipLaunchKernelGGL((unsort_kernel<Bf16, true>), grid, block, 0, s, a, g, nchunk, (uint32_t)items);
-    else if (bf16)
-        hipLaunchKernelGGL((unsort_kernel<Bf16, false>), grid, block, 0, s, a, g, nchunk, (uint32_t)items);
-    else if (a.weights)
-        hipLaunchKernelGGL((unsort_kernel<Fp32, true>), grid, block, 0, s, a, g, nchunk, (uint32_t)items);
-    else
-        hipLaunchKernelGGL((unsort_kernel<Fp32, false>), grid, block, 0, s, a, g, nchunk, (uint32_t)items);
+    hipLaunchKernelGGL((unsort_kernel<T, WEIGHTS, VPT, G>), grid_of(items), dim3(kUnsortBlock), 0, s, a, g, nchunk,
+                       (uint32_t)items);
     return hipGetLastError();
+}
+
+// Slots with several rows have enough loads in flight with one vector a
+// lane; where most have none or one (regions of many ranks), four.
+template <typename T, bool WEIGHTS>
+hipError_t unsort_shape(const moe_ep_unsort_args &a, hipStream_t s)
+{
+    const int64_t nslots = (int64_t)a.ranks * a.slots;
+    const int g = slots_per_group(nslots, a.num_rows, a.top_k);
+    return a.num_rows <= nslots ? unsort_launch<T, WEIGHTS, 4, 2>(a, s, g) : unsort_launch<T, WEIGHTS, 1, 8>(a, s, g);
+}
+
+} // namespace
+
+hipError_t launch_expert_unsort(const moe_ep_unsort_args &a, hipStream_t s)
+{
+    if (a.row_type == MOE_EP_BF16_ROWS)
+        return a.weights ? unsort_shape<Bf16, true>(a, s) : unsort_shape<Bf16, false>(a, s);
+    return a.weights ? unsort_shape<Fp32, true>(a, s) : unsort_shape<Fp32, false>(a, s);
 }
 
 hipError_t launch_expert_unsort_backward(const moe_ep_unsort_grad_args &a, hipStream_t s)

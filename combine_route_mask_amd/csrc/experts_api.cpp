@@ -69,6 +69,9 @@ int64_t sort_workspace(int32_t ranks, int32_t slots, int32_t top_k, int32_t epr)
 {
     if (slots == 0 || sort_is_direct(ranks, slots, top_k, ranks * epr))
         return 0;
+    // a total for each rank and a place for each pair
+    if (sort_is_planned(slots, top_k, epr))
+        return 4 * ((int64_t)ranks + (int64_t)ranks * slots * top_k);
     // one count for each (expert, tile of its rank)
     return 4 * (int64_t)ranks * epr * sort_tiles(slots, top_k);
 }

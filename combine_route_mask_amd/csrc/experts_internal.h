@@ -17,7 +17,7 @@ int fail(int code, const std::string &msg);
 int ok();
 
 // A sort's ids are cut into tiles of this many pairs (whole slots).
-constexpr int kSortTilePairs = 2048;
+constexpr int kSortTilePairs = 1024;
 // Largest sort whose every workgroup ranks its slot against all pairs itself.
 constexpr int64_t kSortDirectPairs = 2048;
 constexpr int kSortDirectExperts = 1024;
@@ -36,6 +36,15 @@ inline int64_t sort_tiles(int64_t slots, int top_k)
 inline bool sort_is_direct(int ranks, int64_t slots, int top_k, int experts)
 {
     return (int64_t)ranks * slots * top_k <= kSortDirectPairs && experts <= kSortDirectExperts;
+}
+
+// Sorts whose ranks' pairs fit one workgroup each (sort_plan_kernel).
+constexpr int kSortPlanPairs = 8192;
+constexpr int kSortPlanExperts = 512;
+
+inline bool sort_is_planned(int64_t slots, int top_k, int experts_per_rank)
+{
+    return slots > 0 && slots * top_k <= kSortPlanPairs && experts_per_rank <= kSortPlanExperts;
 }
 
 hipError_t launch_expert_sort(const moe_ep_sort_args &a, hipStream_t s);

@@ -14,6 +14,8 @@ namespace moe_ep {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 AnyAligned __attribute__((aligned(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
 
 struct Tile {
     int expert;          // -1: no such tile
@@ -421,10 +423,10 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
             }
         }
     }
-    const float *scales = a.w_scales + (int64_t)t.expert * a.n;
+    // Rows of any n start at any element: 16-byte stores need no more than an
+    // element's alignment.
     constexpr int V = RowType<T>::kPer / 4; // results of 4 channels in a 16-byte store
-    // rows of whole vectors, all aligned
-    const bool vectors = a.n % RowType<T>::kPer == 0 && (((uintptr_t)a.out | (uintptr_t)a.w_scales) & 15) == 0;
+    const float *scales = a.w_scales + (int64_t)t.expert * a.n;
     float sx[FM];
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
@@ -434,25 +436,36 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
 #pragma unroll
     for (int i = 0; i < FN; i += V) {
         const int n = n0 + wn + 4 * FN * l4 + 4 * i;
+        const bool all = n + 4 * V <= a.n;
         float sw[4 * V];
 #pragma unroll
-        for (int e = 0; e < 4 * V; ++e)
-            sw[e] = n + e < a.n ? scales[n + e] : 0.0f;
+        for (int v = 0; v < V; ++v) {
+            f32x4 four = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (all)
+                four = *reinterpret_cast<const f32x4 *>(scales + n + 4 * v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sw[4 * v + e] = four[e];
+                if (!all && n + 4 * v + e < a.n)
+                    sw[4 * v + e] = scales[n + 4 * v + e];
+            }
+        }
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
             const int64_t m = t.first + wm + 16 * j + l16;
+            if (m >= t.last)
+                continue;
             float y[4 * V];
 #pragma unroll
             for (int e = 0; e < 4 * V; ++e)
                 y[e] = (float)acc[i + e / 4][j][e % 4] * (sx[j] * sw[e]);
             uint8_t *out = static_cast<uint8_t *>(a.out) + (m * a.n + n) * RowType<T>::kBytes;
-            if (vectors) {
-                if (m < t.last && n < a.n)
-                    *reinterpret_cast<u32x4 *>(out) = RowType<T>::pack(y);
+            if (all) {
+                *reinterpret_cast<AnyAligned *>(out) = RowType<T>::pack(y);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4 * V; ++e)
-                    if (m < t.last && n + e < a.n)
+                    if (n + e < a.n)
                         store_element<T>(out + e * RowType<T>::kBytes, y[e]);
             }
         }
@@ -521,7 +534,8 @@ hipError_t tile_launch(const moe_ep_matmul_args &a, hipStream_t s)
 //  - 64 x 64 (four waves, three workgroups a CU, three stages) keeps the most
 //    loads in flight, for few rows, where the weights' bytes count, and for
 //    few tiles: E 8, 4096 x 7168, 32 rows 38, with 128 x 128 42; E 1,
-//    2048 x 2048, 512 rows 9.8 / 14.9;
+//    2048 x 2048, 512 rows 9.8 / 14.9 (a short k ends before the stages fill:
+//    E 8, 7168 x 2048, 16 rows 24.4 / 21.7, but E 32, 4 rows 91 / 98);
 //  - one row tile of 16 and too few channel tiles even for that: workgroups
 //    of 16 channels that split k, E 1, 7168 x 7168, 1 row 14.0 / 19.1.
 hipError_t launch_expert_matmul(const moe_ep_matmul_args &a, hipStream_t s)

@@ -113,6 +113,16 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x)
     return max(x, (uint32_t)__shfl_xor((int)x, 32));
 }
 
+__device__ __forceinline__ int wave_add(int x)
+{
+    x += (int)dpp<kDppXor1>((uint32_t)x);
+    x += (int)dpp<kDppXor2>((uint32_t)x);
+    x += (int)dpp<kDppMirror8>((uint32_t)x);
+    x += (int)dpp<kDppMirror16>((uint32_t)x);
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+
 // Sum over the wave, the same in every lane (each step adds the same two
 // numbers on both sides).
 __device__ __forceinline__ float wave_sum(float x)
@@ -132,36 +142,36 @@ __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(
 constexpr uint32_t kInfinity = 0x7F800000u;
 
 // The int8 rule of a row whose largest magnitude is `top`: scale = top / 127,
-// code = x / scale to nearest even, taken as the correctly rounded quotient
-// 127 x / top.  Ties are common (bf16 rows are ratios of 8-bit integers) and
-// this form keeps them exact, where a product with 127 / top would fall to
-// either side.  A huge row is brought down by a power of two first, so that
-// 127 x stays finite.
+// code = x / scale = 127 x / top to nearest even.  Ties are common (bf16 rows
+// are ratios of 8-bit integers), so the quotient has to be right on them: a
+// product with 1 / top is brought to the correctly rounded quotient by the
+// remainder, which the fma gives exactly (a quotient that fp32 holds, such as
+// a tie, comes out as it is).  Rows of extreme magnitude are brought near 1 by
+// a power of two first, so that 127 x and 1 / top stay normal.
 struct Int8Row {
-    float scale, by, top;
+    float scale, by, top, inv;
+    bool finite;
     __device__ __forceinline__ explicit Int8Row(uint32_t bits)
     {
         top = __uint_as_float(bits);
-        if (bits == 0 || bits >= kInfinity) {
-            scale = bits ? __uint_as_float(0x7FC00000u) : 0.0f;
-            by = 0.0f;
-            top = 1.0f;
-        } else {
-            scale = top / 127.0f;
-            by = top > 0x1p+100f ? 127.0f * 0x1p-20f : 127.0f;
-            top = top > 0x1p+100f ? top * 0x1p-20f : top;
-        }
+        finite = bits < kInfinity;
+        scale = finite ? top / 127.0f : __uint_as_float(0x7FC00000u);
+        const float up = top > 0x1p+60f ? 0x1p-100f : top < 0x1p-60f ? 0x1p+100f : 1.0f;
+        by = 127.0f * up;
+        top = bits ? top * up : 1.0f;
+        inv = 1.0f / top;
     }
-    // NaN * 0 and infinity * 0 convert to 0.
-    __device__ __forceinline__ int code(float x) const
+    // 127 x / top plus 1.5 * 2^23: the sum's low byte is the code.
+    __device__ __forceinline__ uint32_t code(float x) const
     {
-        const float c = rintf((x * by) / top);
-        return c == c ? (int)c : 0;
+        const float t = x * by, c = t * inv;
+        return __float_as_uint(fmaf(fmaf(-c, top, t), inv, c) + 12582912.0f);
     }
     __device__ __forceinline__ uint32_t codes4(const float *f) const
     {
-        return (uint32_t)(code(f[0]) & 0xFF) | ((uint32_t)(code(f[1]) & 0xFF) << 8) |
-               ((uint32_t)(code(f[2]) & 0xFF) << 16) | ((uint32_t)(code(f[3]) & 0xFF) << 24);
+        const uint32_t lo = __builtin_amdgcn_perm(code(f[1]), code(f[0]), 0x0C0C0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(code(f[3]), code(f[2]), 0x04000C0Cu);
+        return finite ? lo | hi : 0;
     }
     __device__ __forceinline__ u32x4 codes16(const float *f) const
     {

@@ -153,8 +153,11 @@ def test_nothing_to_do_needs_no_gpu(X, m):
 
 def test_sort_workspace(X, m):
     assert X.expert_sort_workspace_bytes(1, 256, 8, 64) == 0          # one launch
-    assert X.expert_sort_workspace_bytes(1, 257, 8, 64) == 4 * 64 * 2
-    assert X.expert_sort_workspace_bytes(64, 32768, 8, 4) == 4 * 256 * 128
+    assert X.expert_sort_workspace_bytes(1, 257, 8, 64) == 4 * (1 + 257 * 8)  # one workgroup a rank
+    assert X.expert_sort_workspace_bytes(8, 1024, 8, 32) == 4 * (8 + 8 * 1024 * 8)
+    assert X.expert_sort_workspace_bytes(1, 1025, 8, 64) == 4 * 64 * 9        # tiles of 128 slots
+    assert X.expert_sort_workspace_bytes(1, 257, 8, 513) == 4 * 513 * 3
+    assert X.expert_sort_workspace_bytes(64, 32768, 8, 4) == 4 * 256 * 256
     for bad in ((0, 1, 1, 1), (1, -1, 1, 1), (1, 1, 65, 1), (1, 1, 1, 4097), (1, 1, 1, 1 << 32), (64, 1 << 30, 8, 4)):
         with pytest.raises(m.MoeEpArgError):
             X.expert_sort_workspace_bytes(*bad)
