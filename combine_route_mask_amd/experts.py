@@ -84,12 +84,13 @@ def _device(t, name):
 
 def _flat(t, name, dev, dtype, shape):
     """A contiguous tensor of this device, type and shape."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return
     if t.device != dev:
         _refuse(f"{name} must be on {dev}, got {t.device}")
     if t.dtype != dtype or t.shape != shape:
         _refuse(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if not t.is_contiguous():
-        _refuse(f"{name} must be contiguous")
+    _refuse(f"{name} must be contiguous")
 
 
 def _plane(t, name, dev):
@@ -99,9 +100,9 @@ def _plane(t, name, dev):
         _refuse(f"{name} must be on {dev}, got {t.device}")
     if t.dim() != 3:
         _refuse(f"{name} must be [ranks, slots, row], got {list(t.shape)}")
-    if t.is_contiguous():
-        return t.shape[1] * t.shape[2] * t.element_size()
     R, S, X = t.shape
+    if t.is_contiguous():
+        return S * X * t.element_size()
     s0, s1, s2 = t.stride()
     if (X > 1 and s2 != 1) or (S > 1 and s1 != X) or (R > 1 and s0 < S * X):
         _refuse(f"{name}: the slots of a rank must be contiguous, got strides {t.stride()}")
@@ -117,17 +118,26 @@ def _row_type(t, name):
 
 def _no_grad(*tensors):
     """Without a gradient of its own, an operator refuses to drop one."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                break
+        else:
+            return
         _refuse("this call has no gradient: detach its inputs or call it under torch.no_grad()")
 
 
+_device_now = torch._C._cuda_getDevice
+_stream_now = torch._C._cuda_getCurrentRawStream
+
+
 class _On:
-    """The stream and device of a call: outputs allocated inside belong to
-    that stream, launches go to it."""
+    """The device and stream of a call as the current ones: outputs allocated
+    inside belong to that stream, launches go to it."""
 
     def __init__(self, dev, stream):
         self.contexts = []
-        if torch.cuda.current_device() != dev.index:
+        if _device_now() != dev.index:
             self.contexts.append(torch.cuda.device(dev))
         if stream is not None:
             if isinstance(stream, int):
@@ -135,12 +145,10 @@ class _On:
             if stream.device != dev:
                 _refuse(f"the stream is on {stream.device}, the tensors on {dev}")
             self.contexts.append(torch.cuda.stream(stream))
-        self.index = dev.index
 
     def __enter__(self):
         for c in self.contexts:
             c.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         for c in reversed(self.contexts):
@@ -173,7 +181,7 @@ def expert_sort(ids, rows, experts_per_rank: int, *, scales=None, capacity: Opti
 
     Differentiable in ``rows`` (bf16 or fp32, neither ``quantize`` nor
     ``out``); the rows behind the last pair are then zeros."""
-    if torch.is_grad_enabled() and rows.requires_grad:
+    if rows.requires_grad and torch.is_grad_enabled():
         _need(not quantize and out is None and rows.dtype in _ROW_TYPES,
               "only a sort of bf16 or fp32 rows into a new tensor has a gradient")
         r, sc, p, o, c = _SortFunction.apply(rows, ids, experts_per_rank, scales, capacity, out_scales, stream)
@@ -183,6 +191,9 @@ def expert_sort(ids, rows, experts_per_rank: int, *, scales=None, capacity: Opti
 
 def _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, stream, zeros=False):
     dev = _device(rows, "rows")
+    if stream is not None or dev.index != _device_now():
+        with _On(dev, stream):
+            return _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, None, zeros)
     if ids.dtype != torch.int32:
         _refuse(f"ids must be int32, got {ids.dtype}")
     ids_stride, rows_stride = _plane(ids, "ids", dev), _plane(rows, "rows", dev)
@@ -204,37 +215,31 @@ def _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, stream, z
             _refuse(f"ids are [{R}, {S}, k], scales {list(scales.shape)}")
         scale_bytes = scales.shape[2] * scales.element_size()
     work = expert_sort_workspace_bytes(R, S, k, epr)
-    on = _On(dev, stream)
-    with on as raw:
-        if out is None:
-            out = (torch.zeros if zeros else torch.empty)((capacity, X), dtype=torch.int8 if quantize else rows.dtype,
-                                                          device=dev)
+    dtype = torch.int8 if quantize else rows.dtype
+    if out is None:
+        out = (torch.zeros if zeros else torch.empty)((capacity, X), dtype=dtype, device=dev)
+    else:
+        _flat(out, "out", dev, dtype, (capacity, X))
+    if quantize or scales is not None:
+        shape, dtype = ((capacity,), torch.float32) if quantize else ((capacity, scales.shape[2]), scales.dtype)
+        if out_scales is None:
+            out_scales = torch.empty(shape, dtype=dtype, device=dev)
         else:
-            _flat(out, "out", dev, torch.int8 if quantize else rows.dtype, (capacity, X))
-        if quantize:
-            if out_scales is None:
-                out_scales = torch.empty(capacity, dtype=torch.float32, device=dev)
-            else:
-                _flat(out_scales, "out_scales", dev, torch.float32, (capacity,))
-        elif scales is not None:
-            if out_scales is None:
-                out_scales = torch.empty((capacity, scales.shape[2]), dtype=scales.dtype, device=dev)
-            else:
-                _flat(out_scales, "out_scales", dev, scales.dtype, (capacity, scales.shape[2]))
-        else:
-            out_scales = None
-        E = R * epr
-        position = torch.empty((R, S, k), dtype=torch.int32, device=dev)
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
-        counts = torch.empty(E, dtype=torch.int32, device=dev)
-        space = torch.empty(work, dtype=torch.uint8, device=dev).data_ptr() if work else 0
-        # the workspace's memory returns to the stream's pool behind this launch
-        _check(lib.moe_ep_expert_sort(_SORT.pack(
-            ids.data_ptr(), ids_stride, rows.data_ptr(), rows_stride, X * rows.element_size(),
-            scales.data_ptr() if scales is not None else 0, scales_stride, scale_bytes,
-            out.data_ptr(), out_scales.data_ptr() if out_scales is not None else 0,
-            position.data_ptr(), offsets.data_ptr(), counts.data_ptr(), space, work, capacity,
-            R, S, k, epr, 1 if quantize else 0, row_type), raw))
+            _flat(out_scales, "out_scales", dev, dtype, shape)
+    else:
+        out_scales = None
+    E = R * epr
+    position = ids.new_empty((R, S, k))
+    offsets = ids.new_empty(E + 1)
+    counts = ids.new_empty(E)
+    # the workspace's memory returns to the stream's pool behind this launch
+    space = torch.empty(work, dtype=torch.uint8, device=dev).data_ptr() if work else 0
+    _check(lib.moe_ep_expert_sort(_SORT.pack(
+        ids.data_ptr(), ids_stride, rows.data_ptr(), rows_stride, X * rows.element_size(),
+        scales.data_ptr() if scales is not None else 0, scales_stride, scale_bytes,
+        out.data_ptr(), out_scales.data_ptr() if out_scales is not None else 0,
+        position.data_ptr(), offsets.data_ptr(), counts.data_ptr(), space, work, capacity,
+        R, S, k, epr, 1 if quantize else 0, row_type), _stream_now(dev.index)))
     return SortedRows(out, out_scales, position, offsets, counts)
 
 
@@ -275,7 +280,7 @@ def expert_unsort(position, rows, weights=None, *, out=None, keep_empty: bool = 
     left alone, as a combine never reads them.
 
     Differentiable in ``rows`` and ``weights`` (without ``out``)."""
-    if torch.is_grad_enabled() and (rows.requires_grad or (weights is not None and weights.requires_grad)):
+    if (rows.requires_grad or (weights is not None and weights.requires_grad)) and torch.is_grad_enabled():
         _need(out is None and not keep_empty, "only an unsort into a new tensor has a gradient")
         return _UnsortFunction.apply(rows, weights, position, stream)
     return _unsort(position, rows, weights, out, keep_empty, stream)
@@ -297,6 +302,9 @@ def _weights(weights, position, dev):
 
 def _unsort(position, rows, weights, out, keep_empty, stream):
     dev = _device(rows, "rows")
+    if stream is not None or dev.index != _device_now():
+        with _On(dev, stream):
+            return _unsort(position, rows, weights, out, keep_empty, None)
     rt = _row_type(rows, "rows")
     if rows.dim() != 2:
         _refuse(f"rows must be [num_rows, hidden], got {list(rows.shape)}")
@@ -305,20 +313,18 @@ def _unsort(position, rows, weights, out, keep_empty, stream):
     _position(position, dev)
     R, S, k = position.shape
     wp, ws = _weights(weights, position, dev)
-    on = _On(dev, stream)
-    with on as raw:
-        if out is None:
-            if keep_empty:
-                _refuse("keep_empty needs a given out")
-            out = torch.empty((R, S, H), dtype=rows.dtype, device=dev)
-            stride = S * H * rows.element_size()
-        else:
-            if out.dtype != rows.dtype or out.shape != (R, S, H):
-                _refuse(f"out must be {rows.dtype} [{R}, {S}, {H}], got {out.dtype} {list(out.shape)}")
-            stride = _plane(out, "out", dev)
-        _check(lib.moe_ep_expert_unsort(_UNSORT.pack(
-            position.data_ptr(), rows.data_ptr(), wp, ws, out.data_ptr(), stride, M, R, S, k, H, rt,
-            1 if keep_empty else 0), raw))
+    if out is None:
+        if keep_empty:
+            _refuse("keep_empty needs a given out")
+        out = rows.new_empty((R, S, H))
+        stride = S * H * rows.element_size()
+    else:
+        if out.dtype != rows.dtype or out.shape != (R, S, H):
+            _refuse(f"out must be {rows.dtype} [{R}, {S}, {H}], got {out.dtype} {list(out.shape)}")
+        stride = _plane(out, "out", dev)
+    _check(lib.moe_ep_expert_unsort(_UNSORT.pack(
+        position.data_ptr(), rows.data_ptr(), wp, ws, out.data_ptr(), stride, M, R, S, k, H, rt,
+        1 if keep_empty else 0), _stream_now(dev.index)))
     return out
 
 
@@ -330,6 +336,10 @@ def expert_unsort_backward(position, grad_out, rows=None, weights=None, *, grad_
     ``grad_rows``, or zeros.  ``rows``, the unsort's input, is needed for
     grad_weights; without it give ``grad_rows``."""
     dev = _device(grad_out, "grad_out")
+    if stream is not None or dev.index != _device_now():
+        with _On(dev, stream):
+            return expert_unsort_backward(position, grad_out, rows, weights, grad_rows=grad_rows, need_rows=need_rows,
+                                          need_weights=need_weights)
     rt = _row_type(grad_out, "grad_out")
     stride = _plane(grad_out, "grad_out", dev)
     _position(position, dev)
@@ -348,17 +358,15 @@ def expert_unsort_backward(position, grad_out, rows=None, weights=None, *, grad_
     if grad_rows is not None:
         _flat(grad_rows, "grad_rows", dev, grad_out.dtype, (M, H))
     wp, ws = _weights(weights, position, dev)
-    on = _On(dev, stream)
-    with on as raw:
-        if not need_rows:
-            grad_rows = None
-        elif grad_rows is None:
-            grad_rows = torch.zeros((M, H), dtype=grad_out.dtype, device=dev)
-        gw = torch.empty((R, S, k), dtype=torch.float32, device=dev) if need_weights else None
-        _check(lib.moe_ep_expert_unsort_backward(_UNSORT_GRAD.pack(
-            position.data_ptr(), grad_out.data_ptr(), stride, rows.data_ptr() if rows is not None else 0, wp, ws,
-            grad_rows.data_ptr() if grad_rows is not None else 0, gw.data_ptr() if gw is not None else 0,
-            M, R, S, k, H, rt, 0), raw))
+    if not need_rows:
+        grad_rows = None
+    elif grad_rows is None:
+        grad_rows = torch.zeros((M, H), dtype=grad_out.dtype, device=dev)
+    gw = torch.empty((R, S, k), dtype=torch.float32, device=dev) if need_weights else None
+    _check(lib.moe_ep_expert_unsort_backward(_UNSORT_GRAD.pack(
+        position.data_ptr(), grad_out.data_ptr(), stride, rows.data_ptr() if rows is not None else 0, wp, ws,
+        grad_rows.data_ptr() if grad_rows is not None else 0, gw.data_ptr() if gw is not None else 0,
+        M, R, S, k, H, rt, 0), _stream_now(dev.index)))
     return grad_rows, gw
 
 
@@ -396,6 +404,10 @@ def expert_matmul(x, x_scales, weight, weight_scales, *, offsets=None, out=None,
     [M, N] are left as they were, in ``out`` or uninitialised.  Dense: weight
     [N, K], scales [N], no offsets.  The sum is exact; bf16 or fp32 result."""
     dev = _device(x, "x")
+    if stream is not None or dev.index != _device_now():
+        with _On(dev, stream):
+            return expert_matmul(x, x_scales, weight, weight_scales, offsets=offsets, out=out, dtype=dtype)
+    _no_grad(x_scales, weight_scales)
     if x.dim() != 2 or weight.dim() not in (2, 3):
         _refuse(f"x must be [M, K] and weight [E, N, K] or [N, K], got {list(x.shape)} and {list(weight.shape)}")
     M, K = x.shape
@@ -414,16 +426,14 @@ def expert_matmul(x, x_scales, weight, weight_scales, *, offsets=None, out=None,
             _refuse("a dense weight [N, K] takes no offsets")
         _flat(weight, "weight", dev, torch.int8, (N, K))
         _flat(weight_scales, "weight_scales", dev, torch.float32, (N,))
-    on = _On(dev, stream)
-    with on as raw:
-        if out is None:
-            out = torch.empty((M, N), dtype=dtype, device=dev)
-        else:
-            _flat(out, "out", dev, out.dtype, (M, N))
-        _check(lib.moe_ep_expert_matmul(_MATMUL.pack(
-            x.data_ptr(), x_scales.data_ptr(), weight.data_ptr(), weight_scales.data_ptr(),
-            offsets.data_ptr() if offsets is not None else 0, out.data_ptr(), M, E, N, K,
-            _row_type(out, "out")), raw))
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=dev)
+    else:
+        _flat(out, "out", dev, out.dtype, (M, N))
+    _check(lib.moe_ep_expert_matmul(_MATMUL.pack(
+        x.data_ptr(), x_scales.data_ptr(), weight.data_ptr(), weight_scales.data_ptr(),
+        offsets.data_ptr() if offsets is not None else 0, out.data_ptr(), M, E, N, K,
+        _row_type(out, "out")), _stream_now(dev.index)))
     return out
 
 
@@ -433,6 +443,9 @@ def silu_mul_quantize(x, *, offsets=None, out=None, out_scales=None, stream=None
     offsets[-1] rows are computed, the others left as they were."""
     _no_grad(x)
     dev = _device(x, "x")
+    if stream is not None or dev.index != _device_now():
+        with _On(dev, stream):
+            return silu_mul_quantize(x, offsets=offsets, out=out, out_scales=out_scales)
     rt = _row_type(x, "x")
     if x.dim() != 2 or x.shape[1] % 2:
         _refuse(f"x must be [M, 2 I], got {list(x.shape)}")
@@ -444,18 +457,16 @@ def silu_mul_quantize(x, *, offsets=None, out=None, out_scales=None, stream=None
             _refuse(f"offsets must be [E + 1], got {list(offsets.shape)}")
         _flat(offsets, "offsets", dev, torch.int32, offsets.shape)
         last = offsets.data_ptr() + 4 * (offsets.numel() - 1)
-    on = _On(dev, stream)
-    with on as raw:
-        if out is None:
-            out = torch.empty((M, I), dtype=torch.int8, device=dev)
-        else:
-            _flat(out, "out", dev, torch.int8, (M, I))
-        if out_scales is None:
-            out_scales = torch.empty(M, dtype=torch.float32, device=dev)
-        else:
-            _flat(out_scales, "out_scales", dev, torch.float32, (M,))
-        _check(lib.moe_ep_silu_mul_quantize(_SILU.pack(x.data_ptr(), last, out.data_ptr(), out_scales.data_ptr(),
-                                                       M, I, rt), raw))
+    if out is None:
+        out = torch.empty((M, I), dtype=torch.int8, device=dev)
+    else:
+        _flat(out, "out", dev, torch.int8, (M, I))
+    if out_scales is None:
+        out_scales = torch.empty(M, dtype=torch.float32, device=dev)
+    else:
+        _flat(out_scales, "out_scales", dev, torch.float32, (M,))
+    _check(lib.moe_ep_silu_mul_quantize(_SILU.pack(x.data_ptr(), last, out.data_ptr(), out_scales.data_ptr(),
+                                                   M, I, rt), _stream_now(dev.index)))
     return QuantizedRows(out, out_scales)
 
 
@@ -473,6 +484,10 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, *, format: str = "mxfp8
         _refuse(f"format must be one of {sorted(_NORMS)}, got {format!r}")
     code, block, row_dtype, scale_dtype = _NORMS[format]
     dev = _device(x, "x")
+    if stream is not None or dev.index != _device_now():
+        with _On(dev, stream):
+            return add_rms_norm(x, residual, weight, eps, format=format, out=out, out_scales=out_scales,
+                                residual_out=residual_out)
     rt = _row_type(x, "x")
     if x.dim() != 2:
         _refuse(f"x must be [M, H], got {list(x.shape)}")
@@ -486,22 +501,20 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, *, format: str = "mxfp8
     if block and H % block:
         _refuse(f"{format} needs a hidden size that is a multiple of {block}, got {H}")
     scale_shape = (M, H // block) if block else (M,)
-    on = _On(dev, stream)
-    with on as raw:
-        if out is None:
-            out = torch.empty((M, H), dtype=row_dtype, device=dev)
-        else:
-            _flat(out, "out", dev, row_dtype, (M, H))
-        if out_scales is None:
-            out_scales = torch.empty(scale_shape, dtype=scale_dtype, device=dev)
-        else:
-            _flat(out_scales, "out_scales", dev, scale_dtype, scale_shape)
-        if residual_out is not None:
-            _flat(residual_out, "residual_out", dev, x.dtype, (M, H))
-        elif residual is not None:
-            residual_out = torch.empty((M, H), dtype=x.dtype, device=dev)
-        _check(lib.moe_ep_add_rms_norm(_NORM.pack(
-            x.data_ptr(), residual.data_ptr() if residual is not None else 0, weight.data_ptr(),
-            residual_out.data_ptr() if residual_out is not None else 0, out.data_ptr(), out_scales.data_ptr(),
-            M, H, rt, code, eps), raw))
+    if out is None:
+        out = torch.empty((M, H), dtype=row_dtype, device=dev)
+    else:
+        _flat(out, "out", dev, row_dtype, (M, H))
+    if out_scales is None:
+        out_scales = torch.empty(scale_shape, dtype=scale_dtype, device=dev)
+    else:
+        _flat(out_scales, "out_scales", dev, scale_dtype, scale_shape)
+    if residual_out is not None:
+        _flat(residual_out, "residual_out", dev, x.dtype, (M, H))
+    elif residual is not None:
+        residual_out = torch.empty_like(x)
+    _check(lib.moe_ep_add_rms_norm(_NORM.pack(
+        x.data_ptr(), residual.data_ptr() if residual is not None else 0, weight.data_ptr(),
+        residual_out.data_ptr() if residual_out is not None else 0, out.data_ptr(), out_scales.data_ptr(),
+        M, H, rt, code, eps), _stream_now(dev.index)))
     return NormedRows(out, out_scales, x if residual_out is None else residual_out)

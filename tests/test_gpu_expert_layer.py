@@ -1,0 +1,364 @@
+"""The expert layer as it is used: between a dispatch and its combine, into
+the next layer's payload; captured into HIP graphs; on other streams; and
+with buffers past 32-bit offsets."""
+import numpy as np
+import pytest
+import torch
+
+import workloads as W
+from tests import expert_util as U
+from tests.gpu_util import log
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def X():
+    from combine_route_mask_amd import experts, moe_ep
+    assert torch.cuda.is_available() and moe_ep.moe_ep_is_supported()
+    yield experts
+    torch.cuda.empty_cache()
+
+
+def _codes(rng, *shape):
+    return torch.from_numpy(rng.integers(-127, 128, size=shape, dtype=np.int8)).cuda()
+
+
+def _scales(rng, *shape):
+    return torch.from_numpy(rng.uniform(0.5, 1.5, size=shape).astype(np.float32)).cuda() / 2000
+
+
+def _weights(rng, E, H, I):
+    return _codes(rng, E, 2 * I, H), _scales(rng, E, 2 * I), _codes(rng, E, H, I), _scales(rng, E, H)
+
+
+def _experts(X, s, w, out=None):
+    """Both products and the activation of sorted int8 rows."""
+    h = X.expert_matmul(s.rows, s.scales, w[0], w[1], offsets=s.offsets)
+    a = X.silu_mul_quantize(h, offsets=s.offsets)
+    return X.expert_matmul(a.rows, a.scales, w[2], w[3], offsets=s.offsets, out=out), h, a
+
+
+@pytest.mark.parametrize("P,T,E,k,H,I,mask", [(4, 13, 16, 4, 256, 96, None), (8, 40, 32, 3, 512, 64, 0b10111011),
+                                              (2, 300, 8, 2, 1024, 272, None), (1, 9, 4, 4, 7168, 48, None)])
+def test_layer_between_dispatch_and_combine(X, P, T, E, k, H, I, mask):
+    from combine_route_mask_amd.moe_ep import MoeEpExchange
+    log(f"layer P{P} T{T} E{E} k{k} H{H} I{I} mask {mask}")
+    rng = np.random.default_rng(P + T)
+    w = W.Workload("layer", P=P, T=T, H=H, E=E, k=k, n_lo=max(1, T // 2), n_hi=T, seed=P)
+    R = W.draw_routing(w, 7)
+    ids, wts = torch.from_numpy(R.ids).cuda(), torch.from_numpy(R.weights).cuda()
+    ids[0, 0, 0] = E + 3  # an id of no expert
+    x = torch.randn((P, T, H), device="cuda", dtype=BF)
+    weights = _weights(rng, E, H, I)
+    ex = MoeEpExchange(P, E, k, T, H)
+    recv = ex.dispatch(x, ids, wts, num_tokens=R.counts.tolist(), active_rank_mask=mask)
+    s = ex.expert_sort(recv, quantize=True)
+    live = [r for r in range(P) if mask is None or mask >> r & 1]
+    assert s.rows.shape[0] == k * sum(int(R.counts[r]) for r in live) == ex.most_pairs
+    y, h, a = _experts(X, s, weights)
+    eo = torch.full((P, P * T, H), float("nan"), dtype=BF, device="cuda")
+    X.expert_unsort(s.position, y, recv["weights"], out=eo, keep_empty=True)
+    got = ex.combine(eo)
+
+    # the same tokens with every expert on one rank, without an exchange
+    held = torch.zeros((P, T), dtype=torch.bool, device="cuda")
+    for r in live:
+        held[r, :int(R.counts[r])] = True
+    one = torch.where(held[:, :, None], ids, E)
+    for r in range(P):
+        if r not in live:  # nothing bound for a masked-off rank arrives
+            one = torch.where((one >= r * (E // P)) & (one < (r + 1) * (E // P)), E, one)
+    s1 = X.expert_sort(one.view(1, P * T, k), x.view(1, P * T, H), E, quantize=True)
+    m = int(s1.offsets[-1])
+    if mask is None:
+        # the live ranks' regions of an unmasked step hold the same pairs in the same order
+        assert torch.equal(s.counts, s1.counts) and torch.equal(s.offsets, s1.offsets)
+        assert torch.equal(s.rows[:m], s1.rows[:m]) and torch.equal(s.scales[:m], s1.scales[:m])
+    y1, _, _ = _experts(X, s1, weights)
+    if mask is None:
+        assert np.array_equal(U.bits(y[:m]), U.bits(y1[:m])), "expert outputs"
+    # each rank's sum rounds to bf16 once, their sum once more
+    ref, mag = U.unsort_reference(s1.position.cpu(), torch.where(torch.arange(len(y1), device="cuda")[:, None] < m, y1, 0),
+                                  wts.view(1, P * T, k))
+    bound = (2 * U.UBF + (k + P + 2) * U.U32) * mag * 1.01
+    sel = held.view(1, -1).cpu()
+    U.check_close(got.view(1, P * T, H)[sel.cuda()], ref[sel], bound[sel], "combined layer")
+
+    # stage by stage from what the stage before gave
+    hd = h[:m].double().cpu()
+    g, u = hd.chunk(2, 1)
+    act = g / (1 + torch.exp(-g)) * u
+    U.check_int8(a.rows[:m], a.scales[:m], act, (float(g.abs().max()) * 2 + 10) * U.U32, "activation")
+
+    # the next layer's MXFP8 payload from the combined rows
+    norm_w = torch.ones(H, dtype=BF, device="cuda")
+    n = X.add_rms_norm(got.view(P * T, H), x.view(P * T, H), norm_w, format="mxfp8")
+    ex8 = MoeEpExchange(P, E, k, T, H, dispatch_format="mxfp8")
+    recv8 = ex8.dispatch(n.rows.view(P, T, H), ids, wts, scales=n.scales.view(P, T, H // 32),
+                         num_tokens=R.counts.tolist())
+    s8 = ex8.expert_sort(recv8)
+    r, q, j = (s8.position >= 0).nonzero(as_tuple=True)
+    at = s8.position[r, q, j].long()
+    assert torch.equal(s8.rows[at], n.rows.view(torch.uint8).view(P * T, H)[q])
+    assert torch.equal(s8.scales[at], n.scales.view(torch.uint8).view(P * T, H // 32)[q])
+    with pytest.raises(ValueError):
+        ex8.expert_sort(recv8, quantize=True)
+    ex.destroy()
+    ex8.destroy()
+
+
+def _state(rng, seed, R=2, S=70, k=3, epr=4, H=256, I=96):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    ids = torch.from_numpy(U.draw_ids(np.random.default_rng(seed), R, S, k, epr)).cuda()
+    return {"ids": ids, "rows": torch.randn((R, S, H), generator=g, device="cuda", dtype=BF),
+            "w": torch.rand((R, S, k), generator=g, device="cuda"),
+            "x": torch.randn((33, H), generator=g, device="cuda", dtype=BF)}
+
+
+def _layer(X, st, weights, stream=None):
+    """Every operator once, on the given stream; all its results."""
+    s = X.expert_sort(st["ids"], st["rows"], 4, quantize=True, stream=stream)
+    c = X.expert_sort(st["ids"], st["rows"], 4, stream=stream)
+    h = X.expert_matmul(s.rows, s.scales, weights[0], weights[1], offsets=s.offsets, stream=stream)
+    a = X.silu_mul_quantize(h, offsets=s.offsets, stream=stream)
+    y = X.expert_matmul(a.rows, a.scales, weights[2], weights[3], offsets=s.offsets, stream=stream)
+    out = X.expert_unsort(s.position, y, st["w"], stream=stream)
+    gr, gw = X.expert_unsort_backward(s.position, st["rows"], y, st["w"], stream=stream)
+    gx = X.expert_sort_backward(s.position, gr, stream=stream)
+    n = X.add_rms_norm(st["x"], st["x"], weights[4], format="deepseek_fp8", stream=stream)
+    z = X.add_rms_norm(st["x"], None, weights[4], format="int8", stream=stream)
+    d = X.expert_matmul(z.rows, z.scales, weights[0][0], weights[1][0], stream=stream)
+    return [s.position, s.offsets, s.counts, c.position, out, gw, gx, n.rows, n.scales, n.residual, z.rows, z.scales, d]
+
+
+def _same(a, b):
+    return all(np.array_equal(U.bits(x), U.bits(y)) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("S", [70, 700, 3000])
+def test_layer_replays_from_captured_graphs(X, S):
+    """Two graphs of the whole layer, captured and replayed in turn with new
+    inputs in place and eager work between: each replay is the eager result
+    (the graphs' workspaces are their own)."""
+    log(f"layer graphs S{S}")
+    rng = np.random.default_rng(3)
+    weights = _weights(rng, 8, 256, 96) + (torch.ones(256, dtype=BF, device="cuda"),)
+    fresh = [_state(rng, seed, S=S) for seed in range(6)]
+    eager = [_layer(X, st, weights) for st in fresh]
+    held = [{k: v.clone() for k, v in fresh[i].items()} for i in range(2)]
+    graphs, outs = [], []
+    for st in held:
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            _layer(X, st, weights)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(_layer(X, st, weights))
+        graphs.append(g)
+    for turn in range(3):
+        for i in range(2):
+            for k, v in held[i].items():
+                v.copy_(fresh[2 * turn + i][k])
+        for g in graphs:
+            g.replay()
+        other = _layer(X, fresh[5 - turn], weights)
+        torch.cuda.synchronize()
+        assert _same(other, eager[5 - turn]), f"eager call {turn}"
+        for i in range(2):
+            assert _same(outs[i], eager[2 * turn + i]), f"graph {i}, replay {turn}"
+    del graphs
+
+
+def test_layer_on_other_streams(X):
+    """The stream argument (an object or a raw handle), two streams at a time
+    with buffers of their own, and the current stream of a with-block."""
+    rng = np.random.default_rng(4)
+    weights = _weights(rng, 8, 256, 96) + (torch.ones(256, dtype=BF, device="cuda"),)
+    sts = [_state(rng, seed, S=600) for seed in (1, 2, 3)]
+    want = [_layer(X, st, weights) for st in sts]
+    torch.cuda.synchronize()
+    a, b, c = (torch.cuda.Stream() for _ in range(3))
+    for _ in range(3):
+        got = [_layer(X, sts[0], weights, stream=a), _layer(X, sts[1], weights, stream=b.cuda_stream)]
+        with torch.cuda.stream(c):
+            got.append(_layer(X, sts[2], weights))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert _same(g, w)
+
+
+def test_gradients_on_a_captured_stream(X):
+    """Autograd through the sort and the unsort while a captured graph of the
+    same operators' gradients, made of their functional forms, is replayed."""
+    st = _state(None, 9, S=200)
+    ids, w = st["ids"], st["w"]
+    x = st["rows"].clone()
+    go = torch.randn_like(x)
+
+    def functional():
+        s = X.expert_sort(ids, x, 4)
+        gr, gw = X.expert_unsort_backward(s.position, go, s.rows, w)
+        return X.expert_sort_backward(s.position, gr), gw
+
+    def by_autograd():
+        xl, wl = x.clone().requires_grad_(), w.clone().requires_grad_()
+        s = X.expert_sort(ids, xl, 4)
+        y = X.expert_unsort(s.position, s.rows, wl)
+        return torch.autograd.grad(y, (xl, wl), go)
+
+    want = functional()
+    auto = by_autograd()
+    assert _same(want, auto)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = functional()
+    for i in range(3):
+        x.mul_(-1)
+        go.mul_(0.5)
+        eager = by_autograd()
+        g.replay()
+        torch.cuda.synchronize()
+        assert _same(got, eager), f"replay {i}"
+    del g
+
+
+def test_offsets_past_32_bits(X):
+    """More than 2^32 bytes of sorted rows, expert weights, tokens and norm rows: the last ones are right."""
+    free = torch.cuda.mem_get_info()[0]
+    if free < 80 << 30:
+        pytest.skip("needs 80 GiB of free device memory")
+    S, k, H, E = 40003, 8, 7168, 16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    ids = torch.randint(0, E, (1, S, k), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.randn((1, S, H), generator=g, device="cuda", dtype=BF)
+    s = X.expert_sort(ids, x, E)
+    order = torch.argsort(ids.view(-1), stable=True)
+    assert s.rows.numel() * 2 > 1 << 32
+    for lo in (0, S * k // 2, S * k - 5000):
+        assert torch.equal(s.rows[lo:lo + 5000], x[0][order[lo:lo + 5000] // k])
+    assert torch.equal(s.position.view(-1)[order], torch.arange(S * k, device="cuda", dtype=torch.int32))
+    w = torch.full((1, S, k), 0.125, device="cuda")  # eight equal rows, exact weights
+    assert torch.equal(X.expert_unsort(s.position, s.rows, w), x)
+    gr, gw = X.expert_unsort_backward(s.position, x, s.rows, w)
+    assert torch.equal(gr[-3000:], (x[0][order[-3000:] // k].float() * 0.125).to(BF))
+    del s, gr, gw
+    q = X.expert_sort(ids, x, E, quantize=True)
+    assert torch.equal(q.rows[-3000:].float() * q.scales[-3000:, None],
+                       (lambda t: t.rows.float() * t.scales[:, None])(
+                           X.expert_sort(torch.zeros((1, 3000, 1), dtype=torch.int32, device="cuda"),
+                                         x[:, order[-3000:] // k].contiguous(), 1, quantize=True)))
+    del q, x, order
+    # 5 GB of weights: the last expert's
+    wts = torch.randint(-127, 128, (40, 8200, 16384), generator=g, device="cuda", dtype=torch.int8)
+    xs = torch.randint(-127, 128, (700, 16384), generator=g, device="cuda", dtype=torch.int8)
+    sw = torch.rand((40, 8200), generator=g, device="cuda")
+    sx = torch.rand(700, generator=g, device="cuda")
+    for first in (690, 0):  # ten rows, and all of them
+        off = torch.zeros(41, dtype=torch.int32, device="cuda")
+        off[40] = 700
+        off[39] = first
+        off[38] = first
+        off[1:38] = first
+        got = X.expert_matmul(xs, sx, wts, sw, offsets=off, dtype=F32)[first:]
+        ref = (xs[first:].double() @ wts[39].double().t().contiguous()).cpu() * sx[first:].double().cpu()[:, None] * sw[39].double().cpu()
+        U.check_close(got, ref, 3.01 * U.U32 * ref.abs(), "last expert")
+    del wts
+    xs = torch.randint(-127, 128, (270011, 16384), generator=g, device="cuda", dtype=torch.int8)
+    sx = torch.rand(270011, generator=g, device="cuda")
+    wd = torch.randint(-127, 128, (72, 16384), generator=g, device="cuda", dtype=torch.int8)
+    got = X.expert_matmul(xs, sx, wd, sw[0, :72].contiguous(), dtype=F32)[-100:]
+    ref = (xs[-100:].double() @ wd.double().t().contiguous()).cpu() * sx[-100:].double().cpu()[:, None] * sw[0, :72].double().cpu()
+    U.check_close(got, ref, 3.01 * U.U32 * ref.abs(), "last rows")
+    del xs
+    x = torch.randn((310007, 7168), generator=g, device="cuda", dtype=BF)
+    n = X.add_rms_norm(x, None, torch.ones(7168, dtype=BF, device="cuda"), format="mxfp8")
+    m = X.add_rms_norm(x[-50:].contiguous(), None, torch.ones(7168, dtype=BF, device="cuda"), format="mxfp8")
+    assert torch.equal(n.rows[-50:].view(torch.uint8), m.rows.view(torch.uint8))
+    assert torch.equal(n.scales[-50:].view(torch.uint8), m.scales.view(torch.uint8))
+    a = X.silu_mul_quantize(x)
+    b = X.silu_mul_quantize(x[-50:].contiguous())
+    assert torch.equal(a.rows[-50:], b.rows) and torch.equal(a.scales[-50:], b.scales)
+
+
+def test_binding_refusals(X):
+    """Shapes, types, strides and gradients that the binding refuses on GPU tensors."""
+    ids = torch.zeros((2, 4, 2), dtype=torch.int32, device="cuda")
+    rows = torch.zeros((2, 4, 16), dtype=BF, device="cuda")
+    pos = torch.zeros((2, 4, 2), dtype=torch.int32, device="cuda")
+    flat = torch.zeros((16, 16), dtype=BF, device="cuda")
+    w = torch.zeros((2, 4, 2), device="cuda")
+    q, s = torch.zeros((8, 16), dtype=torch.int8, device="cuda"), torch.zeros(8, device="cuda")
+    ew, es = torch.zeros((3, 8, 16), dtype=torch.int8, device="cuda"), torch.zeros((3, 8), device="cuda")
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    wt = torch.ones(16, dtype=BF, device="cuda")
+    leaf = flat.clone().requires_grad_()
+    bad = [
+        lambda: X.expert_sort(ids.long(), rows, 4), lambda: X.expert_sort(ids[0], rows, 4),
+        lambda: X.expert_sort(ids, rows[:1], 4), lambda: X.expert_sort(ids, rows.transpose(1, 2), 4),
+        lambda: X.expert_sort(ids, rows, 0), lambda: X.expert_sort(ids, rows, 4, capacity=-1),
+        lambda: X.expert_sort(ids, rows, 4, scales=torch.zeros((2, 3, 4), device="cuda")),
+        lambda: X.expert_sort(ids, rows, 4, out=flat.float()), lambda: X.expert_sort(ids, rows, 4, out=flat[:3]),
+        lambda: X.expert_sort(ids, rows.half(), 4, quantize=True),
+        lambda: X.expert_sort(ids, rows, 4, quantize=True, scales=w),
+        lambda: X.expert_sort(ids, rows[:, :, :4], 4), lambda: X.expert_sort(ids, rows[:, :, :7].contiguous(), 4),
+        lambda: X.expert_sort(ids, rows.clone().requires_grad_(), 4, quantize=True),
+        lambda: X.expert_sort(ids, rows.clone().requires_grad_(), 4, out=flat),
+        lambda: X.expert_unsort(pos, flat.half()), lambda: X.expert_unsort(pos[0], flat),
+        lambda: X.expert_unsort(pos.long(), flat), lambda: X.expert_unsort(pos, flat, w.double()),
+        lambda: X.expert_unsort(pos, flat, w[:, :, :1]), lambda: X.expert_unsort(pos, flat, out=rows.float()),
+        lambda: X.expert_unsort(pos, flat, keep_empty=True), lambda: X.expert_unsort(pos, flat.t()),
+        lambda: X.expert_unsort(pos, leaf, out=rows), lambda: X.expert_unsort(pos, flat[:, :4].contiguous()),
+        lambda: X.expert_unsort_backward(pos, rows), lambda: X.expert_unsort_backward(pos, rows, flat.float()),
+        lambda: X.expert_unsort_backward(pos, rows, None, w, grad_rows=flat),
+        lambda: X.expert_unsort_backward(pos, rows[:1], flat),
+        lambda: X.expert_matmul(q, s, ew, es), lambda: X.expert_matmul(q, s, ew, es, offsets=off[:3]),
+        lambda: X.expert_matmul(q, s, ew[0], es[0], offsets=off), lambda: X.expert_matmul(q, s, ew[:, :, :8], es, offsets=off),
+        lambda: X.expert_matmul(q, s[:4], ew, es, offsets=off), lambda: X.expert_matmul(q.float(), s, ew, es, offsets=off),
+        lambda: X.expert_matmul(q, s, ew, es, offsets=off, dtype=torch.float16),
+        lambda: X.expert_matmul(q, s.clone().requires_grad_(), ew, es, offsets=off),
+        lambda: X.expert_matmul(q[:, :8].contiguous(), s, ew[0, :, :8].contiguous(), es[0]),
+        lambda: X.silu_mul_quantize(flat.half()), lambda: X.silu_mul_quantize(flat[:, :15].contiguous()),
+        lambda: X.silu_mul_quantize(flat), lambda: X.silu_mul_quantize(leaf),
+        lambda: X.silu_mul_quantize(flat.repeat(1, 2), offsets=off.long()),
+        lambda: X.add_rms_norm(flat, flat, wt, format="mxfp8"), lambda: X.add_rms_norm(flat, flat, wt.float(), format="int8"),
+        lambda: X.add_rms_norm(flat, flat[:3], wt, format="int8"), lambda: X.add_rms_norm(flat, None, wt, -1.0, format="int8"),
+        lambda: X.add_rms_norm(leaf, None, wt, format="int8"),
+        lambda: X.add_rms_norm(flat, None, wt, format="int8", out=flat),
+        lambda: X.add_rms_norm(flat, None, wt, format="int8", residual_out=flat.float()),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    with torch.no_grad():
+        X.silu_mul_quantize(flat.repeat(1, 2).requires_grad_())
+
+
+def test_empty_calls(X):
+    """No row, no slot, no capacity: nothing to do, and the offsets say so."""
+    ids, rows = torch.zeros((2, 0, 3), dtype=torch.int32, device="cuda"), torch.zeros((2, 0, 32), dtype=BF, device="cuda")
+    s = X.expert_sort(ids, rows, 5, quantize=True)
+    assert s.rows.shape == (0, 32) and s.offsets.tolist() == [0] * 11 and s.counts.tolist() == [0] * 10
+    w1, s1, w2, s2 = _weights(np.random.default_rng(0), 10, 32, 16)
+    y, _, a = _experts(X, s, (w1, s1, w2, s2))
+    assert y.shape == (0, 32) and a.rows.shape == (0, 16)
+    assert X.expert_unsort(s.position, y).shape == (2, 0, 32)
+    gr, gw = X.expert_unsort_backward(s.position, rows, y)
+    assert gr.shape == (0, 32) and gw.shape == (2, 0, 3)
+    n = X.add_rms_norm(y, None, torch.ones(32, dtype=BF, device="cuda"), format="mxfp8")
+    assert n.rows.shape == (0, 32) and n.scales.shape == (0, 1)
+    # slots, but none of their experts here
+    ids = torch.full((2, 5, 3), 10, dtype=torch.int32, device="cuda")
+    rows = torch.ones((2, 5, 32), dtype=BF, device="cuda")
+    s = X.expert_sort(ids, rows, 5, capacity=4)
+    assert s.offsets.tolist() == [0] * 11 and bool((s.position == -1).all())
+    assert not bool(X.expert_unsort(s.position, s.rows).any())
+    gr, gw = X.expert_unsort_backward(s.position, rows, s.rows)
+    assert not bool(gr.any()) and not bool(gw.any())
