@@ -126,79 +126,10 @@ __device__ __forceinline__ void store_element(void *p, float y)
         *static_cast<float *>(p) = y;
 }
 
-constexpr int kSkinnyWaves = 4;
-
-// One row tile and few channels: a workgroup takes 16 channels of one expert
-// and 16 rows; each of its waves takes a quarter of k, straight from memory
-// into the MFMA's registers, four steps of 64 bytes in flight, and the int32
-// sums meet in LDS.
-template <typename T>
-__global__ __launch_bounds__(kSkinnyWaves * 64) void matmul_skinny_kernel(moe_ep_matmul_args a, int ntiles)
-{
-    constexpr int W = kSkinnyWaves, U = 4;
-    __shared__ i32x4 part[W - 1][64];
-    const Tile t = find_tile<16>(a, ntiles);
-    if (t.expert < 0)
-        return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, k16 = (lane >> 4) * 16;
-    // channels and rows past the last read the last's and are not stored
-    const int8_t *wp = a.w + ((int64_t)t.expert * a.n + min(t.n * 16 + l16, a.n - 1)) * a.k + k16;
-    const int8_t *xp = a.x + min(t.first + l16, t.last - 1) * a.k + k16;
-    i32x4 acc = {0, 0, 0, 0};
-    const int steps = (a.k + 63) / 64, share = (steps + W - 1) / W;
-    const int lo = wave * share, hi = min(steps, lo + share);
-    for (int s0 = lo; s0 < hi; s0 += U) {
-        i32x4 wv[U], xv[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = (s0 + u) * 64;
-            wv[u] = xv[u] = i32x4{0, 0, 0, 0};
-            if (s0 + u < hi && k + k16 < a.k) { // zeros past the end add nothing
-                wv[u] = __builtin_nontemporal_load(reinterpret_cast<const i32x4 *>(wp + k));
-                xv[u] = *reinterpret_cast<const i32x4 *>(xp + k);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u], xv[u], acc, 0, 0, 0);
-    }
-    if (wave)
-        part[wave - 1][lane] = acc;
-    __syncthreads();
-    const int64_t m = t.first + l16;
-    if (wave || m >= t.last)
-        return;
-#pragma unroll
-    for (int w = 0; w < W - 1; ++w)
-        acc += part[w][lane];
-    const float *scales = a.w_scales + (int64_t)t.expert * a.n;
-    const float sx = a.x_scales[m];
-    const int n = t.n * 16 + (lane >> 4) * 4;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (n + e < a.n)
-            store_element<T>(static_cast<uint8_t *>(a.out) + (m * a.n + n + e) * RowType<T>::kBytes,
-                             (float)acc[e] * (sx * scales[n + e]));
-}
-
-hipError_t skinny_launch(const moe_ep_matmul_args &a, hipStream_t s)
-{
-    const int64_t ntiles = (a.n + 15) / 16;
-    dim3 grid;
-    if (!tile_grid(most_tiles(a, 16) * ntiles, kSkinnyWaves * 64, grid))
-        return hipErrorInvalidValue;
-    const dim3 block(kSkinnyWaves * 64);
-    if (a.out_type == MOE_EP_BF16_ROWS)
-        hipLaunchKernelGGL(matmul_skinny_kernel<Bf16>, grid, block, 0, s, a, (int)ntiles);
-    else
-        hipLaunchKernelGGL(matmul_skinny_kernel<Fp32>, grid, block, 0, s, a, (int)ntiles);
-    return hipGetLastError();
-}
-
-// Many rows an expert: the matrix cores bound the call.  A workgroup takes
-// BN channels and BM rows, 128 bytes of k at a time, through STAGES of LDS:
-// the next stages' rows go from memory straight into LDS while this one's
-// are multiplied.  NW x MW waves, each FN x FM results of 16 x 16.
+// A workgroup takes BN channels and BM rows, 128 bytes of k at a time,
+// through STAGES of LDS: the next stages' rows go from memory straight into
+// LDS while this one's are multiplied.  NW x MW waves, each FN x FM results of
+// 16 x 16.
 constexpr int kTileK = 128;
 
 template <int NW_, int MW_, int FN_, int FM_, int STAGES_>
@@ -211,7 +142,9 @@ struct TileShape {
 
 // 16 bytes a lane from base + offset + k into LDS: lane l's to `to` + 16 l.
 // (The buffer form: a global load into LDS makes every later LDS wait wait
-// for all reads.)
+// for all reads.)  An offset from kPastEnd on is beyond the buffer: zeros.
+constexpr uint32_t kPastEnd = 0x80000000u;
+
 __device__ __forceinline__ void load_lds(const int8_t *base, uint32_t offset, int k, uint8_t *to)
 {
 #if defined(__HIP_DEVICE_COMPILE__) // the host compiler does not know the resource type
@@ -260,12 +193,12 @@ __device__ __forceinline__ void read_w(const uint8_t *stage, const Operands<S> &
 }
 
 template <typename S>
-__device__ __forceinline__ void load_part(uint8_t *stage, const Operands<S> &o, int i, int k)
+__device__ __forceinline__ void load_part(uint8_t *stage, const Operands<S> &o, int i, int k, uint32_t past)
 {
     if (i < S::LN)
-        load_lds(o.wp, o.wo[i], k, stage + (i * S::W + o.wave) * 1024);
+        load_lds(o.wp, o.wo[i] | past, k, stage + (i * S::W + o.wave) * 1024);
     else
-        load_lds(o.xp, o.xo[i - S::LN], k, stage + S::BN * kTileK + ((i - S::LN) * S::W + o.wave) * 1024);
+        load_lds(o.xp, o.xo[i - S::LN] | past, k, stage + S::BN * kTileK + ((i - S::LN) * S::W + o.wave) * 1024);
 }
 
 constexpr int kAhead = 2; // weight fragments are read this many products before they are used
@@ -279,8 +212,8 @@ constexpr int kAhead = 2; // weight fragments are read this many products before
 // another; wait_barrier() does, for those that have to have arrived.
 template <typename S, typename ACC>
 __device__ __forceinline__ void tile_step(const uint8_t *__restrict__ cur, const uint8_t *__restrict__ next,
-                                          uint8_t *__restrict__ fill, int k, const Operands<S> &o, Fragments<S> &f,
-                                          ACC &acc, Fragments<S> &g)
+                                          uint8_t *__restrict__ fill, int k, uint32_t past, const Operands<S> &o,
+                                          Fragments<S> &f, ACC &acc, Fragments<S> &g)
 {
     constexpr int G = 2 * S::FN, L = S::LN + S::LM, PER = (2 * L + G - 1) / G, FIRST = S::FN - S::FM - kAhead + 1;
 #pragma unroll
@@ -288,7 +221,7 @@ __device__ __forceinline__ void tile_step(const uint8_t *__restrict__ cur, const
 #pragma unroll
         for (int u = PER * i; u < PER * i + PER; ++u)
             if (u < L)
-                load_part<S>(fill, o, u, k);
+                load_part<S>(fill, o, u, k, past);
         if (i + kAhead < G)
             read_w<S>(cur, o, f, i + kAhead);
 #pragma unroll
@@ -356,73 +289,40 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
     }
     i32x4 acc[FN][FM] = {};
     Fragments<S> f, g;
-    const int whole = a.k / kTileK;
-    uint8_t *cur = lds;
-    if (whole) {
-        // k starts elsewhere in each channel tile and goes round: rows a
-        // power of two apart would otherwise have all workgroups read the
-        // same few memory channels at a time (64 rows, 32 experts, N = K =
-        // 4096: 106 us all from k = 0, 79 us)
-        const int start = (int)((uint32_t)(t.expert * ((a.n + S::BN - 1) / S::BN) + t.n) % (uint32_t)whole);
-        constexpr int L = S::LN + S::LM;
+    const int steps = (a.k + kTileK - 1) / kTileK;
+    // of the last step, a lane's chunk past the end of k is zeros
+    const uint32_t end = (steps - 1) * kTileK + chunk < (uint32_t)a.k ? 0 : kPastEnd;
+    // k starts elsewhere in each channel tile and goes round: rows a power of
+    // two apart would otherwise have all workgroups read the same few memory
+    // channels at a time (64 rows, 32 experts, N = K = 4096: 106 us all from
+    // k = 0, 79 us)
+    const int start = (int)((uint32_t)(t.expert * ((a.n + S::BN - 1) / S::BN) + t.n) % (uint32_t)steps);
+    constexpr int L = S::LN + S::LM;
 #pragma unroll
-        for (int st = 0; st < S::STAGES - 1; ++st)
+    for (int st = 0; st < S::STAGES - 1; ++st) {
+        const int at = (start + st) % steps;
 #pragma unroll
-            for (int i = 0; i < L; ++i)
-                load_part<S>(lds + st * S::BYTES, o, i, (start + st) % whole * kTileK);
-        wait_barrier<(S::STAGES - 2) * L>();
-#pragma unroll
-        for (int j = 0; j < FM; ++j)
-            read_x<S>(cur, o, f, 0, j);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            read_w<S>(cur, o, f, i);
-        uint8_t *next = lds + S::BYTES, *fill = lds + (S::STAGES - 1) * S::BYTES;
-        int at = (start + S::STAGES - 1) % whole;
-        // the loads behind the last whole step are not read
-        for (int i = 0; i < whole; ++i) {
-            tile_step<S>(cur, next, fill, at * kTileK, o, f, acc, g);
-            at = at + 1 == whole ? 0 : at + 1;
-            fill = cur;
-            cur = next;
-            next = next == lds + (S::STAGES - 1) * S::BYTES ? lds : next + S::BYTES;
-        }
-        wait_barrier<0>(); // nothing is on its way into LDS
+        for (int i = 0; i < L; ++i)
+            load_part<S>(lds + st * S::BYTES, o, i, at * kTileK, at == steps - 1 ? end : 0);
     }
-    if (whole * kTileK < a.k) {
-        // the rest of k, through registers, zeros past its end
-        const int k = whole * kTileK;
-        const bool in = k + (int)chunk < a.k;
-        uint8_t *put = lds + lane * 16;
+    wait_barrier<(S::STAGES - 2) * L>();
+    uint8_t *cur = lds, *next = lds + S::BYTES, *fill = lds + (S::STAGES - 1) * S::BYTES;
 #pragma unroll
-        for (int i = 0; i < S::LN; ++i) {
-            i32x4 v = {0, 0, 0, 0};
-            if (in)
-                v = *reinterpret_cast<const i32x4 *>(o.wp + k + o.wo[i]);
-            *reinterpret_cast<i32x4 *>(put + (i * S::W + o.wave) * 1024) = v;
-        }
+    for (int j = 0; j < FM; ++j)
+        read_x<S>(cur, o, f, 0, j);
 #pragma unroll
-        for (int i = 0; i < S::LM; ++i) {
-            i32x4 v = {0, 0, 0, 0};
-            if (in)
-                v = *reinterpret_cast<const i32x4 *>(o.xp + k + o.xo[i]);
-            *reinterpret_cast<i32x4 *>(put + S::BN * kTileK + (i * S::W + o.wave) * 1024) = v;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int j = 0; j < FM; ++j)
-                read_x<S>(lds, o, f, h, j);
-#pragma unroll
-            for (int i = 0; i < FN; ++i) {
-                read_w<S>(lds, o, f, h * FN + i);
-#pragma unroll
-                for (int j = 0; j < FM; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w[h * FN + i], f.x[h][j], acc[i][j], 0, 0, 0);
-            }
-        }
+    for (int i = 0; i < kAhead; ++i)
+        read_w<S>(cur, o, f, i);
+    int at = (start + S::STAGES - 1) % steps;
+    // the loads behind the last step are not read
+    for (int i = 0; i < steps; ++i) {
+        tile_step<S>(cur, next, fill, at * kTileK, at == steps - 1 ? end : 0, o, f, acc, g);
+        at = at + 1 == steps ? 0 : at + 1;
+        fill = cur;
+        cur = next;
+        next = next == lds + (S::STAGES - 1) * S::BYTES ? lds : next + S::BYTES;
     }
+    wait_barrier<0>(); // nothing is on its way into LDS
     // Rows of any n start at any element: 16-byte stores need no more than an
     // element's alignment.
     constexpr int V = RowType<T>::kPer / 4; // results of 4 channels in a 16-byte store
@@ -531,23 +431,19 @@ hipError_t tile_launch(const moe_ep_matmul_args &a, hipStream_t s)
 //    256 rows 258 / 240, and k = 1024 (E 32, N 2048, 1024 rows) 147 / 114;
 //  - 128 x 128 (four waves, two workgroups a CU): E 32, 4096 x 4096, 96 rows
 //    142, with 64 x 64 157;
-//  - 64 x 64 (four waves, three workgroups a CU, three stages) keeps the most
-//    loads in flight, for few rows, where the weights' bytes count, and for
-//    few tiles: E 8, 4096 x 7168, 32 rows 38, with 128 x 128 42; E 1,
-//    2048 x 2048, 512 rows 9.8 / 14.9 (a short k ends before the stages fill:
-//    E 8, 7168 x 2048, 16 rows 24.4 / 21.7, but E 32, 4 rows 91 / 98);
-//  - one row tile of 16 and too few channel tiles even for that: workgroups
-//    of 16 channels that split k, E 1, 7168 x 7168, 1 row 14.0 / 19.1.
+//  - 64 x 64 (four waves, three workgroups a CU, three stages; four for up to
+//    32 rows) keeps the most loads in flight, for few rows, where the weights'
+//    bytes count, and for few tiles: E 8, 4096 x 7168, 32 rows 38, with
+//    128 x 128 42; E 1, 2048 x 2048, 512 rows 9.8 / 14.9; E 1, 7168 x 7168,
+//    1 row 14.0 (19.1 with three stages).
 hipError_t launch_expert_matmul(const moe_ep_matmul_args &a, hipStream_t s)
 {
     const int64_t average = (a.num_rows + a.num_experts - 1) / a.num_experts;
     const auto tiles = [&](int64_t size) {
         return a.num_experts * ((average + size - 1) / size) * ((a.n + size - 1) / size);
     };
-    if (average <= 16 && tiles(64) < 256)
-        return skinny_launch(a, s);
     if (average <= 48 || tiles(128) <= 256)
-        return tile_launch<TileShape<2, 2, 2, 2, 3>>(a, s);
+        return tile_launch<TileShape<2, 2, 2, 1, 4>, TileShape<2, 2, 2, 2, 3>>(a, s);
     if (a.k < 4096 || average < 512 || tiles(256) < 512)
         return tile_launch<TileShape<2, 2, 4, 2, 2>, TileShape<2, 2, 4, 4, 2>>(a, s);
     return tile_launch<TileShape<4, 2, 4, 2, 2>, TileShape<4, 2, 4, 4, 2>, TileShape<2, 4, 8, 4, 2>>(a, s);
