@@ -48,11 +48,15 @@ __device__ __forceinline__ void expert_rows(const moe_ep_matmul_args &a, int e, 
     }
 }
 
+constexpr int kBand = 4;
+
 // The workgroup's tile: up to BM rows of one expert and one of its `ntiles`
 // channel tiles, found by each wave from the offsets (the host does not know
-// them).  Tiles are numbered by expert, channel tile, row tile, so that
-// neighbours share their weights, and each of the eight XCDs (workgroup
-// number modulo 8) takes a run of them, so that the sharing is in one L2.
+// them).  Tiles are numbered by expert, band of kBand row tiles, channel
+// tile, row tile, and each of the eight XCDs (workgroup number modulo 8) takes
+// a run of them: the tiles that run at a time on its 32 CUs are 4 x 8, which
+// read the least through its L2 (8192 x 8192 x 8192: 444 us; in columns of all
+// row tiles 512 us, bands of 6 and 8 456).
 template <int BM>
 __device__ __forceinline__ Tile find_tile(const moe_ep_matmul_args &a, int ntiles)
 {
@@ -90,11 +94,14 @@ __device__ __forceinline__ Tile find_tile(const moe_ep_matmul_args &a, int ntile
         l = __builtin_ctzll(hit);
     }
     const int tiles = __builtin_amdgcn_readlane(n, l), here = at - __builtin_amdgcn_readlane(start, l);
-    t.n = here / tiles;
+    const int band = here / (kBand * ntiles), height = min(kBand, tiles - band * kBand), in = here - band * kBand * ntiles;
+    if (height < 1)
+        return t;
+    t.n = in / height;
     if (t.n >= ntiles)
         return t;
     t.expert = base + l;
-    t.first = (int64_t)__builtin_amdgcn_readlane(lo, l) + (int64_t)(here % tiles) * BM;
+    t.first = (int64_t)__builtin_amdgcn_readlane(lo, l) + (int64_t)(band * kBand + in % height) * BM;
     t.last = min((int64_t)__builtin_amdgcn_readlane(hi, l), t.first + BM);
     return t;
 }
@@ -206,22 +213,19 @@ constexpr int kAhead = 2; // weight fragments are read this many products before
 // The products of stage `cur`, groups of FM.  The first kAhead fragments are
 // in registers already; the last groups run behind the barrier and read the
 // first of `next`, so that neither LDS nor the barrier leaves the matrix
-// cores idle for long.  `fill` (the stage read last, or `next` where there
-// are two) takes the loads for STAGES - 1 steps on.  The stages are distinct
-// objects to the compiler, so that a read of one does not wait for loads into
-// another; wait_barrier() does, for those that have to have arrived.
+// cores idle for long.  Behind it `fill`, which is `cur`, takes the loads for
+// STAGES steps on: they have at least a whole step to arrive.  The stages are
+// distinct objects to the compiler, so that a read of one does not wait for
+// loads into another; wait_barrier() does, for those that have to have
+// arrived.
 template <typename S, typename ACC>
 __device__ __forceinline__ void tile_step(const uint8_t *__restrict__ cur, const uint8_t *__restrict__ next,
                                           uint8_t *__restrict__ fill, int k, uint32_t past, const Operands<S> &o,
                                           Fragments<S> &f, ACC &acc, Fragments<S> &g)
 {
-    constexpr int G = 2 * S::FN, L = S::LN + S::LM, PER = (2 * L + G - 1) / G, FIRST = S::FN - S::FM - kAhead + 1;
+    constexpr int G = 2 * S::FN, L = S::LN + S::LM, FIRST = S::FN - S::FM - kAhead + 1;
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-#pragma unroll
-        for (int u = PER * i; u < PER * i + PER; ++u)
-            if (u < L)
-                load_part<S>(fill, o, u, k, past);
         if (i + kAhead < G)
             read_w<S>(cur, o, f, i + kAhead);
 #pragma unroll
@@ -237,6 +241,10 @@ __device__ __forceinline__ void tile_step(const uint8_t *__restrict__ cur, const
             for (int j = 0; j < S::FM; ++j)
                 if (j % kAhead == i - (G - kAhead))
                     read_x<S>(next, o, g, 0, j);
+#pragma unroll
+            for (int u = 0; u < L; ++u)
+                if (u * kAhead / L == i - (G - kAhead))
+                    load_part<S>(fill, o, u, k, past);
         }
 #pragma unroll
         for (int j = 0; j < S::FM; ++j)
@@ -287,6 +295,10 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
         o.wat[h] = place + wn * kTileK;
         o.xat[h] = place + (S::BN + wm) * kTileK;
     }
+    float sx[FM];
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+        sx[j] = a.x_scales[min(t.first + wm + 16 * j + l16, t.last - 1)];
     i32x4 acc[FN][FM] = {};
     Fragments<S> f, g;
     const int steps = (a.k + kTileK - 1) / kTileK;
@@ -299,26 +311,25 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
     const int start = (int)((uint32_t)(t.expert * ((a.n + S::BN - 1) / S::BN) + t.n) % (uint32_t)steps);
     constexpr int L = S::LN + S::LM;
 #pragma unroll
-    for (int st = 0; st < S::STAGES - 1; ++st) {
+    for (int st = 0; st < S::STAGES; ++st) {
         const int at = (start + st) % steps;
 #pragma unroll
         for (int i = 0; i < L; ++i)
             load_part<S>(lds + st * S::BYTES, o, i, at * kTileK, at == steps - 1 ? end : 0);
     }
-    wait_barrier<(S::STAGES - 2) * L>();
-    uint8_t *cur = lds, *next = lds + S::BYTES, *fill = lds + (S::STAGES - 1) * S::BYTES;
+    wait_barrier<(S::STAGES - 1) * L>();
+    uint8_t *cur = lds, *next = lds + S::BYTES;
 #pragma unroll
     for (int j = 0; j < FM; ++j)
         read_x<S>(cur, o, f, 0, j);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
         read_w<S>(cur, o, f, i);
-    int at = (start + S::STAGES - 1) % steps;
+    int at = (start + S::STAGES) % steps;
     // the loads behind the last step are not read
     for (int i = 0; i < steps; ++i) {
-        tile_step<S>(cur, next, fill, at * kTileK, at == steps - 1 ? end : 0, o, f, acc, g);
+        tile_step<S>(cur, next, cur, at * kTileK, at == steps - 1 ? end : 0, o, f, acc, g);
         at = at + 1 == steps ? 0 : at + 1;
-        fill = cur;
         cur = next;
         next = next == lds + (S::STAGES - 1) * S::BYTES ? lds : next + S::BYTES;
     }
@@ -327,46 +338,39 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
     // element's alignment.
     constexpr int V = RowType<T>::kPer / 4; // results of 4 channels in a 16-byte store
     const float *scales = a.w_scales + (int64_t)t.expert * a.n;
-    float sx[FM];
+    const int nw = n0 + wn + 4 * FN * l4; // the lane's first channel
+    f32x4 sw[FN];
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+        const int n = nw + 4 * i;
+        if (n + 4 <= a.n) {
+            sw[i] = *reinterpret_cast<const f32x4 *>(scales + n);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sw[i][e] = n + e < a.n ? scales[n + e] : 0.0f;
+        }
+    }
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
         const int64_t m = t.first + wm + 16 * j + l16;
-        sx[j] = m < t.last ? a.x_scales[m] : 0.0f;
-    }
+        if (m >= t.last)
+            continue;
+        uint8_t *out = static_cast<uint8_t *>(a.out) + (m * a.n + nw) * RowType<T>::kBytes;
 #pragma unroll
-    for (int i = 0; i < FN; i += V) {
-        const int n = n0 + wn + 4 * FN * l4 + 4 * i;
-        const bool all = n + 4 * V <= a.n;
-        float sw[4 * V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            f32x4 four = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (all)
-                four = *reinterpret_cast<const f32x4 *>(scales + n + 4 * v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                sw[4 * v + e] = four[e];
-                if (!all && n + 4 * v + e < a.n)
-                    sw[4 * v + e] = scales[n + 4 * v + e];
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < FM; ++j) {
-            const int64_t m = t.first + wm + 16 * j + l16;
-            if (m >= t.last)
-                continue;
+        for (int i = 0; i < FN; i += V) {
+            const int n = nw + 4 * i;
             float y[4 * V];
 #pragma unroll
             for (int e = 0; e < 4 * V; ++e)
-                y[e] = (float)acc[i + e / 4][j][e % 4] * (sx[j] * sw[e]);
-            uint8_t *out = static_cast<uint8_t *>(a.out) + (m * a.n + n) * RowType<T>::kBytes;
-            if (all) {
-                *reinterpret_cast<AnyAligned *>(out) = RowType<T>::pack(y);
+                y[e] = (float)acc[i + e / 4][j][e % 4] * (sx[j] * sw[i + e / 4][e % 4]);
+            if (n + 4 * V <= a.n) {
+                *reinterpret_cast<AnyAligned *>(out + 4 * i * RowType<T>::kBytes) = RowType<T>::pack(y);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4 * V; ++e)
                     if (n + e < a.n)
-                        store_element<T>(out + e * RowType<T>::kBytes, y[e]);
+                        store_element<T>(out + (4 * i + e) * RowType<T>::kBytes, y[e]);
             }
         }
     }

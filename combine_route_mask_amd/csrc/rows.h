@@ -27,12 +27,18 @@ struct RowType<Bf16> {
         for (int i = 0; i < 4; ++i)
             unpack_bf16x2(v[i], f[2 * i], f[2 * i + 1]);
     }
+    // gfx950 rounds two floats to bf16 (to nearest even) in one instruction;
+    // NaN stays NaN.
     static __device__ __forceinline__ u32x4 pack(const float *f)
     {
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
         u32x4 v;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+        for (int i = 0; i < 4; ++i) {
+            const f32x2 two = {f[2 * i], f[2 * i + 1]};
+            v[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(two, bf16x2));
+        }
         return v;
     }
 };

@@ -145,6 +145,27 @@ UNSORTS = [(1, 1, 8, 7168), (1, 1, 1, 8), (8, 16, 4, 136), (1, 1000, 8, 72), (64
            (1, 33, 3, 16392), (16, 64, 2, 8)]
 
 
+def test_unsort_rounds_every_bf16_back_to_itself(X):
+    """One row a slot without weights: every finite bf16 value, subnormals
+    among them, comes back (-0 as the sum +0 + -0 = +0), NaN and infinities
+    as themselves."""
+    v = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(BF).view(1, 8, 8192).cuda()
+    p = torch.arange(8, dtype=torch.int32, device="cuda").view(1, 8, 1)
+    got = X.expert_unsort(p, v[0])
+    nan = v.isnan()
+    assert torch.equal(got.isnan(), nan)
+    assert torch.equal(got[~nan].view(torch.int16), (v[~nan] + 0.0).view(torch.int16))
+    # halves between neighbours round to even: 2^-9 (1 + m / 128) twice of its half step
+    x = torch.tensor([1 + 2 * i / 256 + (2 ** -9 if i % 2 else -2 ** -9) for i in range(8)], dtype=F32)
+    rows = torch.stack([x, torch.full((8,), 2.0 ** -9)]).cuda()
+    p = torch.tensor([[[0, 1]]], dtype=torch.int32, device="cuda")
+    assert torch.equal(X.expert_unsort(p, rows).cpu()[0, 0], x + 2.0 ** -9)
+    half = torch.tensor([[1.0 + i / 128 for i in range(8)], [2.0 ** -8] * 8], dtype=BF).cuda()
+    ref = (half[0].double() + half[1].double()).cpu()
+    even = torch.where((torch.arange(8) % 2) == 0, half[0].double().cpu(), ref + 2.0 ** -8)
+    assert torch.equal(X.expert_unsort(p, half).double().cpu()[0, 0], even)
+
+
 def _positions(rng, R, S, k, full=False):
     """Places of a random share of the pairs, in random order, and the number of rows (more than the places)."""
     here = np.ones((R, S, k), bool) if full else rng.random((R, S, k)) < 0.6
