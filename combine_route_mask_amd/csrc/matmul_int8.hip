@@ -426,31 +426,40 @@ hipError_t tile_launch(const moe_ep_matmul_args &a, hipStream_t s)
 
 } // namespace
 
-// The shape follows from the average rows of an expert and from how many
-// tiles there are for 256 CUs (times in us, E experts of N x K):
-//  - 256 x 256 (eight waves, one workgroup a CU) reads the least for its
-//    products, 32 bytes a clock and CU at full rate, and wins where there are
-//    two rounds of it and k is long enough for its first and last step:
-//    E 32, 4096 x 4096, 512 rows: 352 against 374 with 128 x 128; but
-//    256 rows 258 / 240, and k = 1024 (E 32, N 2048, 1024 rows) 147 / 114;
-//  - 128 x 128 (four waves, two workgroups a CU): E 32, 4096 x 4096, 96 rows
-//    142, with 64 x 64 157;
-//  - 64 x 64 (four waves, three workgroups a CU, three stages; four for up to
-//    32 rows) keeps the most loads in flight, for few rows, where the weights'
-//    bytes count, and for few tiles: E 8, 4096 x 7168, 32 rows 38, with
-//    128 x 128 42; E 1, 2048 x 2048, 512 rows 9.8 / 14.9; E 1, 7168 x 7168,
-//    1 row 14.0 (19.1 with three stages).
+// The shape follows from the average rows of an expert (of num_rows, which a
+// caller's capacity may exceed) and from how many tiles there are for 256 CUs.
+// Times in us, E experts of N x K, ragged rows:
+//  - up to 256 x 256, eight waves, one workgroup a CU: the fewest bytes for
+//    its products; wins over 128 x 128 from about 112 rows on where there are
+//    tiles for the CUs and k is long enough for its first and last step.
+//    E 32, 4096 x 4096: 128 rows 135 / 153, 256 rows 231 / 227, 512 rows
+//    312 / 367; E 32, 2048 x 4096, 192 rows 72 / 87; E 1, 7168 x 7168, 1024
+//    rows (112 tiles) 82 / 56.  With k = 2048 only while an expert fits one
+//    tile: E 8, 7168 x 2048, 128 rows 30 / 38, 512 rows 99 / 77; never with
+//    k = 1024 (E 32, N 4096, 1024 rows 245 / 228);
+//  - up to 128 x 128, four waves, two workgroups a CU; for at most 32 rows an
+//    expert its 64-row shape with three stages in place of two: E 32,
+//    4096 x 4096, 1 row 68 / 79, but 64 rows 124 / 110;
+//  - up to 64 x 64, four waves, three workgroups a CU, three stages, or four
+//    for up to 32 rows: where 128 x 128 has not 200 tiles.  E 1, 4096 x 4096,
+//    256 rows 11 / 19; E 1, 7168 x 7168, 1 row 13 / 32.
 hipError_t launch_expert_matmul(const moe_ep_matmul_args &a, hipStream_t s)
 {
+    using T64 = TileShape<2, 2, 2, 2, 3>;
+    using T64Few = TileShape<2, 2, 2, 1, 4>;
+    using T128 = TileShape<2, 2, 4, 4, 2>;
     const int64_t average = (a.num_rows + a.num_experts - 1) / a.num_experts;
     const auto tiles = [&](int64_t size) {
         return a.num_experts * ((average + size - 1) / size) * ((a.n + size - 1) / size);
     };
-    if (average <= 48 || tiles(128) <= 256)
-        return tile_launch<TileShape<2, 2, 2, 1, 4>, TileShape<2, 2, 2, 2, 3>>(a, s);
-    if (a.k < 4096 || average < 512 || tiles(256) < 512)
-        return tile_launch<TileShape<2, 2, 4, 2, 2>, TileShape<2, 2, 4, 4, 2>>(a, s);
-    return tile_launch<TileShape<4, 2, 4, 2, 2>, TileShape<4, 2, 4, 4, 2>, TileShape<2, 4, 8, 4, 2>>(a, s);
+    if (tiles(128) < 200)
+        return tile_launch<T64Few, T64>(a, s);
+    if (average <= 32)
+        return tile_launch<TileShape<2, 2, 4, 2, 3>, T128>(a, s);
+    if (average >= 112 && tiles(256) >= 200 && (a.k >= 4096 || (a.k >= 1536 && average < 224)))
+        return tile_launch<TileShape<4, 2, 4, 2, 2>, TileShape<4, 2, 4, 4, 2>, TileShape<2, 4, 8, 3, 2>,
+                           TileShape<2, 4, 8, 4, 2>>(a, s);
+    return tile_launch<TileShape<2, 2, 4, 2, 2>, T128>(a, s);
 }
 
 } // namespace moe_ep

@@ -69,7 +69,8 @@ CASES = [
     (2048, 8, 512, 1024, "even"), (2300, 8, 515, 1040, "ragged"), (5000, 2, 258, 16, "ragged"),
     (5000, 7, 300, 112, "ragged"), (4096, 16, 1024, 512, "ragged"), (1500, 4096, 8, 32, "ragged"),
     (16, 1, 1024, 131056, "even"), (520, 1, 264, 16384, "even"), (2048, 8, 2055, 1040, "ragged"),
-    (2100, 4, 16400, 4112, "ragged"),
+    (2100, 4, 16400, 4112, "ragged"), (600, 40, 700, 1040, "ragged"), (3100, 12, 4400, 1552, "ragged"),
+    (2600, 20, 1290, 4224, "ragged"),
 ]
 
 
