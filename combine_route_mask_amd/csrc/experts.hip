@@ -837,7 +837,7 @@ hipError_t launch_expert_sort(const moe_ep_sort_args &a, hipStream_t s)
         a.quantize ? 1 : (uint32_t)((nvec + kGatherBlock * kGatherVectors - 1) / (kGatherBlock * kGatherVectors));
     const int64_t items = groups * nchunk;
     if (items > INT32_MAX)
-        return hipErrorInvalidValue;
+        return hipErrorInvalidConfiguration;
     dim3 grid = grid_of(items);
     grid.x += planned;
     const dim3 block(kGatherBlock);
@@ -872,7 +872,7 @@ hipError_t unsort_launch(const moe_ep_unsort_args &a, hipStream_t s, int g)
     const uint32_t nchunk = (uint32_t)((nvec + kUnsortBlock * VPT - 1) / (kUnsortBlock * VPT));
     const int64_t items = (nslots + g - 1) / g * nchunk;
     if (items > INT32_MAX)
-        return hipErrorInvalidValue;
+        return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((unsort_kernel<T, WEIGHTS, VPT, G>), grid_of(items), dim3(kUnsortBlock), 0, s, a, g, nchunk,
                        (uint32_t)items);
     return hipGetLastError();

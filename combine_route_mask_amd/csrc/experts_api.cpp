@@ -32,6 +32,8 @@ int guarded(F f)
 
 int launched(hipError_t e, const char *what)
 {
+    if (e == hipErrorInvalidConfiguration) // the launchers' own limit
+        return fail(MOE_EP_ERR_CAPACITY, std::string(what) + " needs more workgroups than a launch holds");
     if (e != hipSuccess)
         return fail(MOE_EP_ERR_HIP, std::string(what) + " launch failed: " + hipGetErrorString(e));
     return ok();

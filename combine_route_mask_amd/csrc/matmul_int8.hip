@@ -415,7 +415,7 @@ hipError_t tile_launch(const moe_ep_matmul_args &a, hipStream_t s)
     const int64_t ntiles = (a.n + S::BN - 1) / S::BN;
     dim3 grid;
     if (!tile_grid(most_tiles(a, largest(S::BM, MORE::BM...)) * ntiles, S::THREADS, grid))
-        return hipErrorInvalidValue;
+        return hipErrorInvalidConfiguration;
     const dim3 block(S::THREADS);
     if (a.out_type == MOE_EP_BF16_ROWS)
         hipLaunchKernelGGL((matmul_tile_kernel<Bf16, S, MORE...>), grid, block, 0, s, a, (int)ntiles);

@@ -172,19 +172,20 @@ def expert_sort(ids, rows, experts_per_rank: int, *, scales=None, capacity: Opti
                 quantize: bool = False, out=None, out_scales=None, stream=None) -> SortedRows:
     """Rows to expert order.  ``ids`` int32 [R, S, k], ``rows`` [R, S, row]
     of any dtype and ``scales`` [R, S, scale row] or None, as a dispatch
-    leaves them (R = 1: a batch of tokens).  A pair (slot, j) counts when its
+    leaves them (R = 1: a batch of tokens); ranks may lie apart.  A pair (slot, j) counts when its
     id is one of its rank's ``experts_per_rank`` experts; counted pairs are
     placed by ascending (id, slot, j), those from place ``capacity`` on (by
     default R*S*k) are dropped.  Rows behind the last pair are left as they
     were, in ``out`` or uninitialised.  ``quantize``: bf16 or fp32 rows become
     int8 codes with scales = amax / 127.
 
-    Differentiable in ``rows`` (bf16 or fp32, neither ``quantize`` nor
-    ``out``); the rows behind the last pair are then zeros."""
+    Differentiable in ``rows`` (bf16 or fp32; not with ``quantize``, ``out``
+    or ``stream``: autograd orders its work by the current stream); the rows
+    behind the last pair are then zeros."""
     if rows.requires_grad and torch.is_grad_enabled():
-        _need(not quantize and out is None and rows.dtype in _ROW_TYPES,
-              "only a sort of bf16 or fp32 rows into a new tensor has a gradient")
-        r, sc, p, o, c = _SortFunction.apply(rows, ids, experts_per_rank, scales, capacity, out_scales, stream)
+        _need(not quantize and out is None and stream is None and rows.dtype in _ROW_TYPES,
+              "only a sort of bf16 or fp32 rows into a new tensor, on the current stream, has a gradient")
+        r, sc, p, o, c = _SortFunction.apply(rows, ids, experts_per_rank, scales, capacity, out_scales)
         return SortedRows(r, sc, p, o, c)
     return _sort(ids, rows, experts_per_rank, scales, capacity, quantize, out, out_scales, stream)
 
@@ -251,10 +252,9 @@ def expert_sort_backward(position, grad_rows, *, out=None, stream=None):
 
 class _SortFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, rows, ids, epr, scales, capacity, out_scales, stream):
-        s = _sort(ids, rows, epr, scales, capacity, False, None, out_scales, stream, zeros=True)
+    def forward(ctx, rows, ids, epr, scales, capacity, out_scales):
+        s = _sort(ids, rows, epr, scales, capacity, False, None, out_scales, None, zeros=True)
         ctx.save_for_backward(s.position)
-        ctx.stream = stream
         ctx.mark_non_differentiable(*(t for t in s[1:] if t is not None))
         ctx.set_materialize_grads(False)
         return tuple(s)
@@ -263,8 +263,8 @@ class _SortFunction(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad, *_):
         if grad is None:
-            return (None,) * 7
-        return (expert_sort_backward(ctx.saved_tensors[0], grad.contiguous(), stream=ctx.stream),) + (None,) * 6
+            return (None,) * 6
+        return (expert_sort_backward(ctx.saved_tensors[0], grad.contiguous()),) + (None,) * 5
 
 
 # ----------------------------------------------------------------------------
@@ -279,10 +279,12 @@ def expert_unsort(position, rows, weights=None, *, out=None, keep_empty: bool = 
     without a row become zeros, or with ``keep_empty`` (a given ``out``) are
     left alone, as a combine never reads them.
 
-    Differentiable in ``rows`` and ``weights`` (without ``out``)."""
+    Differentiable in ``rows`` and ``weights`` (without ``out`` or
+    ``stream``)."""
     if (rows.requires_grad or (weights is not None and weights.requires_grad)) and torch.is_grad_enabled():
-        _need(out is None and not keep_empty, "only an unsort into a new tensor has a gradient")
-        return _UnsortFunction.apply(rows, weights, position, stream)
+        _need(out is None and not keep_empty and stream is None,
+              "only an unsort into a new tensor, on the current stream, has a gradient")
+        return _UnsortFunction.apply(rows, weights, position)
     return _unsort(position, rows, weights, out, keep_empty, stream)
 
 
@@ -372,12 +374,12 @@ def expert_unsort_backward(position, grad_out, rows=None, weights=None, *, grad_
 
 class _UnsortFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, rows, weights, position, stream):
+    def forward(ctx, rows, weights, position):
         need_weights = weights is not None and weights.requires_grad
         # the rows matter to the weights' gradient only
         ctx.save_for_backward(position, weights, rows if need_weights else None)
-        ctx.rows_shape, ctx.stream = rows.shape, stream
-        return _unsort(position, rows, weights, None, False, stream)
+        ctx.rows_shape = rows.shape
+        return _unsort(position, rows, weights, None, False, None)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -386,11 +388,10 @@ class _UnsortFunction(torch.autograd.Function):
         need_rows = ctx.needs_input_grad[0]
         g = None
         if rows is None:
-            with _On(grad.device, ctx.stream):
-                g = torch.zeros(ctx.rows_shape, dtype=grad.dtype, device=grad.device)
+            g = torch.zeros(ctx.rows_shape, dtype=grad.dtype, device=grad.device)
         gr, gw = expert_unsort_backward(position, grad.contiguous(), rows, weights, grad_rows=g, need_rows=need_rows,
-                                        need_weights=ctx.needs_input_grad[1], stream=ctx.stream)
-        return gr, gw, None, None
+                                        need_weights=ctx.needs_input_grad[1])
+        return gr, gw, None
 
 
 # ----------------------------------------------------------------------------

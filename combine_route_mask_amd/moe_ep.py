@@ -270,7 +270,7 @@ class MoeEpExchange:
                                      device=device)
         self.handle = moe_ep_create(self.params, self.workspace.data_ptr(), self.size_per_rank)
         self.views: Optional[DispatchViews] = None
-        self.most_pairs = 0  # expert rows of the last dispatch, at most
+        self._step = ((), None)  # token counts and rank mask of the last dispatch
 
     @property
     def P(self):
@@ -349,8 +349,7 @@ class MoeEpExchange:
                             T, stream, active_rank_mask, extra_payload, eplb_local_stats)
         self.views = v
         k = self.params.top_k
-        self.most_pairs = k * sum(int(n) for r, n in enumerate(num_tokens)
-                                  if active_rank_mask is None or (int(active_rank_mask) >> r) & 1)
+        self._step = (tuple(num_tokens), active_rank_mask)
         out = {
             "tokens_per_rank": v.tokens_per_rank,
             "payload": self._plane(v.payload_offset, v.payload_row_bytes, T),
@@ -373,6 +372,14 @@ class MoeEpExchange:
             out["eplb_gathered_stats"] = base.as_strided((P, P * n * 4), (self.size_per_rank, 1),
                                                          v.eplb_offset).view(torch.int32).view(P, P, n)
         return out
+
+    @property
+    def most_pairs(self) -> int:
+        """Expert rows of the last dispatch, at most: the tokens of the ranks
+        taking part times top_k."""
+        counts, mask = self._step
+        return self.params.top_k * sum(int(n) for r, n in enumerate(counts)
+                                       if mask is None or (int(mask) >> r) & 1)
 
     def expert_sort(self, recv, quantize: bool = False, capacity: Optional[int] = None, out=None,
                     out_scales=None, stream=None):

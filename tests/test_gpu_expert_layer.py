@@ -310,6 +310,8 @@ def test_binding_refusals(X):
         lambda: X.expert_sort(ids, rows[:, :, :4], 4), lambda: X.expert_sort(ids, rows[:, :, :7].contiguous(), 4),
         lambda: X.expert_sort(ids, rows.clone().requires_grad_(), 4, quantize=True),
         lambda: X.expert_sort(ids, rows.clone().requires_grad_(), 4, out=flat),
+        lambda: X.expert_sort(ids, rows.clone().requires_grad_(), 4, stream=torch.cuda.Stream()),
+        lambda: X.expert_unsort(pos, leaf, stream=torch.cuda.Stream()),
         lambda: X.expert_unsort(pos, flat.half()), lambda: X.expert_unsort(pos[0], flat),
         lambda: X.expert_unsort(pos.long(), flat), lambda: X.expert_unsort(pos, flat, w.double()),
         lambda: X.expert_unsort(pos, flat, w[:, :, :1]), lambda: X.expert_unsort(pos, flat, out=rows.float()),
