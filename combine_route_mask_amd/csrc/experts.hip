@@ -391,9 +391,9 @@ __global__ __launch_bounds__(kTileBlock) void sort_place_kernel(moe_ep_sort_args
 // ---------------------------------------------------------------------------
 // Sorts in between: each rank's pairs fit one workgroup's registers, so one
 // launch of a workgroup a rank counts, scans and places them within the rank
-// (the gather adds the pairs of the ranks before).  Against the three
-// launches for large sorts: 8 ranks of 1024 slots, top_k 8, 17 us become
-// FIGURE us.
+// (the gather adds the pairs of the ranks before).  8 ranks of 1024 slots,
+// top_k 8: 9 us, where the three launches for large sorts take 17 (one
+// workgroup for 32768 pairs takes 30 us, the three launches 14).
 // ---------------------------------------------------------------------------
 
 constexpr int kPlanBlock = 1024;
@@ -663,106 +663,111 @@ __global__ __launch_bounds__(kUnsortBlock) void unsort_kernel(moe_ep_unsort_args
 // Gradient of the weighted way back.
 // ---------------------------------------------------------------------------
 
-constexpr int kGradBlock = 256;
-constexpr int kGradVectors = 4;
-
 // One workgroup for a group of g slots.  The slot's grad_out row is held in
-// registers (256 * 4 vectors at a time) while each of its k rows passes once:
-// read for the dot product, written scaled.  The k dot products are summed
-// over lanes, then waves, in an order that the shape fixes.
-template <typename T>
-__global__ __launch_bounds__(kGradBlock) void unsort_grad_kernel(moe_ep_unsort_grad_args a, int g,
-                                                                 uint32_t items)
+// registers (BS * VPT vectors at a time) while each of its k rows passes once:
+// read for the dot product, one row ahead, and written scaled.  The k dot
+// products are summed over lanes, then waves, in an order that the shape
+// fixes.
+template <typename T, int BS, int VPT>
+__global__ __launch_bounds__(BS) void unsort_grad_kernel(moe_ep_unsort_grad_args a, int g, uint32_t items)
 {
-    constexpr int BS = kGradBlock, VPT = kGradVectors, N = RowType<T>::kPer, kWaves = BS / 64;
+    constexpr int N = RowType<T>::kPer, kWaves = BS / 64;
     __shared__ float dots[kWaves][64];
     const int64_t nslots = (int64_t)a.ranks * a.slots, row_bytes = (int64_t)a.hidden_size * RowType<T>::kBytes;
     const int k = a.top_k, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (uint32_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int64_t s0 = (int64_t)item * g;
-    const int ns = (int)min((int64_t)g, nslots - s0);
-    int pos = -1;
-    float w = 1.0f;
-    if (lane < ns * k) {
-        pos = a.position[s0 * k + lane];
-        if (a.weights) {
-            const uint32_t slot = (uint32_t)s0 + (uint32_t)lane / (uint32_t)k, S = (uint32_t)a.slots;
-            w = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(a.weights) +
-                                                (int64_t)(slot / S) * a.weights_rank_stride)[(int64_t)(slot % S) * k + lane % k];
-        }
-    }
-    const uint64_t ballot = __ballot(pos >= 0 && pos < a.num_rows);
-    dots[wave][lane] = 0.0f;
-    for (int i = 0; i < ns; ++i) {
-        const uint64_t pairs = slot_pairs(ballot, i, k);
-        if (!pairs)
-            continue;
-        const uint32_t slot = (uint32_t)(s0 + i), S = (uint32_t)a.slots;
-        const uint8_t *go = static_cast<const uint8_t *>(a.grad_out) + (int64_t)(slot / S) * a.grad_out_rank_stride +
-                            (int64_t)(slot % S) * row_bytes;
-        for (int64_t c0 = threadIdx.x; c0 * 16 - threadIdx.x * 16 < row_bytes; c0 += BS * VPT) {
-            float f[VPT][N];
-#pragma unroll
-            for (int u = 0; u < VPT; ++u) {
-                const int64_t at = (c0 + u * BS) * 16;
-                u32x4 v = {0, 0, 0, 0};
-                if (at < row_bytes)
-                    v = load16_nt(go + at);
-                RowType<T>::unpack(v, f[u]);
+        const int64_t s0 = (int64_t)item * g;
+        const int ns = (int)min((int64_t)g, nslots - s0);
+        int pos = -1;
+        float w = 1.0f;
+        if (lane < ns * k) {
+            pos = a.position[s0 * k + lane];
+            if (a.weights) {
+                const uint32_t slot = (uint32_t)s0 + (uint32_t)lane / (uint32_t)k, S = (uint32_t)a.slots;
+                w = reinterpret_cast<const float *>(reinterpret_cast<const uint8_t *>(a.weights) +
+                                                    (int64_t)(slot / S) * a.weights_rank_stride)[(int64_t)(slot % S) * k + lane % k];
             }
-            for (uint64_t m = pairs; m; m &= m - 1) {
-                const int j = i * k + __builtin_ctzll(m);
-                const int64_t row = (int64_t)__builtin_amdgcn_readlane(pos, j) * row_bytes;
-                if (a.grad_weights) {
-                    u32x4 v[VPT];
+        }
+        const uint64_t ballot = __ballot(pos >= 0 && pos < a.num_rows);
+        dots[wave][lane] = 0.0f;
+        for (int i = 0; i < ns; ++i) {
+            const uint64_t pairs = slot_pairs(ballot, i, k);
+            if (!pairs)
+                continue;
+            const uint32_t slot = (uint32_t)(s0 + i), S = (uint32_t)a.slots;
+            const uint8_t *go = static_cast<const uint8_t *>(a.grad_out) +
+                                (int64_t)(slot / S) * a.grad_out_rank_stride + (int64_t)(slot % S) * row_bytes;
+            for (int64_t base = 0; base < row_bytes; base += BS * VPT * 16) {
+                const int64_t at = base + threadIdx.x * 16;
+                const auto load = [&](const uint8_t *row, u32x4 *v) {
 #pragma unroll
                     for (int u = 0; u < VPT; ++u) {
-                        const int64_t at = (c0 + u * BS) * 16;
                         v[u] = u32x4{0, 0, 0, 0};
-                        if (at < row_bytes)
-                            v[u] = load16_nt(static_cast<const uint8_t *>(a.rows) + row + at);
+                        if (at + u * BS * 16 < row_bytes)
+                            v[u] = load16_nt(row + at + u * BS * 16);
                     }
-                    float dot = 0.0f;
+                };
+                const auto place = [&](uint64_t m) {
+                    return (int64_t)__builtin_amdgcn_readlane(pos, i * k + __builtin_ctzll(m)) * row_bytes;
+                };
+                u32x4 v[VPT], ahead[VPT];
+                float f[VPT][N];
+                load(go, v);
+                if (a.grad_weights)
+                    load(static_cast<const uint8_t *>(a.rows) + place(pairs), ahead);
 #pragma unroll
-                    for (int u = 0; u < VPT; ++u) {
-                        float x[N];
-                        RowType<T>::unpack(v[u], x);
+                for (int u = 0; u < VPT; ++u)
+                    RowType<T>::unpack(v[u], f[u]);
+                for (uint64_t m = pairs; m; m &= m - 1) {
+                    const int j = i * k + __builtin_ctzll(m);
+                    if (a.grad_weights) {
 #pragma unroll
-                        for (int e = 0; e < N; ++e)
-                            dot = fmaf(x[e], f[u][e], dot);
+                        for (int u = 0; u < VPT; ++u)
+                            v[u] = ahead[u];
+                        if (m & (m - 1))
+                            load(static_cast<const uint8_t *>(a.rows) + place(m & (m - 1)), ahead);
                     }
-                    dot = wave_sum(dot);
-                    if (lane == j)
-                        dots[wave][j] += dot;
-                }
-                if (a.grad_rows) {
-                    const float wj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), j));
+                    if (a.grad_rows) {
+                        const float wj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), j));
+                        uint8_t *to = static_cast<uint8_t *>(a.grad_rows) + place(m) + at;
 #pragma unroll
-                    for (int u = 0; u < VPT; ++u) {
-                        const int64_t at = (c0 + u * BS) * 16;
-                        if (at < row_bytes) {
-                            float y[N];
+                        for (int u = 0; u < VPT; ++u)
+                            if (at + u * BS * 16 < row_bytes) {
+                                float y[N];
+#pragma unroll
+                                for (int e = 0; e < N; ++e)
+                                    y[e] = wj * f[u][e];
+                                store16_nt(to + u * BS * 16, RowType<T>::pack(y));
+                            }
+                    }
+                    if (a.grad_weights) {
+                        float dot = 0.0f;
+#pragma unroll
+                        for (int u = 0; u < VPT; ++u) {
+                            float x[N];
+                            RowType<T>::unpack(v[u], x);
 #pragma unroll
                             for (int e = 0; e < N; ++e)
-                                y[e] = wj * f[u][e];
-                            store16_nt(static_cast<uint8_t *>(a.grad_rows) + row + at, RowType<T>::pack(y));
+                                dot = fmaf(x[e], f[u][e], dot);
                         }
+                        dot = wave_sum(dot);
+                        if (lane == j)
+                            dots[wave][j] += dot;
                     }
                 }
             }
         }
-    }
-    if (a.grad_weights) {
-        __syncthreads();
-        if ((int)threadIdx.x < ns * k) {
-            float sum = 0.0f;
+        if (a.grad_weights) {
+            __syncthreads();
+            if ((int)threadIdx.x < ns * k) {
+                float sum = 0.0f;
 #pragma unroll
-            for (int v = 0; v < kWaves; ++v)
-                sum += dots[v][lane];
-            a.grad_weights[s0 * k + lane] = sum;
+                for (int v = 0; v < kWaves; ++v)
+                    sum += dots[v][lane];
+                a.grad_weights[s0 * k + lane] = sum;
+            }
+            __syncthreads(); // before the next item clears the sums
         }
-        __syncthreads(); // before the next item clears the sums
-    }
     }
 }
 
@@ -902,11 +907,24 @@ hipError_t launch_expert_unsort_backward(const moe_ep_unsort_grad_args &a, hipSt
     const int64_t nslots = (int64_t)a.ranks * a.slots;
     const int g = slots_per_group(nslots, a.num_rows, a.top_k);
     const int64_t items = (nslots + g - 1) / g;
-    const dim3 grid = grid_of(items), block(kGradBlock);
-    if (a.row_type == MOE_EP_BF16_ROWS)
-        hipLaunchKernelGGL(unsort_grad_kernel<Bf16>, grid, block, 0, s, a, g, (uint32_t)items);
-    else
-        hipLaunchKernelGGL(unsort_grad_kernel<Fp32>, grid, block, 0, s, a, g, (uint32_t)items);
+    const dim3 grid = grid_of(items);
+    // 4095 slots of 8 rows of 7168 bf16 take 199-210 us in every shape from
+    // 64 threads of 8 vectors to 1024 of one (5.0 TB/s, half of it writes: a
+    // device copy's rate); rows of 512 vectors and fewer gain by smaller
+    // workgroups (4096 slots of 2 rows of 2048: 18.8 us against 24.8).
+    const bool shorter = (int64_t)a.hidden_size * (a.row_type == MOE_EP_BF16_ROWS ? 2 : 4) <= 512 * 16;
+    const dim3 block(shorter ? 128 : 256);
+    if (a.row_type == MOE_EP_BF16_ROWS) {
+        if (shorter)
+            hipLaunchKernelGGL((unsort_grad_kernel<Bf16, 128, 4>), grid, block, 0, s, a, g, (uint32_t)items);
+        else
+            hipLaunchKernelGGL((unsort_grad_kernel<Bf16, 256, 4>), grid, block, 0, s, a, g, (uint32_t)items);
+    } else {
+        if (shorter)
+            hipLaunchKernelGGL((unsort_grad_kernel<Fp32, 128, 4>), grid, block, 0, s, a, g, (uint32_t)items);
+        else
+            hipLaunchKernelGGL((unsort_grad_kernel<Fp32, 256, 4>), grid, block, 0, s, a, g, (uint32_t)items);
+    }
     return hipGetLastError();
 }
 
