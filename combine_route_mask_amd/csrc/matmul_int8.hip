@@ -441,8 +441,10 @@ hipError_t tile_launch(const moe_ep_matmul_args &a, hipStream_t s)
 //    expert its 64-row shape with three stages in place of two: E 32,
 //    4096 x 4096, 1 row 68 / 79, but 64 rows 124 / 110;
 //  - up to 64 x 64, four waves, three workgroups a CU, three stages, or four
-//    for up to 32 rows: where 128 x 128 has not 200 tiles.  E 1, 4096 x 4096,
-//    256 rows 11 / 19; E 1, 7168 x 7168, 1 row 13 / 32.
+//    for up to 32 rows: where 128 x 128 has not 200 tiles (E 1, 4096 x 4096,
+//    256 rows 11 / 19; E 1, 7168 x 7168, 1 row 13 / 32), and for a few rows
+//    against long weights, where only the bytes in flight count (64 rows, E 32,
+//    4096 x 7168: 137 / 145; but E 64, 1024 x 2048, 2 rows 24 / 23).
 hipError_t launch_expert_matmul(const moe_ep_matmul_args &a, hipStream_t s)
 {
     using T64 = TileShape<2, 2, 2, 2, 3>;
@@ -452,7 +454,7 @@ hipError_t launch_expert_matmul(const moe_ep_matmul_args &a, hipStream_t s)
     const auto tiles = [&](int64_t size) {
         return a.num_experts * ((average + size - 1) / size) * ((a.n + size - 1) / size);
     };
-    if (tiles(128) < 200)
+    if (tiles(128) < 200 || (average <= 8 && a.k >= 4096))
         return tile_launch<T64Few, T64>(a, s);
     if (average <= 32)
         return tile_launch<TileShape<2, 2, 4, 2, 3>, T128>(a, s);
