@@ -11,11 +11,12 @@
 namespace moe_ep {
 namespace {
 
-// Local expert of id on rank r, or -1 (unsigned compare covers both ends).
-__device__ __forceinline__ int local_expert(int32_t id, int r, int epr)
+// Local expert of id on rank r, or -1 (unsigned compare covers both ends; a
+// masked-off rank has no expert).
+__device__ __forceinline__ int local_expert(const moe_ep_sort_args &a, int32_t id, int r)
 {
-    const uint32_t e = (uint32_t)id - (uint32_t)(r * epr);
-    return e < (uint32_t)epr ? (int)e : -1;
+    const uint32_t epr = (uint32_t)a.experts_per_rank, e = (uint32_t)id - (uint32_t)r * epr;
+    return e < (a.masked_ranks >> r & 1 ? 0u : epr) ? (int)e : -1;
 }
 
 __device__ __forceinline__ const int32_t *rank_ids(const moe_ep_sort_args &a, int r)
@@ -157,7 +158,7 @@ __global__ __launch_bounds__(kDirectBlock) void sort_direct_kernel(moe_ep_sort_a
         __syncthreads();
         for (int p = threadIdx.x; p < npairs; p += BS) {
             const int r = p / per_rank;
-            const int e = local_expert(rank_ids(a, r)[p - r * per_rank], r, epr);
+            const int e = local_expert(a, rank_ids(a, r)[p - r * per_rank], r);
             if (e >= 0)
                 atomicAdd(&lds[r * epr + e], 1);
         }
@@ -195,7 +196,7 @@ __global__ __launch_bounds__(kDirectBlock) void sort_direct_kernel(moe_ep_sort_a
     const int mine = slot * k; // first pair of the slot
     int key = -1;              // lane j: global expert of pair j
     if (lane < k) {
-        const int e = local_expert(rank_ids(a, r)[q * k + lane], r, epr);
+        const int e = local_expert(a, rank_ids(a, r)[q * k + lane], r);
         key = e < 0 ? -1 : r * epr + e;
     }
     if (threadIdx.x < 64)
@@ -209,7 +210,7 @@ __global__ __launch_bounds__(kDirectBlock) void sort_direct_kernel(moe_ep_sort_a
             int other = 0x7FFFFFFF;
             if (p < npairs) {
                 const int rp = p / per_rank;
-                const int e = local_expert(rank_ids(a, rp)[p - rp * per_rank], rp, epr);
+                const int e = local_expert(a, rank_ids(a, rp)[p - rp * per_rank], rp);
                 other = e < 0 ? other : rp * epr + e;
             }
             for (uint64_t m = counted; m; m &= m - 1) {
@@ -261,7 +262,7 @@ __global__ __launch_bounds__(kTileBlock) void sort_count_kernel(moe_ep_sort_args
     const int64_t lo = (int64_t)t * per, hi = min(lo + per, (int64_t)a.slots * a.top_k);
     const int32_t *ids = rank_ids(a, r);
     for (int64_t p = lo + threadIdx.x; p < hi; p += kTileBlock) {
-        const int e = local_expert(ids[p], r, epr);
+        const int e = local_expert(a, ids[p], r);
         if (e >= 0)
             atomicAdd(&hist[e], 1);
     }
@@ -357,7 +358,7 @@ __global__ __launch_bounds__(kTileBlock) void sort_place_kernel(moe_ep_sort_args
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int64_t p = first + i * 64 + lane;
-        e[i] = p < hi ? local_expert(ids[p], r, epr) : -1;
+        e[i] = p < hi ? local_expert(a, ids[p], r) : -1;
     }
     for (int x = threadIdx.x; x < kWaves * epr; x += kTileBlock)
         next[x] = 0;
@@ -413,7 +414,7 @@ __global__ __launch_bounds__(kPlanBlock) void sort_plan_kernel(moe_ep_sort_args 
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int p = first + i * 64 + lane;
-        e[i] = i * 64 < share && p < pairs ? local_expert(ids[p], r, epr) : -1;
+        e[i] = i * 64 < share && p < pairs ? local_expert(a, ids[p], r) : -1;
     }
     for (int x = threadIdx.x; x < kPlanWaves * epr; x += kPlanBlock)
         next[x] = 0;

@@ -111,6 +111,8 @@ int moe_ep_expert_sort(const moe_ep_sort_args *args, void *stream)
         const moe_ep_sort_args &a = *args;
         if (int rc = check_sort_shape(a.ranks, a.slots, a.top_k, a.experts_per_rank))
             return rc;
+        if (a.ranks < 64 && a.masked_ranks >> a.ranks)
+            return bad("masked_ranks has bits set at or above ranks");
         if (a.capacity < 0 || a.capacity > INT32_MAX)
             return fail(MOE_EP_ERR_CAPACITY, "capacity must be in [0, 2^31 - 1]");
         if (a.quantize != 0 && a.quantize != 1)

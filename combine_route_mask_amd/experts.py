@@ -37,7 +37,7 @@ _NORMS = {"int8": (NORM_INT8, 0, torch.int8, torch.float32),
           "deepseek_fp8": (NORM_DEEPSEEK_FP8, 128, torch.float8_e4m3fn, torch.float32)}
 
 # The argument blocks of include/moe_ep.h in native layout.
-_SORT = struct.Struct("@PqPqqPqqPPPPPPqqiiiiii")
+_SORT = struct.Struct("@PqPqqPqqPPPPPPqqiiiiiiQ")
 _UNSORT = struct.Struct("@PPPqPqqiiiiii")
 _UNSORT_GRAD = struct.Struct("@PPqPPqPPqiiiiii")
 _MATMUL = struct.Struct("@PPPPPPqiiii")
@@ -169,13 +169,15 @@ def expert_sort_workspace_bytes(ranks: int, slots: int, top_k: int, experts_per_
 
 
 def expert_sort(ids, rows, experts_per_rank: int, *, scales=None, capacity: Optional[int] = None,
-                quantize: bool = False, out=None, out_scales=None, stream=None) -> SortedRows:
+                quantize: bool = False, active_rank_mask: Optional[int] = None, out=None, out_scales=None,
+                stream=None) -> SortedRows:
     """Rows to expert order.  ``ids`` int32 [R, S, k], ``rows`` [R, S, row]
     of any dtype and ``scales`` [R, S, scale row] or None, as a dispatch
     leaves them (R = 1: a batch of tokens); ranks may lie apart.  A pair (slot, j) counts when its
     id is one of its rank's ``experts_per_rank`` experts; counted pairs are
     placed by ascending (id, slot, j), those from place ``capacity`` on (by
-    default R*S*k) are dropped.  Rows behind the last pair are left as they
+    default R*S*k) are dropped; ranks outside ``active_rank_mask`` (the
+    dispatch's) hold no pair.  Rows behind the last pair are left as they
     were, in ``out`` or uninitialised.  ``quantize``: bf16 or fp32 rows become
     int8 codes with scales = amax / 127.
 
@@ -185,16 +187,16 @@ def expert_sort(ids, rows, experts_per_rank: int, *, scales=None, capacity: Opti
     if rows.requires_grad and torch.is_grad_enabled():
         _need(not quantize and out is None and stream is None and rows.dtype in _ROW_TYPES,
               "only a sort of bf16 or fp32 rows into a new tensor, on the current stream, has a gradient")
-        r, sc, p, o, c = _SortFunction.apply(rows, ids, experts_per_rank, scales, capacity, out_scales)
+        r, sc, p, o, c = _SortFunction.apply(rows, ids, experts_per_rank, scales, capacity, out_scales, active_rank_mask)
         return SortedRows(r, sc, p, o, c)
-    return _sort(ids, rows, experts_per_rank, scales, capacity, quantize, out, out_scales, stream)
+    return _sort(ids, rows, experts_per_rank, scales, capacity, quantize, out, out_scales, stream, active_rank_mask)
 
 
-def _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, stream, zeros=False):
+def _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, stream, active_rank_mask, zeros=False):
     dev = _device(rows, "rows")
     if stream is not None or dev.index != _device_now():
         with _On(dev, stream):
-            return _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, None, zeros)
+            return _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, None, active_rank_mask, zeros)
     if ids.dtype != torch.int32:
         _refuse(f"ids must be int32, got {ids.dtype}")
     ids_stride, rows_stride = _plane(ids, "ids", dev), _plane(rows, "rows", dev)
@@ -203,6 +205,11 @@ def _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, stream, z
         _refuse(f"ids are [{R}, {S}, k], rows {list(rows.shape)}")
     X = rows.shape[2]
     row_type = _row_type(rows, "rows") if quantize else 0
+    masked = 0
+    if active_rank_mask is not None:
+        if not 0 <= active_rank_mask < 1 << R:
+            _refuse(f"active_rank_mask must be a mask of {R} ranks, got {active_rank_mask:#x}")
+        masked = active_rank_mask ^ (1 << R) - 1
     if capacity is None:
         capacity = R * S * k
     elif capacity < 0:
@@ -240,7 +247,7 @@ def _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, stream, z
         scales.data_ptr() if scales is not None else 0, scales_stride, scale_bytes,
         out.data_ptr(), out_scales.data_ptr() if out_scales is not None else 0,
         position.data_ptr(), offsets.data_ptr(), counts.data_ptr(), space, work, capacity,
-        R, S, k, epr, 1 if quantize else 0, row_type), _stream_now(dev.index)))
+        R, S, k, epr, 1 if quantize else 0, row_type, masked), _stream_now(dev.index)))
     return SortedRows(out, out_scales, position, offsets, counts)
 
 
@@ -252,8 +259,8 @@ def expert_sort_backward(position, grad_rows, *, out=None, stream=None):
 
 class _SortFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, rows, ids, epr, scales, capacity, out_scales):
-        s = _sort(ids, rows, epr, scales, capacity, False, None, out_scales, None, zeros=True)
+    def forward(ctx, rows, ids, epr, scales, capacity, out_scales, active_rank_mask):
+        s = _sort(ids, rows, epr, scales, capacity, False, None, out_scales, None, active_rank_mask, zeros=True)
         ctx.save_for_backward(s.position)
         ctx.mark_non_differentiable(*(t for t in s[1:] if t is not None))
         ctx.set_materialize_grads(False)
@@ -263,8 +270,8 @@ class _SortFunction(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad, *_):
         if grad is None:
-            return (None,) * 6
-        return (expert_sort_backward(ctx.saved_tensors[0], grad.contiguous()),) + (None,) * 5
+            return (None,) * 7
+        return (expert_sort_backward(ctx.saved_tensors[0], grad.contiguous()),) + (None,) * 6
 
 
 # ----------------------------------------------------------------------------

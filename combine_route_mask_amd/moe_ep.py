@@ -349,7 +349,7 @@ class MoeEpExchange:
                             T, stream, active_rank_mask, extra_payload, eplb_local_stats)
         self.views = v
         k = self.params.top_k
-        self._step = (tuple(num_tokens), active_rank_mask)
+        self._step = (tuple(num_tokens), None if active_rank_mask is None else int(active_rank_mask))
         out = {
             "tokens_per_rank": v.tokens_per_rank,
             "payload": self._plane(v.payload_offset, v.payload_row_bytes, T),
@@ -379,18 +379,20 @@ class MoeEpExchange:
         taking part times top_k."""
         counts, mask = self._step
         return self.params.top_k * sum(int(n) for r, n in enumerate(counts)
-                                       if mask is None or (int(mask) >> r) & 1)
+                                       if mask is None or mask >> r & 1)
 
     def expert_sort(self, recv, quantize: bool = False, capacity: Optional[int] = None, out=None,
                     out_scales=None, stream=None):
         """The received rows of the last dispatch (``recv``, its result) in
-        expert order, all ranks' experts after one another: see
-        ``experts.expert_sort``.  The capacity defaults to the step's tokens
+        expert order, all ranks' experts after one another (masked-off
+        ranks have none): see ``experts.expert_sort``.  The capacity defaults to the step's tokens
         times top_k, which holds every pair.  ``quantize`` (BF16 payloads)
         makes int8 rows with one scale each."""
         import torch
         from . import experts
         _need(self.views is not None, "expert_sort before any dispatch")
+        _need(not 0 <= self.params.invalid_expert_id < self.params.num_experts,
+              "empty slots carry an expert's id: create the exchange with an invalid_expert_id outside [0, num_experts)")
         rows = recv["payload"]
         if self.params.dispatch_format == FMT_BF16:
             rows = rows.view(torch.bfloat16)
@@ -399,7 +401,8 @@ class MoeEpExchange:
         return experts.expert_sort(recv["ids"], rows, self.params.num_experts // self.P,
                                    scales=recv["scales"],
                                    capacity=self.most_pairs if capacity is None else capacity,
-                                   quantize=quantize, out=out, out_scales=out_scales, stream=stream)
+                                   quantize=quantize, active_rank_mask=self._step[1], out=out,
+                                   out_scales=out_scales, stream=stream)
 
     def combine_landing(self):
         """FP8 combine landing planes of the last step: codes

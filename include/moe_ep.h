@@ -297,7 +297,9 @@ int moe_ep_reduce_scatterv(int32_t ep_size, const int32_t *sizes, int32_t hidden
  * region; with ranks = 1 simply a batch of tokens).  A pair (r, q, j) counts
  * when its id lies on its rank: r*e <= id < (r+1)*e, e = experts_per_rank;
  * other ids (other ranks' experts, the invalid id, anything out of range)
- * are passed over.  Counted pairs are placed by ascending (id, q, j): the
+ * are passed over, and so are all ids of the ranks in masked_ranks: a
+ * dispatch leaves a masked-off rank's region as it was, earlier steps' ids
+ * among it.  Counted pairs are placed by ascending (id, q, j): the
  * order depends on the ids alone.
  *  position  [R][S][k]: a pair's place, -1 where it has none
  *  counts    [R*e]: pairs of each expert
@@ -342,6 +344,7 @@ typedef struct moe_ep_sort_args {
     int32_t experts_per_rank;
     int32_t quantize;            /* 0: copy, 1: int8 codes and scales        */
     int32_t row_type;            /* MOE_EP_*_ROWS, read when quantize = 1    */
+    uint64_t masked_ranks;       /* bit r: rank r's slots hold nothing; bits >= R clear */
 } moe_ep_sort_args;
 
 /* Bytes of workspace an expert sort of this shape needs (0: none; -1: bad

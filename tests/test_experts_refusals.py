@@ -30,7 +30,7 @@ def _fields(struct):
     out = []
     for decl in body.split(";"):
         if decl.strip():
-            kind = "P" if "*" in decl else {"int64_t": "q", "int32_t": "i", "float": "f"}[decl.split()[0]]
+            kind = "P" if "*" in decl else {"int64_t": "q", "uint64_t": "Q", "int32_t": "i", "float": "f"}[decl.split()[0]]
             out.append((re.findall(r"\w+", decl)[-1], kind))
     return out
 
@@ -50,7 +50,7 @@ GOOD = {
         ids=A, ids_rank_stride=512, rows=A, rows_rank_stride=4096, row_bytes=128, scales=0, scales_rank_stride=0,
         scale_row_bytes=0, out_rows=A, out_scales=0, position=A, offsets=A, counts=A, workspace=A,
         workspace_bytes=1 << 16, capacity=100, ranks=2, slots=32, top_k=4, experts_per_rank=8, quantize=0,
-        row_type=0)),
+        row_type=0, masked_ranks=2)),
     "moe_ep_expert_unsort": ("moe_ep_unsort_args", dict(
         position=A, rows=A, weights=A, weights_rank_stride=512, out=A, out_rank_stride=4096, num_rows=100, ranks=2,
         slots=32, top_k=4, hidden_size=64, row_type=0, keep_empty=0)),
@@ -72,7 +72,7 @@ BAD = [
     ("moe_ep_expert_sort", dict(slots=-1), ARG), ("moe_ep_expert_sort", dict(top_k=0), ARG),
     ("moe_ep_expert_sort", dict(top_k=65), ARG), ("moe_ep_expert_sort", dict(experts_per_rank=0), ARG),
     ("moe_ep_expert_sort", dict(experts_per_rank=2049), ARG),
-    ("moe_ep_expert_sort", dict(slots=1 << 30), CAP), ("moe_ep_expert_sort", dict(capacity=-1), CAP),
+    ("moe_ep_expert_sort", dict(masked_ranks=4), ARG), ("moe_ep_expert_sort", dict(slots=1 << 30), CAP), ("moe_ep_expert_sort", dict(capacity=-1), CAP),
     ("moe_ep_expert_sort", dict(capacity=1 << 31), CAP), ("moe_ep_expert_sort", dict(row_bytes=0), ARG),
     ("moe_ep_expert_sort", dict(row_bytes=24), ARG), ("moe_ep_expert_sort", dict(row_bytes=(1 << 24) + 16), ARG),
     ("moe_ep_expert_sort", dict(ids=0), ARG), ("moe_ep_expert_sort", dict(ids=A + 2), ARG),

@@ -110,6 +110,47 @@ def test_layer_between_dispatch_and_combine(X, P, T, E, k, H, I, mask):
     ex8.destroy()
 
 
+@pytest.mark.parametrize("P,T,E,k", [(4, 9, 16, 4), (4, 130, 16, 4), (8, 700, 32, 2), (4, 2200, 16, 4)])
+def test_masked_ranks_hold_no_pairs(X, P, T, E, k):
+    """A dispatch leaves a masked-off rank's region as the step before left
+    it (at first: whatever the workspace held): its ids are no pairs, at every
+    size class of the sort, and take no place from the live ranks' ones."""
+    from combine_route_mask_amd.moe_ep import MoeEpArgError, MoeEpExchange
+    H = 64
+    log(f"masked ranks P{P} T{T} E{E} k{k}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    ids = torch.rand((P, T, E), generator=g, device="cuda").argsort(2)[:, :, :k].to(torch.int32)
+    wts = torch.rand((P, T, k), generator=g, device="cuda")
+    x = torch.randn((P, T, H), generator=g, device="cuda", dtype=BF)
+    ex = MoeEpExchange(P, E, k, T, H)
+    ex.workspace.zero_()  # zeros: ids of expert 0, on rank 0
+    for mask in (0b0110, None, 0b1101 | (0xF0 if P == 8 else 0)):
+        recv = ex.dispatch(x, ids, wts, num_tokens=[T] * P, active_rank_mask=mask)
+        live = [r for r in range(P) if mask is None or mask >> r & 1]
+        want = recv["ids"].clone()
+        for r in range(P):
+            if r not in live:
+                want[r] = E
+        for quantize in (False, True):
+            s = ex.expert_sort(recv, quantize=quantize)
+            ref = X.expert_sort(want, recv["payload"].view(BF).contiguous(), E // P, capacity=ex.most_pairs,
+                                quantize=quantize)
+            m = int(ref.offsets[-1])
+            assert torch.equal(s.counts, ref.counts) and torch.equal(s.offsets, ref.offsets), mask
+            assert torch.equal(s.position, ref.position) and torch.equal(s.rows[:m], ref.rows[:m]), mask
+            if mask is None:
+                assert m == P * T * k
+    with pytest.raises(MoeEpArgError):
+        X.expert_sort(want, x.view(P, T, H).repeat(1, P, 1), E // P, active_rank_mask=1 << P)
+    ex.destroy()
+    odd = MoeEpExchange(P, E, k, T, H, invalid_expert_id=0)
+    recv = odd.dispatch(x, ids, wts, num_tokens=[T] * P)
+    with pytest.raises(MoeEpArgError):  # empty slots would be pairs
+        odd.expert_sort(recv)
+    odd.destroy()
+
+
 def _state(rng, seed, R=2, S=70, k=3, epr=4, H=256, I=96):
     g = torch.Generator(device="cuda")
     g.manual_seed(seed)
