@@ -116,6 +116,9 @@ def _row_type(t, name):
     return rt
 
 
+_written = torch.autograd.graph.increment_version  # of a given output: autograd then knows what it saved is gone
+
+
 def _no_grad(*tensors):
     """Without a gradient of its own, an operator refuses to drop one."""
     if torch.is_grad_enabled():
@@ -216,6 +219,7 @@ def _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, stream, a
         _refuse("capacity may not be negative")
     scales_stride = scale_bytes = 0
     if scales is not None:
+        _no_grad(scales)
         if quantize:
             _refuse("quantised rows take no scale rows")
         scales_stride = _plane(scales, "scales", dev)
@@ -228,12 +232,14 @@ def _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, stream, a
         out = (torch.zeros if zeros else torch.empty)((capacity, X), dtype=dtype, device=dev)
     else:
         _flat(out, "out", dev, dtype, (capacity, X))
+        _written(out)
     if quantize or scales is not None:
         shape, dtype = ((capacity,), torch.float32) if quantize else ((capacity, scales.shape[2]), scales.dtype)
         if out_scales is None:
             out_scales = torch.empty(shape, dtype=dtype, device=dev)
         else:
             _flat(out_scales, "out_scales", dev, dtype, shape)
+            _written(out_scales)
     else:
         out_scales = None
     E = R * epr
@@ -331,6 +337,7 @@ def _unsort(position, rows, weights, out, keep_empty, stream):
         if out.dtype != rows.dtype or out.shape != (R, S, H):
             _refuse(f"out must be {rows.dtype} [{R}, {S}, {H}], got {out.dtype} {list(out.shape)}")
         stride = _plane(out, "out", dev)
+        _written(out)
     _check(lib.moe_ep_expert_unsort(_UNSORT.pack(
         position.data_ptr(), rows.data_ptr(), wp, ws, out.data_ptr(), stride, M, R, S, k, H, rt,
         1 if keep_empty else 0), _stream_now(dev.index)))
@@ -366,6 +373,7 @@ def expert_unsort_backward(position, grad_out, rows=None, weights=None, *, grad_
         _flat(rows, "rows", dev, grad_out.dtype, (M, H))
     if grad_rows is not None:
         _flat(grad_rows, "grad_rows", dev, grad_out.dtype, (M, H))
+        _written(grad_rows)
     wp, ws = _weights(weights, position, dev)
     if not need_rows:
         grad_rows = None
@@ -383,8 +391,12 @@ class _UnsortFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, rows, weights, position):
         need_weights = weights is not None and weights.requires_grad
+        kept = weights
+        if weights is not None and weights.untyped_storage().nbytes() != 4 * weights.numel():
+            # a plane of a workspace, which the next dispatch overwrites unseen by autograd
+            kept = weights.clone()
         # the rows matter to the weights' gradient only
-        ctx.save_for_backward(position, weights, rows if need_weights else None)
+        ctx.save_for_backward(position, kept, rows if need_weights else None)
         ctx.rows_shape = rows.shape
         return _unsort(position, rows, weights, None, False, None)
 
@@ -438,6 +450,7 @@ def expert_matmul(x, x_scales, weight, weight_scales, *, offsets=None, out=None,
         out = torch.empty((M, N), dtype=dtype, device=dev)
     else:
         _flat(out, "out", dev, out.dtype, (M, N))
+        _written(out)
     _check(lib.moe_ep_expert_matmul(_MATMUL.pack(
         x.data_ptr(), x_scales.data_ptr(), weight.data_ptr(), weight_scales.data_ptr(),
         offsets.data_ptr() if offsets is not None else 0, out.data_ptr(), M, E, N, K,
@@ -469,10 +482,12 @@ def silu_mul_quantize(x, *, offsets=None, out=None, out_scales=None, stream=None
         out = torch.empty((M, I), dtype=torch.int8, device=dev)
     else:
         _flat(out, "out", dev, torch.int8, (M, I))
+        _written(out)
     if out_scales is None:
         out_scales = torch.empty(M, dtype=torch.float32, device=dev)
     else:
         _flat(out_scales, "out_scales", dev, torch.float32, (M,))
+        _written(out_scales)
     _check(lib.moe_ep_silu_mul_quantize(_SILU.pack(x.data_ptr(), last, out.data_ptr(), out_scales.data_ptr(),
                                                    M, I, rt), _stream_now(dev.index)))
     return QuantizedRows(out, out_scales)
@@ -513,12 +528,15 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, *, format: str = "mxfp8
         out = torch.empty((M, H), dtype=row_dtype, device=dev)
     else:
         _flat(out, "out", dev, row_dtype, (M, H))
+        _written(out)
     if out_scales is None:
         out_scales = torch.empty(scale_shape, dtype=scale_dtype, device=dev)
     else:
         _flat(out_scales, "out_scales", dev, scale_dtype, scale_shape)
+        _written(out_scales)
     if residual_out is not None:
         _flat(residual_out, "residual_out", dev, x.dtype, (M, H))
+        _written(residual_out)
     elif residual is not None:
         residual_out = torch.empty_like(x)
     _check(lib.moe_ep_add_rms_norm(_NORM.pack(

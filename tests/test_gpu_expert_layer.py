@@ -269,6 +269,36 @@ def test_gradients_on_a_captured_stream(X):
     del g
 
 
+def test_saved_tensors_are_the_forward_ones(X):
+    """Weights in a workspace that the next step overwrites keep the values
+    of their forward in its gradient; a buffer that an operator writes in place
+    is no longer the one that autograd saved, and backward says so."""
+    st = _state(None, 11, S=40)
+    ids, x, w = st["ids"], st["rows"], st["w"]
+    space = torch.zeros((2, 4096), device="cuda")
+    plane = space[:, :40 * 3].view(2, 40, 3)
+    plane.copy_(w)
+    go = torch.randn_like(x)
+    for own_grad in (False, True):
+        xl = x.clone().requires_grad_()
+        wl = plane.detach().requires_grad_(own_grad)
+        s = X.expert_sort(ids, xl, 4)
+        y = X.expert_unsort(s.position, s.rows, wl)
+        kept = space.clone()
+        space.data.fill_(7.0)  # as a kernel writes: unseen by autograd
+        got = torch.autograd.grad(y, (xl, wl) if own_grad else (xl,), go)
+        space.data.copy_(kept)
+        gr, gw = X.expert_unsort_backward(s.position, go, s.rows.detach(), w)
+        want = (X.expert_sort_backward(s.position, gr), gw)
+        assert _same(got, want[:len(got)])
+    rows = X.expert_sort(ids, x, 4)
+    wl = w.clone().requires_grad_()
+    y = X.expert_unsort(rows.position, rows.rows, wl)
+    X.expert_sort(ids, go, 4, out=rows.rows)
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.backward(go)
+
+
 def test_offsets_past_32_bits(X):
     """More than 2^32 bytes of sorted rows, expert weights, tokens and norm rows: the last ones are right."""
     free = torch.cuda.mem_get_info()[0]
