@@ -245,7 +245,8 @@ __global__ __launch_bounds__(kDirectBlock) void sort_direct_kernel(moe_ep_sort_a
 }
 
 // ---------------------------------------------------------------------------
-// Large sorts: counts by tile, one scan, places by tile, then the rows.
+// Large sorts: counts by tile, a scan for each expert, places by tile, then
+// the rows.
 // ---------------------------------------------------------------------------
 
 constexpr int kTileBlock = 256;
@@ -272,53 +273,59 @@ __global__ __launch_bounds__(kTileBlock) void sort_count_kernel(moe_ep_sort_args
         ws[((int64_t)r * epr + e) * tiles + t] = hist[e];
 }
 
-constexpr int kScanBlock = 1024;
-
-// Exclusive prefix of ws in place (expert-major, so that an expert's first
-// entry becomes its first place), offsets and counts.  One workgroup: the
-// table has one entry for each 2048 pairs and expert.
-__global__ __launch_bounds__(kScanBlock) void sort_scan_kernel(moe_ep_sort_args a, int tiles)
+// Inclusive prefix over the workgroup's threads; `sums` holds a word for each
+// wave, `total` is all threads' sum.
+template <int BS>
+__device__ __forceinline__ int block_prefix(int x, int32_t *sums, int &total)
 {
-    __shared__ int32_t first[MOE_EP_MAX_SORT_EXPERTS + 1];
-    __shared__ int32_t sums[kScanBlock / 64];
-    const int E = a.ranks * a.experts_per_rank, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t n = (int64_t)E * tiles;
-    int32_t *ws = static_cast<int32_t *>(a.workspace);
-    const int64_t per = (n + kScanBlock - 1) / kScanBlock;
-    const int64_t lo = min(n, (int64_t)threadIdx.x * per), hi = min(n, lo + per);
-    int sum = 0;
-    for (int64_t i = lo; i < hi; ++i)
-        sum += ws[i];
-    int before = sum;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
-        const int y = __shfl_up(before, m);
-        before += lane >= m ? y : 0;
+        const int y = __shfl_up(x, m);
+        x += lane >= m ? y : 0;
     }
+    __syncthreads(); // the last use of sums is over
     if (lane == 63)
-        sums[wave] = before;
+        sums[wave] = x;
     __syncthreads();
-    int total = 0;
-    for (int w = 0; w < kScanBlock / 64; ++w) {
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < BS / 64; ++w) {
         if (w == wave)
-            before += total;
+            x += total;
         total += sums[w];
     }
-    before -= sum;
-    for (int64_t i = lo; i < hi; ++i) {
-        const int c = ws[i];
-        if (i % tiles == 0)
-            first[i / tiles] = before;
-        ws[i] = before;
-        before += c;
+    return x;
+}
+
+// Each expert's tiles: exclusive prefix in place, and its pairs.  A workgroup
+// an expert (one workgroup for the whole table took 300 us of a sort of
+// 524288 pairs over 256 experts).
+__global__ __launch_bounds__(kTileBlock) void sort_scan_kernel(moe_ep_sort_args a, int tiles)
+{
+    constexpr int PER = 4;
+    __shared__ int32_t sums[kTileBlock / 64];
+    int32_t *row = static_cast<int32_t *>(a.workspace) + (int64_t)blockIdx.x * tiles;
+    int carry = 0;
+    for (int base = 0; base < tiles; base += kTileBlock * PER) {
+        const int first = base + threadIdx.x * PER;
+        int v[PER], sum = 0, total;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            v[i] = first + i < tiles ? row[first + i] : 0;
+            sum += v[i];
+        }
+        int before = carry + block_prefix<kTileBlock>(sum, sums, total) - sum;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (first + i < tiles)
+                row[first + i] = before;
+            before += v[i];
+        }
+        carry += total;
     }
     if (threadIdx.x == 0)
-        first[E] = total;
-    __syncthreads();
-    for (int e = threadIdx.x; e <= E; e += kScanBlock) {
-        a.offsets[e] = (int32_t)min((int64_t)first[e], a.capacity);
-        if (e < E)
-            a.counts[e] = first[e + 1] - first[e];
-    }
+        a.counts[blockIdx.x] = carry;
 }
 
 // Places of a wave's 64 pairs, lane by lane (local experts e, -1 for none):
@@ -344,9 +351,10 @@ __device__ __forceinline__ int place_pairs(int e, int bits, int lane, int32_t *n
 }
 
 // Places of a tile's pairs: each wave takes a quarter of the tile in order.
+// A rank's first tile writes its offsets.
 __global__ __launch_bounds__(kTileBlock) void sort_place_kernel(moe_ep_sort_args a, int tiles, int bits)
 {
-    extern __shared__ int32_t next[]; // [waves][epr]
+    extern __shared__ int32_t next[]; // [waves][epr], at least a word for each wave
     constexpr int kWaves = kTileBlock / 64, IT = kSortTilePairs / kTileBlock;
     const int r = blockIdx.x / tiles, t = blockIdx.x % tiles, epr = a.experts_per_rank;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -360,6 +368,20 @@ __global__ __launch_bounds__(kTileBlock) void sort_place_kernel(moe_ep_sort_args
         const int64_t p = first + i * 64 + lane;
         e[i] = p < hi ? local_expert(a, ids[p], r) : -1;
     }
+    // thread x takes the experts x * share ..: `start` is the first one's
+    // first place, behind the pairs of all experts before
+    const int32_t *counts = a.counts + r * epr;
+    const int share = (epr + kTileBlock - 1) / kTileBlock;
+    const int elo = min(epr, (int)threadIdx.x * share), ehi = min(epr, elo + share);
+    int own = 0, earlier = 0, start, total;
+    for (int x = elo; x < ehi; ++x)
+        own += counts[x];
+    for (int x = threadIdx.x; x < r * epr; x += kTileBlock)
+        earlier += a.counts[x];
+    block_prefix<kTileBlock>(earlier, next, total);
+    start = total - own;
+    start += block_prefix<kTileBlock>(own, next, total);
+    __syncthreads();
     for (int x = threadIdx.x; x < kWaves * epr; x += kTileBlock)
         next[x] = 0;
     __syncthreads();
@@ -370,13 +392,18 @@ __global__ __launch_bounds__(kTileBlock) void sort_place_kernel(moe_ep_sort_args
             atomicAdd(&mine[e[i]], 1);
     __syncthreads();
     const int32_t *ws = static_cast<const int32_t *>(a.workspace);
-    for (int x = threadIdx.x; x < epr; x += kTileBlock) {
-        int before = ws[((int64_t)r * epr + x) * tiles + t];
+    for (int x = elo; x < ehi; ++x) {
+        if (t == 0)
+            a.offsets[r * epr + x] = (int32_t)min((int64_t)start, a.capacity);
+        int before = start + ws[((int64_t)r * epr + x) * tiles + t];
         for (int w = 0; w < kWaves; ++w) {
             const int c = next[w * epr + x];
             next[w * epr + x] = before;
             before += c;
         }
+        start += counts[x];
+        if (t == 0 && r == a.ranks - 1 && x == epr - 1)
+            a.offsets[a.ranks * epr] = (int32_t)min((int64_t)start, a.capacity);
     }
     __syncthreads();
     int32_t *position = a.position + (int64_t)r * a.slots * a.top_k;
@@ -808,6 +835,13 @@ hipError_t launch_expert_sort(const moe_ep_sort_args &a, hipStream_t s)
             hipLaunchKernelGGL((sort_direct_kernel<Fp32, true>), grid, dim3(kDirectBlock), 0, s, a, nchunk);
         return hipGetLastError();
     }
+    const int g = slots_per_group(nslots, a.capacity, a.top_k);
+    const int64_t groups = (nslots + g - 1) / g;
+    const uint32_t nchunk =
+        a.quantize ? 1 : (uint32_t)((nvec + kGatherBlock * kGatherVectors - 1) / (kGatherBlock * kGatherVectors));
+    const int64_t items = groups * nchunk;
+    if (items > INT32_MAX)
+        return hipErrorInvalidConfiguration;
     const int epr = a.experts_per_rank;
     int bits = 0;
     while ((1 << bits) < epr)
@@ -820,30 +854,19 @@ hipError_t launch_expert_sort(const moe_ep_sort_args &a, hipStream_t s)
             return e;
     } else {
         const int tiles = (int)sort_tiles(a.slots, a.top_k);
-        if (a.slots) {
-            hipLaunchKernelGGL(sort_count_kernel, dim3(a.ranks * tiles), dim3(kTileBlock), epr * 4, s, a, tiles);
-            if (hipError_t e = hipGetLastError())
-                return e;
-        }
-        hipLaunchKernelGGL(sort_scan_kernel, dim3(1), dim3(kScanBlock), 0, s, a, tiles);
+        hipLaunchKernelGGL(sort_count_kernel, dim3(a.ranks * tiles), dim3(kTileBlock), epr * 4, s, a, tiles);
         if (hipError_t e = hipGetLastError())
             return e;
-        if (!a.slots)
-            return hipSuccess;
+        hipLaunchKernelGGL(sort_scan_kernel, dim3(E), dim3(kTileBlock), 0, s, a, tiles);
+        if (hipError_t e = hipGetLastError())
+            return e;
         hipLaunchKernelGGL(sort_place_kernel, dim3(a.ranks * tiles), dim3(kTileBlock), (kTileBlock / 64) * epr * 4, s,
                            a, tiles, bits);
         if (hipError_t e = hipGetLastError())
             return e;
-        if (!a.capacity)
+        if (!a.capacity || !a.slots)
             return hipSuccess;
     }
-    const int g = slots_per_group(nslots, a.capacity, a.top_k);
-    const int64_t groups = (nslots + g - 1) / g;
-    const uint32_t nchunk =
-        a.quantize ? 1 : (uint32_t)((nvec + kGatherBlock * kGatherVectors - 1) / (kGatherBlock * kGatherVectors));
-    const int64_t items = groups * nchunk;
-    if (items > INT32_MAX)
-        return hipErrorInvalidConfiguration;
     dim3 grid = grid_of(items);
     grid.x += planned;
     const dim3 block(kGatherBlock);

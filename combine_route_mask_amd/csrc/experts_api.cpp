@@ -69,7 +69,7 @@ int check_sort_shape(int32_t ranks, int32_t slots, int32_t top_k, int32_t expert
 
 int64_t sort_workspace(int32_t ranks, int32_t slots, int32_t top_k, int32_t epr)
 {
-    if (slots == 0 || sort_is_direct(ranks, slots, top_k, ranks * epr))
+    if (sort_is_direct(ranks, slots, top_k, ranks * epr))
         return 0;
     // a total for each rank and a place for each pair
     if (sort_is_planned(slots, top_k, epr))

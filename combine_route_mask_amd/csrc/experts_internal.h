@@ -30,7 +30,7 @@ __host__ __device__ inline int sort_tile_slots(int top_k)
 inline int64_t sort_tiles(int64_t slots, int top_k)
 {
     const int64_t ts = sort_tile_slots(top_k);
-    return (slots + ts - 1) / ts;
+    return slots ? (slots + ts - 1) / ts : 1; // an empty one still writes counts and offsets
 }
 
 inline bool sort_is_direct(int ranks, int64_t slots, int top_k, int experts)

@@ -45,6 +45,15 @@ _SILU = struct.Struct("@PPPPqii")
 _NORM = struct.Struct("@PPPPPPqiiif")
 
 
+def _call(entry, block, dev, *values):
+    """The entry point with its packed argument block, on the device's current stream."""
+    try:
+        packed = block.pack(*values)
+    except (struct.error, OverflowError) as e:
+        _refuse(f"an argument is out of range: {e}")
+    _check(entry(packed, _stream_now(dev.index)))
+
+
 class SortedRows(NamedTuple):
     """Rows in expert order.  ``rows`` [capacity, row] and ``scales`` (scale
     rows, or fp32 [capacity] of int8 rows, or None); ``position`` int32
@@ -163,7 +172,8 @@ class _On:
 # ----------------------------------------------------------------------------
 
 def expert_sort_workspace_bytes(ranks: int, slots: int, top_k: int, experts_per_rank: int) -> int:
-    if not 1 <= experts_per_rank <= MAX_SORT_EXPERTS or max(ranks, slots, top_k) > _INT_MAX:
+    if (not 1 <= experts_per_rank <= MAX_SORT_EXPERTS or min(ranks, slots, top_k) < 0
+            or max(ranks, slots, top_k) > _INT_MAX):
         _refuse(f"bad sort shape: {ranks} ranks, {slots} slots, top_k {top_k}, {experts_per_rank} experts a rank")
     n = lib.moe_ep_expert_sort_workspace_bytes(ranks, slots, top_k, experts_per_rank)
     if n < 0:
@@ -246,14 +256,14 @@ def _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, stream, a
     position = ids.new_empty((R, S, k))
     offsets = ids.new_empty(E + 1)
     counts = ids.new_empty(E)
-    # the workspace's memory returns to the stream's pool behind this launch
-    space = torch.empty(work, dtype=torch.uint8, device=dev).data_ptr() if work else 0
-    _check(lib.moe_ep_expert_sort(_SORT.pack(
-        ids.data_ptr(), ids_stride, rows.data_ptr(), rows_stride, X * rows.element_size(),
-        scales.data_ptr() if scales is not None else 0, scales_stride, scale_bytes,
-        out.data_ptr(), out_scales.data_ptr() if out_scales is not None else 0,
-        position.data_ptr(), offsets.data_ptr(), counts.data_ptr(), space, work, capacity,
-        R, S, k, epr, 1 if quantize else 0, row_type, masked), _stream_now(dev.index)))
+    # held until the launches are on the stream: no other thread's call may take its memory between them
+    space = torch.empty(work, dtype=torch.uint8, device=dev) if work else None
+    _call(lib.moe_ep_expert_sort, _SORT, dev,
+          ids.data_ptr(), ids_stride, rows.data_ptr(), rows_stride, X * rows.element_size(),
+          scales.data_ptr() if scales is not None else 0, scales_stride, scale_bytes,
+          out.data_ptr(), out_scales.data_ptr() if out_scales is not None else 0,
+          position.data_ptr(), offsets.data_ptr(), counts.data_ptr(), space.data_ptr() if work else 0, work,
+          capacity, R, S, k, epr, 1 if quantize else 0, row_type, masked)
     return SortedRows(out, out_scales, position, offsets, counts)
 
 
@@ -338,9 +348,9 @@ def _unsort(position, rows, weights, out, keep_empty, stream):
             _refuse(f"out must be {rows.dtype} [{R}, {S}, {H}], got {out.dtype} {list(out.shape)}")
         stride = _plane(out, "out", dev)
         _written(out)
-    _check(lib.moe_ep_expert_unsort(_UNSORT.pack(
-        position.data_ptr(), rows.data_ptr(), wp, ws, out.data_ptr(), stride, M, R, S, k, H, rt,
-        1 if keep_empty else 0), _stream_now(dev.index)))
+    _call(lib.moe_ep_expert_unsort, _UNSORT, dev,
+          position.data_ptr(), rows.data_ptr(), wp, ws, out.data_ptr(), stride, M, R, S, k, H, rt,
+          1 if keep_empty else 0)
     return out
 
 
@@ -380,10 +390,10 @@ def expert_unsort_backward(position, grad_out, rows=None, weights=None, *, grad_
     elif grad_rows is None:
         grad_rows = torch.zeros((M, H), dtype=grad_out.dtype, device=dev)
     gw = torch.empty((R, S, k), dtype=torch.float32, device=dev) if need_weights else None
-    _check(lib.moe_ep_expert_unsort_backward(_UNSORT_GRAD.pack(
-        position.data_ptr(), grad_out.data_ptr(), stride, rows.data_ptr() if rows is not None else 0, wp, ws,
-        grad_rows.data_ptr() if grad_rows is not None else 0, gw.data_ptr() if gw is not None else 0,
-        M, R, S, k, H, rt, 0), _stream_now(dev.index)))
+    _call(lib.moe_ep_expert_unsort_backward, _UNSORT_GRAD, dev,
+          position.data_ptr(), grad_out.data_ptr(), stride, rows.data_ptr() if rows is not None else 0, wp, ws,
+          grad_rows.data_ptr() if grad_rows is not None else 0, gw.data_ptr() if gw is not None else 0,
+          M, R, S, k, H, rt, 0)
     return grad_rows, gw
 
 
@@ -451,10 +461,10 @@ def expert_matmul(x, x_scales, weight, weight_scales, *, offsets=None, out=None,
     else:
         _flat(out, "out", dev, out.dtype, (M, N))
         _written(out)
-    _check(lib.moe_ep_expert_matmul(_MATMUL.pack(
-        x.data_ptr(), x_scales.data_ptr(), weight.data_ptr(), weight_scales.data_ptr(),
-        offsets.data_ptr() if offsets is not None else 0, out.data_ptr(), M, E, N, K,
-        _row_type(out, "out")), _stream_now(dev.index)))
+    _call(lib.moe_ep_expert_matmul, _MATMUL, dev,
+          x.data_ptr(), x_scales.data_ptr(), weight.data_ptr(), weight_scales.data_ptr(),
+          offsets.data_ptr() if offsets is not None else 0, out.data_ptr(), M, E, N, K,
+          _row_type(out, "out"))
     return out
 
 
@@ -488,8 +498,8 @@ def silu_mul_quantize(x, *, offsets=None, out=None, out_scales=None, stream=None
     else:
         _flat(out_scales, "out_scales", dev, torch.float32, (M,))
         _written(out_scales)
-    _check(lib.moe_ep_silu_mul_quantize(_SILU.pack(x.data_ptr(), last, out.data_ptr(), out_scales.data_ptr(),
-                                                   M, I, rt), _stream_now(dev.index)))
+    _call(lib.moe_ep_silu_mul_quantize, _SILU, dev,
+          x.data_ptr(), last, out.data_ptr(), out_scales.data_ptr(), M, I, rt)
     return QuantizedRows(out, out_scales)
 
 
@@ -539,8 +549,8 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, *, format: str = "mxfp8
         _written(residual_out)
     elif residual is not None:
         residual_out = torch.empty_like(x)
-    _check(lib.moe_ep_add_rms_norm(_NORM.pack(
-        x.data_ptr(), residual.data_ptr() if residual is not None else 0, weight.data_ptr(),
-        residual_out.data_ptr() if residual_out is not None else 0, out.data_ptr(), out_scales.data_ptr(),
-        M, H, rt, code, eps), _stream_now(dev.index)))
+    _call(lib.moe_ep_add_rms_norm, _NORM, dev,
+          x.data_ptr(), residual.data_ptr() if residual is not None else 0, weight.data_ptr(),
+          residual_out.data_ptr() if residual_out is not None else 0, out.data_ptr(), out_scales.data_ptr(),
+          M, H, rt, code, eps)
     return NormedRows(out, out_scales, x if residual_out is None else residual_out)

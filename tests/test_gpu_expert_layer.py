@@ -414,6 +414,23 @@ def test_binding_refusals(X):
         X.silu_mul_quantize(flat.repeat(1, 2).requires_grad_())
 
 
+def test_sizes_past_the_argument_blocks(X):
+    """Numbers that an argument block cannot hold are refused by name."""
+    from combine_route_mask_amd.moe_ep import MoeEpArgError
+    ids = torch.zeros((1, 4, 2), dtype=torch.int32, device="cuda")
+    rows = torch.zeros((1, 4, 16), dtype=BF, device="cuda")
+    for call in (lambda: X.expert_sort(ids, rows, 4, capacity=2.5, out=None),
+                 lambda: X.expert_sort(ids, rows, 4, active_rank_mask=-1),
+                 lambda: X.expert_sort(ids, rows, 4, scales=torch.zeros((1, 4, 2), device="cuda", requires_grad=True)),
+                 lambda: X.expert_sort_workspace_bytes(1 - (1 << 32), 4, 2, 4),
+                 lambda: X.expert_matmul(torch.zeros((0, 1 << 33), dtype=torch.int8, device="cuda"),
+                                         torch.zeros(0, device="cuda"),
+                                         torch.zeros((0, 1 << 33), dtype=torch.int8, device="cuda"),
+                                         torch.zeros(0, device="cuda"))):
+        with pytest.raises((MoeEpArgError, TypeError)):
+            call()
+
+
 def test_empty_calls(X):
     """No row, no slot, no capacity: nothing to do, and the offsets say so."""
     ids, rows = torch.zeros((2, 0, 3), dtype=torch.int32, device="cuda"), torch.zeros((2, 0, 32), dtype=BF, device="cuda")

@@ -68,6 +68,9 @@ SORTS = [
     (2, 900, 4, 16, 48, BF, 0, 0.37),
     (1, 61, 8, 16, 48, BF, 0, 0.0),
     (1, 900, 4, 16, 48, BF, 0, 0.0),
+    (2, 0, 2, 2000, 64, BF, 0, None),       # no slot, experts of a table
+    (3, 3000, 3, 1300, 8, BF, 0, 0.9),      # several experts a thread, ranks before
+    (1, 132000, 8, 200, 8, BF, 0, None),    # an expert's tiles take two passes of its scan
 ]
 
 
