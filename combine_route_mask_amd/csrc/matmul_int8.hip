@@ -49,6 +49,7 @@ __device__ __forceinline__ void expert_rows(const moe_ep_matmul_args &a, int e, 
 }
 
 constexpr int kBand = 4;
+constexpr int kUnit = 64; // tiles begin this many rows apart, or a multiple
 
 // The workgroup's tile: up to BM rows of one expert and one of its `ntiles`
 // channel tiles, found by each wave from the offsets (the host does not know
@@ -101,8 +102,11 @@ __device__ __forceinline__ Tile find_tile(const moe_ep_matmul_args &a, int ntile
     if (t.n >= ntiles)
         return t;
     t.expert = base + l;
-    t.first = (int64_t)__builtin_amdgcn_readlane(lo, l) + (int64_t)(band * kBand + in % height) * BM;
-    t.last = min((int64_t)__builtin_amdgcn_readlane(hi, l), t.first + BM);
+    const int begin = __builtin_amdgcn_readlane(lo, l), end = __builtin_amdgcn_readlane(hi, l);
+    const int units = (int)(((int64_t)end - begin + kUnit - 1) / kUnit), each = units / tiles, more = units % tiles;
+    const int row = band * kBand + in % height; // row tiles of each + 1 units, `more` of them, then of each
+    t.first = begin + (int64_t)(row * each + min(row, more)) * kUnit;
+    t.last = min((int64_t)end, t.first + (each + (row < more)) * kUnit);
     return t;
 }
 
@@ -273,16 +277,19 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
     // LDS rows are 128 bytes, all on the same banks: chunk c of row r lies at
     // place c ^ (r & 7), so that 8 rows' reads of one chunk cover all banks.
     // Within a wave's 16 FN channels LDS row 16 i + r holds channel
-    // 4 FN (r / 4) + 4 i + r % 4: a lane's results then are 4 FN channels in
-    // a row.  Channels and rows past the last read the last's and are not
-    // stored.
+    // 16 V (i / V) + 4 V (r / 4) + 4 (i % V) + r % 4: V fragments then give a
+    // lane the channels of one 16-byte store, and the four lanes of a row
+    // store 64 bytes in a row.  Channels and rows past the last read the
+    // last's and are not stored.
+    constexpr int V = RowType<T>::kPer / 4; // results of 4 channels in a 16-byte store
+    static_assert(FN % V == 0);
     const int sub = lane / 8;
     const uint32_t chunk = (uint32_t)((lane % 8) ^ sub) * 16;
     const int nlast = min(S::BN, a.n - n0) - 1, mlast = (int)(t.last - t.first) - 1;
 #pragma unroll
     for (int i = 0; i < S::LN; ++i) {
         const int row = (i * S::W + o.wave) * 8 + sub, r = row & 15;
-        const int n = row / (16 * FN) * (16 * FN) + 4 * FN * (r >> 2) + 4 * (row / 16 % FN) + (r & 3);
+        const int n = (row / (16 * V)) * (16 * V) + 4 * V * (r >> 2) + 4 * (row / 16 % V) + (r & 3);
         o.wo[i] = (uint32_t)min(n, nlast) * (uint32_t)a.k + chunk;
     }
 #pragma unroll
@@ -336,13 +343,12 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
     wait_barrier<0>(); // nothing is on its way into LDS
     // Rows of any n start at any element: 16-byte stores need no more than an
     // element's alignment.
-    constexpr int V = RowType<T>::kPer / 4; // results of 4 channels in a 16-byte store
     const float *scales = a.w_scales + (int64_t)t.expert * a.n;
-    const int nw = n0 + wn + 4 * FN * l4; // the lane's first channel
+    const int nw = n0 + wn + 4 * V * l4; // the lane's first channel
     f32x4 sw[FN];
 #pragma unroll
     for (int i = 0; i < FN; ++i) {
-        const int n = nw + 4 * i;
+        const int n = nw + 16 * V * (i / V) + 4 * (i % V);
         if (n + 4 <= a.n) {
             sw[i] = *reinterpret_cast<const f32x4 *>(scales + n);
         } else {
@@ -359,18 +365,18 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
         uint8_t *out = static_cast<uint8_t *>(a.out) + (m * a.n + nw) * RowType<T>::kBytes;
 #pragma unroll
         for (int i = 0; i < FN; i += V) {
-            const int n = nw + 4 * i;
+            const int n = nw + 16 * i;
             float y[4 * V];
 #pragma unroll
             for (int e = 0; e < 4 * V; ++e)
                 y[e] = (float)acc[i + e / 4][j][e % 4] * (sx[j] * sw[i + e / 4][e % 4]);
             if (n + 4 * V <= a.n) {
-                *reinterpret_cast<AnyAligned *>(out + 4 * i * RowType<T>::kBytes) = RowType<T>::pack(y);
+                *reinterpret_cast<AnyAligned *>(out + 16 * i * RowType<T>::kBytes) = RowType<T>::pack(y);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4 * V; ++e)
                     if (n + e < a.n)
-                        store_element<T>(out + (4 * i + e) * RowType<T>::kBytes, y[e]);
+                        store_element<T>(out + (16 * i + e) * RowType<T>::kBytes, y[e]);
             }
         }
     }
