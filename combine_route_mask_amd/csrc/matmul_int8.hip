@@ -333,9 +333,10 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
     for (int i = 0; i < kAhead; ++i)
         read_w<S>(cur, o, f, i);
     int at = (start + S::STAGES) % steps;
-    // the loads behind the last step are not read
+    // the loads behind the last step are not read, nor do they reach memory
     for (int i = 0; i < steps; ++i) {
-        tile_step<S>(cur, next, cur, at * kTileK, at == steps - 1 ? end : 0, o, f, acc, g);
+        const uint32_t past = i >= steps - S::STAGES ? kPastEnd : at == steps - 1 ? end : 0;
+        tile_step<S>(cur, next, cur, at * kTileK, past, o, f, acc, g);
         at = at + 1 == steps ? 0 : at + 1;
         cur = next;
         next = next == lds + (S::STAGES - 1) * S::BYTES ? lds : next + S::BYTES;
