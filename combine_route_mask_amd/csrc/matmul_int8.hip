@@ -15,7 +15,7 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 AnyAligned __attribute__((aligned(2)));
-typedef float f32x4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 struct Tile {
     int expert;          // -1: no such tile
@@ -51,64 +51,78 @@ __device__ __forceinline__ void expert_rows(const moe_ep_matmul_args &a, int e, 
 constexpr int kBand = 4;
 constexpr int kUnit = 64; // tiles begin this many rows apart, or a multiple
 
-// The workgroup's tile: up to BM rows of one expert and one of its `ntiles`
-// channel tiles, found by each wave from the offsets (the host does not know
-// them).  Tiles are numbered by expert, band of kBand row tiles, channel
+// Finds a workgroup's tiles: up to BM rows of one expert and one of its
+// `ntiles` channel tiles, by each wave from the offsets (the host does not
+// know them).  Tiles are numbered by expert, band of kBand row tiles, channel
 // tile, row tile, and each of the eight XCDs (workgroup number modulo 8) takes
 // a run of them: the tiles that run at a time on its 32 CUs are 4 x 8, which
 // read the least through its L2 (8192 x 8192 x 8192: 444 us; in columns of all
-// row tiles 512 us, bands of 6 and 8 456).
+// row tiles 512 us, bands of 6 and 8 456).  An expert's row tiles are of even
+// height.
 template <int BM>
-__device__ __forceinline__ Tile find_tile(const moe_ep_matmul_args &a, int ntiles)
-{
-    Tile t = {-1, 0, 0, 0};
-    const int lane = threadIdx.x & 63, slot = blockIdx.x >> 3;
-    // lane l sums the experts l * share ..; then the lane that holds the
-    // tile is looked into, one expert a lane
-    const int share = (a.num_experts + 63) / 64;
-    int lo = 0, hi = 0, n = 0;
-    for (int i = 0; i < share; ++i) {
-        expert_rows(a, lane * share + i, lo, hi);
-        n += (hi - lo + BM - 1) / BM;
+struct TileFinder {
+    int lane, ntiles, share, per, total, first;
+    int lo, hi, n, start; // of the lane's experts
+
+    // lane l sums the experts l * share ..; a tile's lane is then looked
+    // into, one expert a lane
+    __device__ __forceinline__ TileFinder(const moe_ep_matmul_args &a, int ntiles_) : ntiles(ntiles_)
+    {
+        lane = threadIdx.x & 63;
+        share = (a.num_experts + 63) / 64;
+        n = 0;
+        for (int i = 0; i < share; ++i) {
+            expert_rows(a, lane * share + i, lo, hi);
+            n += (hi - lo + BM - 1) / BM;
+        }
+        const int sum = prefix_sum(n, lane);
+        total = __builtin_amdgcn_readlane(sum, 63) * ntiles;
+        per = (total + 7) / 8;
+        first = (int)(blockIdx.x & 7) * per;
+        start = (sum - n) * ntiles;
     }
-    const int sum = prefix_sum(n, lane);
-    const int total = __builtin_amdgcn_readlane(sum, 63) * ntiles, per = (total + 7) / 8;
-    const int at = (int)(blockIdx.x & 7) * per + slot;
-    if (slot >= per || at >= total)
-        return t;
-    int start = (sum - n) * ntiles;
-    uint64_t hit = __ballot(at >= start && at < start + n * ntiles);
-    if (!hit) // offsets that do not ascend: no tile, and nothing out of range
-        return t;
-    int l = __builtin_ctzll(hit), base = 0;
-    if (share > 1) {
-        start = __builtin_amdgcn_readlane(start, l);
-        base = l * share;
-        lo = hi = 0;
-        if (lane < share)
-            expert_rows(a, base + lane, lo, hi);
-        n = (hi - lo + BM - 1) / BM;
-        start += (prefix_sum(n, lane) - n) * ntiles;
-        hit = __ballot(at >= start && at < start + n * ntiles);
-        if (!hit)
+
+    __device__ __forceinline__ Tile tile(const moe_ep_matmul_args &a, int slot) const
+    {
+        Tile t = {-1, 0, 0, 0};
+        const int at = first + slot;
+        if (slot >= per || at >= total)
             return t;
-        l = __builtin_ctzll(hit);
+        uint64_t hit = __ballot(at >= start && at < start + n * ntiles);
+        if (!hit) // offsets that do not ascend: no tile, and nothing out of range
+            return t;
+        int l = __builtin_ctzll(hit), base = 0;
+        int elo = lo, ehi = hi, en = n, estart = start;
+        if (share > 1) {
+            estart = __builtin_amdgcn_readlane(start, l);
+            base = l * share;
+            elo = ehi = 0;
+            if (lane < share)
+                expert_rows(a, base + lane, elo, ehi);
+            en = (ehi - elo + BM - 1) / BM;
+            estart += (prefix_sum(en, lane) - en) * ntiles;
+            hit = __ballot(at >= estart && at < estart + en * ntiles);
+            if (!hit)
+                return t;
+            l = __builtin_ctzll(hit);
+        }
+        const int tiles = __builtin_amdgcn_readlane(en, l), here = at - __builtin_amdgcn_readlane(estart, l);
+        const int band = here / (kBand * ntiles), height = min(kBand, tiles - band * kBand);
+        const int in = here - band * kBand * ntiles;
+        if (height < 1)
+            return t;
+        t.n = in / height;
+        if (t.n >= ntiles)
+            return t;
+        t.expert = base + l;
+        const int begin = __builtin_amdgcn_readlane(elo, l), end = __builtin_amdgcn_readlane(ehi, l);
+        const int units = (int)(((int64_t)end - begin + kUnit - 1) / kUnit), each = units / tiles, more = units % tiles;
+        const int row = band * kBand + in % height; // row tiles of each + 1 units, `more` of them, then of each
+        t.first = begin + (int64_t)(row * each + min(row, more)) * kUnit;
+        t.last = min((int64_t)end, t.first + (each + (row < more)) * kUnit);
+        return t;
     }
-    const int tiles = __builtin_amdgcn_readlane(n, l), here = at - __builtin_amdgcn_readlane(start, l);
-    const int band = here / (kBand * ntiles), height = min(kBand, tiles - band * kBand), in = here - band * kBand * ntiles;
-    if (height < 1)
-        return t;
-    t.n = in / height;
-    if (t.n >= ntiles)
-        return t;
-    t.expert = base + l;
-    const int begin = __builtin_amdgcn_readlane(lo, l), end = __builtin_amdgcn_readlane(hi, l);
-    const int units = (int)(((int64_t)end - begin + kUnit - 1) / kUnit), each = units / tiles, more = units % tiles;
-    const int row = band * kBand + in % height; // row tiles of each + 1 units, `more` of them, then of each
-    t.first = begin + (int64_t)(row * each + min(row, more)) * kUnit;
-    t.last = min((int64_t)end, t.first + (each + (row < more)) * kUnit);
-    return t;
-}
+};
 
 // At most this many row tiles, whatever the offsets: each expert with rows
 // has at most one that is not full.
@@ -117,15 +131,6 @@ inline int64_t most_tiles(const moe_ep_matmul_args &a, int64_t bm)
     const int64_t full = a.num_rows / bm;
     return a.offsets ? full + (a.num_rows < a.num_experts ? a.num_rows : a.num_experts)
                      : (a.num_rows + bm - 1) / bm;
-}
-
-// One workgroup a tile, in eight runs of the same length; false when there
-// are more than a grid of 32-bit thread numbers holds.
-inline bool tile_grid(int64_t tiles, int threads, dim3 &grid)
-{
-    tiles = (tiles + 7) / 8 * 8;
-    grid = dim3((unsigned)tiles);
-    return tiles * threads <= INT32_MAX;
 }
 
 template <typename T>
@@ -165,6 +170,16 @@ __device__ __forceinline__ void load_lds(const int8_t *base, uint32_t offset, in
 #endif
 }
 
+// 4 bytes a lane, as above.
+__device__ __forceinline__ void load_lds_word(const float *base, uint32_t offset, uint8_t *to)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    const __amdgpu_buffer_rsrc_t rsrc =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(base), 0, 0x7FFFFFFF, 0x00027000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void *)to, 4, offset, 0, 0, 0);
+#endif
+}
+
 // Waits until at most N of the wave's loads are on their way and all its LDS
 // reads are back, then for the other waves.
 template <int N>
@@ -176,14 +191,16 @@ __device__ __forceinline__ void wait_barrier()
     asm volatile("" ::: "memory");
 }
 
-// A workgroup's operands: where a thread's rows start, and where the wave's
-// first fragments lie in a stage.
+// A tile's operands: where a thread's rows start, and where the wave's first
+// fragments lie in a stage.
 template <typename S>
 struct Operands {
     const int8_t *wp, *xp;
     uint32_t wo[S::LN], xo[S::LM];
     int wave;
     uint32_t wat[2], xat[2];
+    int steps, start; // steps of k, and the first of them
+    uint32_t end;     // kPastEnd where the lane's chunk of the last step is past k
 };
 
 template <typename S>
@@ -265,7 +282,7 @@ __device__ __forceinline__ void tile_step(const uint8_t *__restrict__ cur, const
 }
 
 template <typename T, typename S>
-__device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const Tile &t, uint8_t *lds)
+__device__ __forceinline__ Operands<S> find_operands(const moe_ep_matmul_args &a, const Tile &t)
 {
     constexpr int FN = S::FN, FM = S::FM;
     const int n0 = t.n * S::BN;
@@ -302,62 +319,86 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
         o.wat[h] = place + wn * kTileK;
         o.xat[h] = place + (S::BN + wm) * kTileK;
     }
-    float sx[FM];
-#pragma unroll
-    for (int j = 0; j < FM; ++j)
-        sx[j] = a.x_scales[min(t.first + wm + 16 * j + l16, t.last - 1)];
-    i32x4 acc[FN][FM] = {};
-    Fragments<S> f, g;
-    const int steps = (a.k + kTileK - 1) / kTileK;
+    o.steps = (a.k + kTileK - 1) / kTileK;
     // of the last step, a lane's chunk past the end of k is zeros
-    const uint32_t end = (steps - 1) * kTileK + chunk < (uint32_t)a.k ? 0 : kPastEnd;
+    o.end = (o.steps - 1) * kTileK + chunk < (uint32_t)a.k ? 0 : kPastEnd;
     // k starts elsewhere in each channel tile and goes round: rows a power of
     // two apart would otherwise have all workgroups read the same few memory
     // channels at a time (64 rows, 32 experts, N = K = 4096: 106 us all from
     // k = 0, 79 us)
-    const int start = (int)((uint32_t)(t.expert * ((a.n + S::BN - 1) / S::BN) + t.n) % (uint32_t)steps);
-    constexpr int L = S::LN + S::LM;
+    o.start = (int)((uint32_t)(t.expert * ((a.n + S::BN - 1) / S::BN) + t.n) % (uint32_t)o.steps);
+    return o;
+}
+
+// The loads of a tile's scales (channels, then rows; a wave takes 64 of them)
+// and first stages.
+template <typename T, typename S>
+__device__ __forceinline__ void load_first(const moe_ep_matmul_args &a, const Tile &t, uint8_t *lds, uint8_t *scales)
+{
+    const Operands<S> o = find_operands<T, S>(a, t);
+    constexpr int NWAVES = S::BN / 64, MWAVES = (S::BM + 63) / 64;
+    static_assert(S::BN % 64 == 0 && NWAVES + MWAVES <= S::W);
+    const int lane = threadIdx.x & 63, n0 = t.n * S::BN;
+    if (o.wave < NWAVES)
+        load_lds_word(a.w_scales + (int64_t)t.expert * a.n + n0, 4 * min(64 * o.wave + lane, a.n - n0 - 1),
+                      scales + 256 * o.wave);
+    else if (o.wave < NWAVES + MWAVES)
+        load_lds_word(a.x_scales + t.first, 4 * min(64 * (o.wave - NWAVES) + lane, (int)(t.last - t.first) - 1),
+                      scales + 256 * o.wave);
 #pragma unroll
     for (int st = 0; st < S::STAGES; ++st) {
-        const int at = (start + st) % steps;
+        const int at = (o.start + st) % o.steps;
 #pragma unroll
-        for (int i = 0; i < L; ++i)
-            load_part<S>(lds + st * S::BYTES, o, i, at * kTileK, at == steps - 1 ? end : 0);
+        for (int i = 0; i < S::LN + S::LM; ++i)
+            load_part<S>(lds + st * S::BYTES, o, i, at * kTileK, at == o.steps - 1 ? o.end : 0);
     }
-    wait_barrier<(S::STAGES - 1) * L>();
+}
+
+// Tile t, whose scales and first stages are on their way.  `ahead` sends off
+// the next tile's once this one's LDS is free: they pass while the results are
+// scaled and stored.
+template <typename T, typename S, typename AHEAD>
+__device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const Tile &t, uint8_t *lds,
+                                              const uint8_t *scales, AHEAD ahead)
+{
+    constexpr int FN = S::FN, FM = S::FM;
+    constexpr int V = RowType<T>::kPer / 4;
+    const Operands<S> o = find_operands<T, S>(a, t);
+    const int steps = o.steps, n0 = t.n * S::BN;
+    const int lane = threadIdx.x & 63, l16 = lane & 15, l4 = lane >> 4;
+    const int wn = (o.wave % S::NW) * FN * 16, wm = (o.wave / S::NW) * FM * 16;
+    i32x4 acc[FN][FM] = {};
+    Fragments<S> f, g;
     uint8_t *cur = lds, *next = lds + S::BYTES;
+    wait_barrier<(S::STAGES - 1) * (S::LN + S::LM)>();
 #pragma unroll
     for (int j = 0; j < FM; ++j)
         read_x<S>(cur, o, f, 0, j);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
         read_w<S>(cur, o, f, i);
-    int at = (start + S::STAGES) % steps;
+    int at = (o.start + S::STAGES) % steps;
     // the loads behind the last step are not read, nor do they reach memory
     for (int i = 0; i < steps; ++i) {
-        const uint32_t past = i >= steps - S::STAGES ? kPastEnd : at == steps - 1 ? end : 0;
+        const uint32_t past = i >= steps - S::STAGES ? kPastEnd : at == steps - 1 ? o.end : 0;
         tile_step<S>(cur, next, cur, at * kTileK, past, o, f, acc, g);
         at = at + 1 == steps ? 0 : at + 1;
         cur = next;
         next = next == lds + (S::STAGES - 1) * S::BYTES ? lds : next + S::BYTES;
     }
-    wait_barrier<0>(); // nothing is on its way into LDS
+    wait_barrier<0>(); // all waves are done with LDS, and nothing is on its way there
+    const int wl = wn + 4 * V * l4, nw = n0 + wl; // the lane's first channel
+    f32x4 sw[FN];
+    float sx[FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+        sw[i] = *reinterpret_cast<const f32x4 *>(scales + 4 * (wl + 16 * V * (i / V) + 4 * (i % V)));
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+        sx[j] = *reinterpret_cast<const float *>(scales + 4 * (S::BN + wm + 16 * j + l16));
+    ahead();
     // Rows of any n start at any element: 16-byte stores need no more than an
     // element's alignment.
-    const float *scales = a.w_scales + (int64_t)t.expert * a.n;
-    const int nw = n0 + wn + 4 * V * l4; // the lane's first channel
-    f32x4 sw[FN];
-#pragma unroll
-    for (int i = 0; i < FN; ++i) {
-        const int n = nw + 16 * V * (i / V) + 4 * (i % V);
-        if (n + 4 <= a.n) {
-            sw[i] = *reinterpret_cast<const f32x4 *>(scales + n);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                sw[i][e] = n + e < a.n ? scales[n + e] : 0.0f;
-        }
-    }
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
         const int64_t m = t.first + wm + 16 * j + l16;
@@ -385,16 +426,16 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
 
 // The tile's rows choose among the shapes, smallest first: the last rows of
 // an expert do not pay for rows that are not there.
-template <typename T, typename S, typename... MORE>
-__device__ __forceinline__ void multiply_shaped(const moe_ep_matmul_args &a, const Tile &t, uint8_t *lds)
+template <typename S, typename... MORE, typename F>
+__device__ __forceinline__ void with_shape(const Tile &t, F f)
 {
     if constexpr (sizeof...(MORE) == 0) {
-        multiply_tile<T, S>(a, t, lds);
+        f(S{});
     } else {
         if (t.last - t.first <= S::BM)
-            multiply_tile<T, S>(a, t, lds);
+            f(S{});
         else
-            multiply_shaped<T, MORE...>(a, t, lds);
+            with_shape<MORE...>(t, f);
     }
 }
 
@@ -406,24 +447,54 @@ constexpr int largest(int x, MORE... more)
     return x > largest(more...) ? x : largest(more...);
 }
 
+// Bytes of a tile's scales.
+template <typename S, typename... MORE>
+constexpr int tile_scales()
+{
+    return 256 * largest(S::BN / 64 + (S::BM + 63) / 64, (MORE::BN / 64 + (MORE::BM + 63) / 64)...);
+}
+
+// A workgroup takes the tiles `slot`, slot + (workgroups of the XCD), ... of
+// its XCD's run.
 template <typename T, typename S, typename... MORE>
 __global__ __launch_bounds__(S::THREADS, 2) void matmul_tile_kernel(moe_ep_matmul_args a, int ntiles)
 {
     __shared__ __align__(16) uint8_t lds[largest(S::STAGES * S::BYTES, (MORE::STAGES * MORE::BYTES)...)];
-    const Tile t = find_tile<largest(S::BM, MORE::BM...)>(a, ntiles);
+    // this tile's and the next one's
+    __shared__ __align__(16) uint8_t scales[2][tile_scales<S, MORE...>()];
+    const TileFinder<largest(S::BM, MORE::BM...)> find(a, ntiles);
+    int slot = (int)(blockIdx.x >> 3);
+    Tile t = find.tile(a, slot);
     if (t.expert < 0)
         return;
-    multiply_shaped<T, S, MORE...>(a, t, lds);
+    with_shape<S, MORE...>(t, [&](auto shape) { load_first<T, decltype(shape)>(a, t, lds, scales[0]); });
+    for (int turn = 0; t.expert >= 0; turn ^= 1) {
+        slot += (int)(gridDim.x >> 3);
+        const Tile next = find.tile(a, slot);
+        with_shape<S, MORE...>(t, [&](auto shape) {
+            multiply_tile<T, decltype(shape)>(a, t, lds, scales[turn], [&] {
+                if (next.expert >= 0)
+                    with_shape<S, MORE...>(next, [&](auto ahead) {
+                        load_first<T, decltype(ahead)>(a, next, lds, scales[turn ^ 1]);
+                    });
+            });
+        });
+        t = next;
+    }
 }
 
+// As many workgroups as the LDS of 256 CUs holds, at most one a tile, in
+// eight runs of the same length.
 template <typename S, typename... MORE>
 hipError_t tile_launch(const moe_ep_matmul_args &a, hipStream_t s)
 {
+    constexpr int kLds = largest(S::STAGES * S::BYTES, (MORE::STAGES * MORE::BYTES)...) + 2 * tile_scales<S, MORE...>();
     const int64_t ntiles = (a.n + S::BN - 1) / S::BN;
-    dim3 grid;
-    if (!tile_grid(most_tiles(a, largest(S::BM, MORE::BM...)) * ntiles, S::THREADS, grid))
+    const int64_t tiles = most_tiles(a, largest(S::BM, MORE::BM...)) * ntiles;
+    if (tiles > INT32_MAX - 8) // they are numbered in 32 bits
         return hipErrorInvalidConfiguration;
-    const dim3 block(S::THREADS);
+    const int64_t run = (tiles + 7) / 8, resident = 32 * (160 * 1024 / kLds);
+    const dim3 grid((unsigned)(8 * (run < resident ? run : resident))), block(S::THREADS);
     if (a.out_type == MOE_EP_BF16_ROWS)
         hipLaunchKernelGGL((matmul_tile_kernel<Bf16, S, MORE...>), grid, block, 0, s, a, (int)ntiles);
     else
@@ -438,20 +509,21 @@ hipError_t tile_launch(const moe_ep_matmul_args &a, hipStream_t s)
 // Times in us, E experts of N x K, ragged rows:
 //  - up to 256 x 256, eight waves, one workgroup a CU: the fewest bytes for
 //    its products; wins over 128 x 128 from about 112 rows on where there are
-//    tiles for the CUs and k is long enough for its first and last step.
-//    E 32, 4096 x 4096: 128 rows 135 / 153, 256 rows 231 / 227, 512 rows
-//    312 / 367; E 32, 2048 x 4096, 192 rows 72 / 87; E 1, 7168 x 7168, 1024
-//    rows (112 tiles) 82 / 56.  With k = 2048 only while an expert fits one
-//    tile: E 8, 7168 x 2048, 128 rows 30 / 38, 512 rows 99 / 77; never with
-//    k = 1024 (E 32, N 4096, 1024 rows 245 / 228);
+//    tiles for the CUs.  E 32, 4096 x 4096: 128 rows 126 / 147, 256 rows
+//    215 / 212, 512 rows 296 / 359, 1024 rows 533 / 643; E 1, 7168 x 7168,
+//    1024 rows (112 tiles) 82 / 56.  With a shorter k only while an expert
+//    fits one tile, or with at least two a expert and three rounds of the
+//    CUs: E 8, 7168 x 2048: 128 rows 28 / 32, 256 rows 59 / 46, 512 rows (448
+//    tiles) 89 / 74, 1024 rows 123 / 136; E 32, 4096 x 1024: 160 rows 39 / 48,
+//    256 rows 66 / 58, 512 rows 111 / 122;
 //  - up to 128 x 128, four waves, two workgroups a CU; for at most 32 rows an
 //    expert its 64-row shape with three stages in place of two: E 32,
-//    4096 x 4096, 1 row 68 / 79, but 64 rows 124 / 110;
+//    4096 x 4096, 1 row 66 / 76, but 64 rows 114 / 105;
 //  - up to 64 x 64, four waves, three workgroups a CU, three stages, or four
-//    for up to 32 rows: where 128 x 128 has not 200 tiles (E 1, 4096 x 4096,
-//    256 rows 11 / 19; E 1, 7168 x 7168, 1 row 13 / 32), and for a few rows
-//    against long weights, where only the bytes in flight count (64 rows, E 32,
-//    4096 x 7168: 137 / 145; but E 64, 1024 x 2048, 2 rows 24 / 23).
+//    for up to 32 rows: where 128 x 128 has not 200 tiles (E 1, 7168 x 7168,
+//    256 rows 25 / 40, 1 row 13 / 33), and for a few rows against long
+//    weights, where only the bytes in flight count (E 8, 4096 x 7168, 1 row
+//    27 / 28; 64 rows over E 32, 4096 x 7168: 133 / 141).
 hipError_t launch_expert_matmul(const moe_ep_matmul_args &a, hipStream_t s)
 {
     using T64 = TileShape<2, 2, 2, 2, 3>;
@@ -465,7 +537,8 @@ hipError_t launch_expert_matmul(const moe_ep_matmul_args &a, hipStream_t s)
         return tile_launch<T64Few, T64>(a, s);
     if (average <= 32)
         return tile_launch<TileShape<2, 2, 4, 2, 3>, T128>(a, s);
-    if (average >= 112 && tiles(256) >= 200 && (a.k >= 4096 || (a.k >= 1536 && average < 224)))
+    if (average >= 112 && tiles(256) >= 200 &&
+        (a.k >= 4096 || (a.k >= 1024 && (average < 224 || (average >= 448 && tiles(256) >= 768)))))
         return tile_launch<TileShape<4, 2, 4, 2, 2>, TileShape<4, 2, 4, 4, 2>, TileShape<2, 4, 8, 3, 2>,
                            TileShape<2, 4, 8, 4, 2>>(a, s);
     return tile_launch<TileShape<2, 2, 4, 2, 2>, T128>(a, s);
