@@ -418,45 +418,66 @@ __global__ __launch_bounds__(kTileBlock) void sort_place_kernel(moe_ep_sort_args
 
 // ---------------------------------------------------------------------------
 // Sorts in between: each rank's pairs fit one workgroup's registers, so one
-// launch of a workgroup a rank counts, scans and places them within the rank
-// (the gather adds the pairs of the ranks before).  8 ranks of 1024 slots,
-// top_k 8: 9 us, where the three launches for large sorts take 17 (one
-// workgroup for 32768 pairs takes 30 us, the three launches 14).
+// launch counts, scans and places them within the rank (the gather adds the
+// pairs of the ranks before).  A workgroup counts all of its rank's pairs and
+// places 2048 of them.  With the gather's launch, 8 ranks of 1024 slots, top_k
+// 8, take 9.0 us, where one workgroup a rank takes 11.5 and the three launches
+// for large sorts 13.1; for twice the pairs 12.4 against 14.3, but with room
+// for them 9.5 at 1024 slots, and 64 ranks then take 35 us against 29.
 // ---------------------------------------------------------------------------
 
 constexpr int kPlanBlock = 1024;
 constexpr int kPlanWaves = kPlanBlock / 64;
+constexpr int kPlanPart = 2048; // pairs that a workgroup places
 
 // ws: totals [ranks], then places within the rank [ranks][slots * k].
-__global__ __launch_bounds__(kPlanBlock) void sort_plan_kernel(moe_ep_sort_args a, int bits)
+__global__ __launch_bounds__(kPlanBlock) void sort_plan_kernel(moe_ep_sort_args a, int parts, int bits)
 {
-    constexpr int IT = kSortPlanPairs / kPlanBlock;
-    extern __shared__ int32_t next[]; // [waves][epr], then [waves] sums
-    const int r = blockIdx.x, epr = a.experts_per_rank, pairs = a.slots * a.top_k;
+    constexpr int IT = kPlanPart / kPlanBlock, OTHERS = kSortPlanPairs / kPlanBlock;
+    extern __shared__ int32_t next[]; // [waves][epr], [2][epr] of the parts before and behind, [waves] sums
+    const int r = blockIdx.x / parts, part = blockIdx.x % parts, epr = a.experts_per_rank, pairs = a.slots * a.top_k;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int32_t *sums = next + kPlanWaves * epr, *mine = next + wave * epr;
+    int32_t *others = next + kPlanWaves * epr, *sums = others + 2 * epr, *mine = next + wave * epr;
     const int32_t *ids = rank_ids(a, r);
-    const int share = ((pairs + kPlanWaves - 1) / kPlanWaves + 63) & ~63, first = wave * share;
-    int e[IT]; // wave w takes the pairs from w * share on, 64 at a time
+    const int lo = part * kPlanPart, first = lo + wave * (IT * 64);
+    int e[IT]; // wave w takes the part's pairs from w * 64 IT on, 64 at a time
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int p = first + i * 64 + lane;
-        e[i] = i * 64 < share && p < pairs ? local_expert(a, ids[p], r) : -1;
+        e[i] = p < pairs ? local_expert(a, ids[p], r) : -1;
     }
-    for (int x = threadIdx.x; x < kPlanWaves * epr; x += kPlanBlock)
+    int other[OTHERS];
+    if (parts > 1) {
+#pragma unroll
+        for (int i = 0; i < OTHERS; ++i) {
+            const int p = i * kPlanBlock + threadIdx.x;
+            other[i] = p < pairs && p / kPlanPart != part ? local_expert(a, ids[p], r) : -1;
+        }
+    }
+    for (int x = threadIdx.x; x < (kPlanWaves + 2) * epr; x += kPlanBlock)
         next[x] = 0;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < IT; ++i)
         if (e[i] >= 0)
             atomicAdd(&mine[e[i]], 1);
+    if (parts > 1) {
+#pragma unroll
+        for (int i = 0; i < OTHERS; ++i)
+            if (other[i] >= 0)
+                atomicAdd(&others[(i * kPlanBlock < lo ? 0 : epr) + other[i]], 1);
+    }
     __syncthreads();
-    // thread x: the pairs of expert x in each wave's share, then those of
-    // the experts before
-    int count = 0;
-    if ((int)threadIdx.x < epr)
+    // thread x: the pairs of expert x in each wave's share and the other
+    // parts, then those of the experts before
+    int count = 0, ahead = 0;
+    if ((int)threadIdx.x < epr) {
+        ahead = others[threadIdx.x];
+        count = ahead + others[epr + threadIdx.x];
+#pragma unroll
         for (int w = 0; w < kPlanWaves; ++w)
             count += next[w * epr + threadIdx.x];
+    }
     int before = count;
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
@@ -472,12 +493,13 @@ __global__ __launch_bounds__(kPlanBlock) void sort_plan_kernel(moe_ep_sort_args 
             before += total;
         total += sums[w];
     }
-    before -= count;
+    before += ahead - count;
     int32_t *ws = static_cast<int32_t *>(a.workspace);
-    if (threadIdx.x == 0)
+    if (part == 0 && threadIdx.x == 0)
         ws[r] = total;
     if ((int)threadIdx.x < epr) {
-        a.counts[r * epr + threadIdx.x] = count;
+        if (part == 0)
+            a.counts[r * epr + threadIdx.x] = count;
         for (int w = 0; w < kPlanWaves; ++w) {
             const int c = next[w * epr + threadIdx.x];
             next[w * epr + threadIdx.x] = before;
@@ -488,12 +510,10 @@ __global__ __launch_bounds__(kPlanBlock) void sort_plan_kernel(moe_ep_sort_args 
     int32_t *places = ws + a.ranks + (int64_t)r * pairs;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-        if (i * 64 < share) {
-            const int place = place_pairs(e[i], bits, lane, mine);
-            const int p = first + i * 64 + lane;
-            if (p < pairs)
-                places[p] = place;
-        }
+        const int place = place_pairs(e[i], bits, lane, mine);
+        const int p = first + i * 64 + lane;
+        if (p < pairs)
+            places[p] = place;
     }
 }
 
@@ -848,8 +868,9 @@ hipError_t launch_expert_sort(const moe_ep_sort_args &a, hipStream_t s)
         ++bits;
     const bool planned = sort_is_planned(a.slots, a.top_k, epr);
     if (planned) {
-        const size_t lds = (size_t)(kPlanWaves * epr + kPlanWaves) * 4;
-        hipLaunchKernelGGL(sort_plan_kernel, dim3(a.ranks), dim3(kPlanBlock), lds, s, a, bits);
+        const int parts = (a.slots * a.top_k + kPlanPart - 1) / kPlanPart;
+        const size_t lds = (size_t)((kPlanWaves + 2) * epr + kPlanWaves) * 4;
+        hipLaunchKernelGGL(sort_plan_kernel, dim3(a.ranks * parts), dim3(kPlanBlock), lds, s, a, parts, bits);
         if (hipError_t e = hipGetLastError())
             return e;
     } else {
