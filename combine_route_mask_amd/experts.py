@@ -18,6 +18,7 @@ library's code) and launches nothing.
 """
 from __future__ import annotations
 
+import functools
 import struct
 from typing import NamedTuple, Optional
 
@@ -139,6 +140,11 @@ def _no_grad(*tensors):
         _refuse("this call has no gradient: detach its inputs or call it under torch.no_grad()")
 
 
+def _empty(shape, strides, dtype, dev):
+    """A contiguous tensor; 0.4 us less of a call than ``torch.empty``."""
+    return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
+
+
 _device_now = torch._C._cuda_getDevice
 _stream_now = torch._C._cuda_getCurrentRawStream
 
@@ -171,6 +177,7 @@ class _On:
 # expert sort
 # ----------------------------------------------------------------------------
 
+@functools.lru_cache(maxsize=4096)
 def expert_sort_workspace_bytes(ranks: int, slots: int, top_k: int, experts_per_rank: int) -> int:
     if (not 1 <= experts_per_rank <= MAX_SORT_EXPERTS or min(ranks, slots, top_k) < 0
             or max(ranks, slots, top_k) > _INT_MAX):
@@ -239,7 +246,7 @@ def _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, stream, a
     work = expert_sort_workspace_bytes(R, S, k, epr)
     dtype = torch.int8 if quantize else rows.dtype
     if out is None:
-        out = (torch.zeros if zeros else torch.empty)((capacity, X), dtype=dtype, device=dev)
+        out = torch.zeros((capacity, X), dtype=dtype, device=dev) if zeros else _empty((capacity, X), (X, 1), dtype, dev)
     else:
         _flat(out, "out", dev, dtype, (capacity, X))
         _written(out)
@@ -253,9 +260,9 @@ def _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, stream, a
     else:
         out_scales = None
     E = R * epr
-    position = ids.new_empty((R, S, k))
-    offsets = ids.new_empty(E + 1)
-    counts = ids.new_empty(E)
+    position = _empty((R, S, k), (S * k, k, 1), torch.int32, dev)
+    offsets = _empty((E + 1,), (1,), torch.int32, dev)
+    counts = _empty((E,), (1,), torch.int32, dev)
     # held until the launches are on the stream: no other thread's call may take its memory between them
     space = torch.empty(work, dtype=torch.uint8, device=dev) if work else None
     _call(lib.moe_ep_expert_sort, _SORT, dev,
@@ -341,7 +348,7 @@ def _unsort(position, rows, weights, out, keep_empty, stream):
     if out is None:
         if keep_empty:
             _refuse("keep_empty needs a given out")
-        out = rows.new_empty((R, S, H))
+        out = _empty((R, S, H), (S * H, H, 1), rows.dtype, dev)
         stride = S * H * rows.element_size()
     else:
         if out.dtype != rows.dtype or out.shape != (R, S, H):
@@ -457,7 +464,7 @@ def expert_matmul(x, x_scales, weight, weight_scales, *, offsets=None, out=None,
         _flat(weight, "weight", dev, torch.int8, (N, K))
         _flat(weight_scales, "weight_scales", dev, torch.float32, (N,))
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=dev)
+        out = _empty((M, N), (N, 1), dtype, dev)
     else:
         _flat(out, "out", dev, out.dtype, (M, N))
         _written(out)
@@ -489,12 +496,12 @@ def silu_mul_quantize(x, *, offsets=None, out=None, out_scales=None, stream=None
         _flat(offsets, "offsets", dev, torch.int32, offsets.shape)
         last = offsets.data_ptr() + 4 * (offsets.numel() - 1)
     if out is None:
-        out = torch.empty((M, I), dtype=torch.int8, device=dev)
+        out = _empty((M, I), (I, 1), torch.int8, dev)
     else:
         _flat(out, "out", dev, torch.int8, (M, I))
         _written(out)
     if out_scales is None:
-        out_scales = torch.empty(M, dtype=torch.float32, device=dev)
+        out_scales = _empty((M,), (1,), torch.float32, dev)
     else:
         _flat(out_scales, "out_scales", dev, torch.float32, (M,))
         _written(out_scales)
@@ -535,12 +542,12 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, *, format: str = "mxfp8
         _refuse(f"{format} needs a hidden size that is a multiple of {block}, got {H}")
     scale_shape = (M, H // block) if block else (M,)
     if out is None:
-        out = torch.empty((M, H), dtype=row_dtype, device=dev)
+        out = torch.empty_like(x, dtype=row_dtype)
     else:
         _flat(out, "out", dev, row_dtype, (M, H))
         _written(out)
     if out_scales is None:
-        out_scales = torch.empty(scale_shape, dtype=scale_dtype, device=dev)
+        out_scales = _empty(scale_shape, (H // block, 1) if block else (1,), scale_dtype, dev)
     else:
         _flat(out_scales, "out_scales", dev, scale_dtype, scale_shape)
         _written(out_scales)
