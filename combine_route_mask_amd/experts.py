@@ -307,7 +307,9 @@ def expert_unsort(position, rows, weights=None, *, out=None, keep_empty: bool = 
     ``position`` int32 [R, S, k] of the sort, ``rows`` [M, H] bf16 or fp32,
     ``weights`` fp32 [R, S, k] (ranks may lie apart) or None for 1.  Slots
     without a row become zeros, or with ``keep_empty`` (a given ``out``) are
-    left alone, as a combine never reads them.
+    left alone: a combine never reads a slot without a token.  It does read
+    one whose pairs a capacity dropped, so leave ``keep_empty`` off where the
+    sort may drop pairs.
 
     Differentiable in ``rows`` and ``weights`` (without ``out`` or
     ``stream``)."""

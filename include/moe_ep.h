@@ -280,7 +280,8 @@ int moe_ep_reduce_scatterv(int32_t ep_size, const int32_t *sizes, int32_t hidden
  * makes the next layer's payload.  These calls need no handle and keep no
  * state: the caller owns every buffer, launches go to the caller's stream
  * without host synchronisation, nothing is allocated, and a call may be
- * captured into a HIP graph.  Buffers belong to the current HIP device.
+ * captured into a HIP graph.  Buffers belong to the current HIP device; an
+ * output overlaps no other buffer of its call unless stated otherwise.
  * Calls whose output, workspace or index buffers overlap must be ordered by
  * the caller; calls on buffers of their own may run at the same time.
  * Every call takes one argument block, all pointers device pointers.
@@ -359,9 +360,11 @@ int moe_ep_expert_sort(const moe_ep_sort_args *args, void *stream);
  * rows[position[r][q][j]] (weights NULL: 1), fp32 from +0 in ascending j,
  * rounded once to row_type.  Pairs with a position outside [0, num_rows)
  * add nothing; a slot without any is filled with zeros (keep_empty = 0) or
- * left alone (keep_empty = 1: what a combine never reads).  With weights
+ * left alone (keep_empty = 1: a combine never reads a slot without a token,
+ * but it does read one whose pairs a capacity dropped, so that a sort that
+ * may drop pairs goes with 0).  With weights
  * NULL it is the gradient of the expert sort.  hidden_size elements a row, a
- * multiple of 16 bytes up to 2^24; `out` may not overlap `rows`.
+ * multiple of 16 bytes up to 2^24.
  */
 typedef struct moe_ep_unsort_args {
     const int32_t *position;     /* [R][S][k], contiguous                    */
