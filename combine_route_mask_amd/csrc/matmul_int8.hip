@@ -58,10 +58,11 @@ constexpr int kUnit = 64; // tiles begin this many rows apart, or a multiple
 // a run of them: the tiles that run at a time on its 32 CUs are 4 x 8, which
 // read the least through its L2 (8192 x 8192 x 8192: 444 us; in columns of all
 // row tiles 512 us, bands of 6 and 8 456).  An expert's row tiles are of even
-// height.
-template <int BM>
+// height.  Of BM and TALL the finder takes what the CUs are done with first:
+// a tile takes about as long as 76 rows and its own.
+template <int BM, int TALL>
 struct TileFinder {
-    int lane, ntiles, share, per, total, first;
+    int lane, ntiles, share, per, total, first, bm;
     int lo, hi, n, start; // of the lane's experts
 
     // lane l sums the experts l * share ..; a tile's lane is then looked
@@ -71,15 +72,35 @@ struct TileFinder {
         lane = threadIdx.x & 63;
         share = (a.num_experts + 63) / 64;
         n = 0;
+        int tall = 0;
+        float rows = 0.0f;
         for (int i = 0; i < share; ++i) {
             expert_rows(a, lane * share + i, lo, hi);
             n += (hi - lo + BM - 1) / BM;
+            tall += (hi - lo + TALL - 1) / TALL;
+            rows += (float)(hi - lo);
         }
-        const int sum = prefix_sum(n, lane);
+        int sum = prefix_sum(n, lane);
+        bm = BM;
+        if (TALL != BM) {
+            const int sum_tall = prefix_sum(tall, lane);
+            rows = wave_sum(rows);
+            if (time_of(__builtin_amdgcn_readlane(sum_tall, 63), rows) < time_of(__builtin_amdgcn_readlane(sum, 63), rows)) {
+                bm = TALL;
+                n = tall;
+                sum = sum_tall;
+            }
+        }
         total = __builtin_amdgcn_readlane(sum, 63) * ntiles;
         per = (total + 7) / 8;
         first = (int)(blockIdx.x & 7) * per;
         start = (sum - n) * ntiles;
+    }
+
+    // Rounds of 256 CUs times a tile.
+    __device__ __forceinline__ float time_of(int tiles, float rows) const
+    {
+        return tiles ? (float)((tiles * ntiles + 255) / 256) * (76.0f + rows / (float)tiles) : 0.0f;
     }
 
     __device__ __forceinline__ Tile tile(const moe_ep_matmul_args &a, int slot) const
@@ -99,7 +120,7 @@ struct TileFinder {
             elo = ehi = 0;
             if (lane < share)
                 expert_rows(a, base + lane, elo, ehi);
-            en = (ehi - elo + BM - 1) / BM;
+            en = (ehi - elo + bm - 1) / bm;
             estart += (prefix_sum(en, lane) - en) * ntiles;
             hit = __ballot(at >= estart && at < estart + en * ntiles);
             if (!hit)
@@ -330,21 +351,25 @@ __device__ __forceinline__ Operands<S> find_operands(const moe_ep_matmul_args &a
     return o;
 }
 
-// The loads of a tile's scales (channels, then rows; a wave takes 64 of them)
+// The loads of a tile's scales (channels, then rows; 64 of them to a wave)
 // and first stages.
 template <typename T, typename S>
 __device__ __forceinline__ void load_first(const moe_ep_matmul_args &a, const Tile &t, uint8_t *lds, uint8_t *scales)
 {
     const Operands<S> o = find_operands<T, S>(a, t);
-    constexpr int NWAVES = S::BN / 64, MWAVES = (S::BM + 63) / 64;
-    static_assert(S::BN % 64 == 0 && NWAVES + MWAVES <= S::W);
+    constexpr int NPIECES = S::BN / 64, PIECES = NPIECES + (S::BM + 63) / 64;
+    static_assert(S::BN % 64 == 0);
     const int lane = threadIdx.x & 63, n0 = t.n * S::BN;
-    if (o.wave < NWAVES)
-        load_lds_word(a.w_scales + (int64_t)t.expert * a.n + n0, 4 * min(64 * o.wave + lane, a.n - n0 - 1),
-                      scales + 256 * o.wave);
-    else if (o.wave < NWAVES + MWAVES)
-        load_lds_word(a.x_scales + t.first, 4 * min(64 * (o.wave - NWAVES) + lane, (int)(t.last - t.first) - 1),
-                      scales + 256 * o.wave);
+#pragma unroll
+    for (int c = 0; c < PIECES; c += S::W) {
+        const int piece = c + o.wave;
+        if (piece < NPIECES)
+            load_lds_word(a.w_scales + (int64_t)t.expert * a.n + n0, 4 * min(64 * piece + lane, a.n - n0 - 1),
+                          scales + 256 * piece);
+        else if (piece < PIECES)
+            load_lds_word(a.x_scales + t.first, 4 * min(64 * (piece - NPIECES) + lane, (int)(t.last - t.first) - 1),
+                          scales + 256 * piece);
+    }
 #pragma unroll
     for (int st = 0; st < S::STAGES; ++st) {
         const int at = (o.start + st) % o.steps;
@@ -462,7 +487,8 @@ __global__ __launch_bounds__(S::THREADS, 2) void matmul_tile_kernel(moe_ep_matmu
     __shared__ __align__(16) uint8_t lds[largest(S::STAGES * S::BYTES, (MORE::STAGES * MORE::BYTES)...)];
     // this tile's and the next one's
     __shared__ __align__(16) uint8_t scales[2][tile_scales<S, MORE...>()];
-    const TileFinder<largest(S::BM, MORE::BM...)> find(a, ntiles);
+    constexpr int TALL = largest(S::BM, MORE::BM...), BM = TALL > 256 ? 256 : TALL;
+    const TileFinder<BM, TALL> find(a, ntiles);
     int slot = (int)(blockIdx.x >> 3);
     Tile t = find.tile(a, slot);
     if (t.expert < 0)
@@ -490,7 +516,8 @@ hipError_t tile_launch(const moe_ep_matmul_args &a, hipStream_t s)
 {
     constexpr int kLds = largest(S::STAGES * S::BYTES, (MORE::STAGES * MORE::BYTES)...) + 2 * tile_scales<S, MORE...>();
     const int64_t ntiles = (a.n + S::BN - 1) / S::BN;
-    const int64_t tiles = most_tiles(a, largest(S::BM, MORE::BM...)) * ntiles;
+    constexpr int TALL = largest(S::BM, MORE::BM...);
+    const int64_t tiles = most_tiles(a, TALL > 256 ? 256 : TALL) * ntiles;
     if (tiles > INT32_MAX - 8) // they are numbered in 32 bits
         return hipErrorInvalidConfiguration;
     const int64_t run = (tiles + 7) / 8, resident = 32 * (160 * 1024 / kLds);
@@ -507,15 +534,15 @@ hipError_t tile_launch(const moe_ep_matmul_args &a, hipStream_t s)
 // The shape follows from the average rows of an expert (of num_rows, which a
 // caller's capacity may exceed) and from how many tiles there are for 256 CUs.
 // Times in us, E experts of N x K, ragged rows:
-//  - up to 256 x 256, eight waves, one workgroup a CU: the fewest bytes for
-//    its products; wins over 128 x 128 from about 112 rows on where there are
-//    tiles for the CUs.  E 32, 4096 x 4096: 128 rows 126 / 147, 256 rows
-//    215 / 212, 512 rows 296 / 359, 1024 rows 533 / 643; E 1, 7168 x 7168,
-//    1024 rows (112 tiles) 82 / 56.  With a shorter k only while an expert
-//    fits one tile, or with at least two a expert and three rounds of the
-//    CUs: E 8, 7168 x 2048: 128 rows 28 / 32, 256 rows 59 / 46, 512 rows (448
-//    tiles) 89 / 74, 1024 rows 123 / 136; E 32, 4096 x 1024: 160 rows 39 / 48,
-//    256 rows 66 / 58, 512 rows 111 / 122;
+//  - 256 channels x up to 256 or 320 rows, eight waves, one workgroup a CU:
+//    the fewest bytes for its products; wins over 128 x 128 from about 112
+//    rows on where there are tiles for the CUs.  E 32, 4096 x 4096: 96 rows
+//    122 / 112, 112 rows 130 / 144, 256 rows 167 / 215, 512 rows 280 / 360,
+//    1024 rows 532 / 644; E 32, 4096 x 1024: 256 rows 53 / 58, 512 rows
+//    104 / 127; E 1, 7168 x 7168, 1024 rows (112 tiles) 78 / 57.  Not for
+//    k below 1024: E 32, 2048 x 512, 192 rows 21 / 19, 512 rows 37 / 35.
+//    (Up to 256 rows only: E 32, 4096 x 4096, 256 rows 215, 512 rows 297;
+//    an expert somewhat above 256 rows then takes two tiles.);
 //  - up to 128 x 128, four waves, two workgroups a CU; for at most 32 rows an
 //    expert its 64-row shape with three stages in place of two: E 32,
 //    4096 x 4096, 1 row 66 / 76, but 64 rows 114 / 105;
@@ -537,10 +564,9 @@ hipError_t launch_expert_matmul(const moe_ep_matmul_args &a, hipStream_t s)
         return tile_launch<T64Few, T64>(a, s);
     if (average <= 32)
         return tile_launch<TileShape<2, 2, 4, 2, 3>, T128>(a, s);
-    if (average >= 112 && tiles(256) >= 200 &&
-        (a.k >= 4096 || (a.k >= 1024 && (average < 224 || (average >= 448 && tiles(256) >= 768)))))
+    if (average >= 112 && tiles(256) >= 200 && a.k >= 1024)
         return tile_launch<TileShape<4, 2, 4, 2, 2>, TileShape<4, 2, 4, 4, 2>, TileShape<2, 4, 8, 3, 2>,
-                           TileShape<2, 4, 8, 4, 2>>(a, s);
+                           TileShape<2, 4, 8, 4, 2>, TileShape<2, 4, 8, 5, 2>>(a, s);
     return tile_launch<TileShape<2, 2, 4, 2, 2>, T128>(a, s);
 }
 

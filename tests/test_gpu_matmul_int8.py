@@ -72,7 +72,7 @@ CASES = [
     (2100, 4, 16400, 4112, "ragged"), (600, 40, 700, 1040, "ragged"), (3100, 12, 4400, 1552, "ragged"),
     (2600, 20, 1290, 4224, "ragged"),
     # several tiles a workgroup, more experts than a wave has lanes
-    (9000, 100, 1500, 272, "ragged"), (300, 70, 1000, 4112, "ragged"), (14000, 70, 1100, 1040, "ragged"),
+    (9000, 100, 1500, 272, "ragged"), (5100, 17, 3400, 1040, "ragged"), (4900, 16, 3401, 1136, "ragged"), (300, 70, 1000, 4112, "ragged"), (14000, 70, 1100, 1040, "ragged"),
 ]
 
 
