@@ -234,6 +234,46 @@ def test_layer_on_other_streams(X):
             assert _same(g, w)
 
 
+def test_calls_from_several_threads(X):
+    """Threads that launch on the same stream at the same time: a call's
+    workspace is its own until its launches are out, and messages are a
+    thread's own."""
+    import threading
+    from combine_route_mask_amd.moe_ep import MoeEpArgError
+    sizes = [(1, 3000, 4, 40), (4, 500, 3, 8), (1, 2900, 3, 70), (2, 40, 8, 16)]
+    states = []
+    for i, (R, S, k, epr) in enumerate(sizes):
+        ids = U.draw_ids(np.random.default_rng(i), R, S, k, epr)
+        rows = torch.randn((R, S, 64), device="cuda", dtype=BF)
+        states.append((torch.from_numpy(ids).cuda(), rows, epr, X.expert_sort(torch.from_numpy(ids).cuda(), rows, epr)))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        ids, rows, epr, want = states[i]
+        try:
+            for _ in range(40):
+                got = X.expert_sort(ids, rows, epr)
+                m = int(got.offsets[-1])
+                if not (torch.equal(got.position, want.position) and torch.equal(got.rows[:m], want.rows[:m])
+                        and torch.equal(got.offsets, want.offsets) and torch.equal(got.counts, want.counts)):
+                    wrong.append(sizes[i])
+                try:
+                    X.expert_sort(ids, rows, 4097 + i)
+                except MoeEpArgError as e:
+                    if str(4097 + i) not in str(e):
+                        wrong.append(str(e))
+        except Exception as e:  # a thread's failure is the test's
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(sizes))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+
+
 def test_gradients_on_a_captured_stream(X):
     """Autograd through the sort and the unsort while a captured graph of the
     same operators' gradients, made of their functional forms, is replayed."""
