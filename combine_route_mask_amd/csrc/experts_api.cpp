@@ -30,8 +30,13 @@ int guarded(F f)
     }
 }
 
-int launched(hipError_t e, const char *what)
+// Launches; an error that an earlier call of the thread left behind is not
+// this call's.
+template <typename F>
+int launched(const char *what, F launch)
 {
+    (void)hipGetLastError();
+    const hipError_t e = launch();
     if (e == hipErrorInvalidConfiguration) // the launchers' own limit
         return fail(MOE_EP_ERR_CAPACITY, std::string(what) + " needs more workgroups than a launch holds");
     if (e != hipSuccess)
@@ -152,7 +157,7 @@ int moe_ep_expert_sort(const moe_ep_sort_args *args, void *stream)
             return bad("workspace must be a 16-byte aligned device pointer");
         if (a.workspace_bytes < need)
             return fail(MOE_EP_ERR_CAPACITY, "workspace is below moe_ep_expert_sort_workspace_bytes()");
-        return launched(launch_expert_sort(a, static_cast<hipStream_t>(stream)), "expert sort");
+        return launched("expert sort", [&] { return launch_expert_sort(a, static_cast<hipStream_t>(stream)); });
     });
 }
 
@@ -183,7 +188,7 @@ int moe_ep_expert_unsort(const moe_ep_unsort_args *args, void *stream)
             return bad("weights must be 4-byte aligned with rank strides of whole planes");
         if (!good_plane(a.out, a.out_rank_stride, a.ranks, a.slots, a.hidden_size * item, 16))
             return bad("out must be a 16-byte aligned device pointer with rank strides of whole planes");
-        return launched(launch_expert_unsort(a, static_cast<hipStream_t>(stream)), "expert unsort");
+        return launched("expert unsort", [&] { return launch_expert_unsort(a, static_cast<hipStream_t>(stream)); });
     });
 }
 
@@ -216,8 +221,8 @@ int moe_ep_expert_unsort_backward(const moe_ep_unsort_grad_args *args, void *str
             return bad("weights must be 4-byte aligned with rank strides of whole planes");
         if (!aligned(a.grad_rows, 16) || !aligned(a.grad_weights, 4))
             return bad("grad_rows must be 16-byte, grad_weights 4-byte aligned");
-        return launched(launch_expert_unsort_backward(a, static_cast<hipStream_t>(stream)),
-                        "expert unsort backward");
+        return launched("expert unsort backward",
+                        [&] { return launch_expert_unsort_backward(a, static_cast<hipStream_t>(stream)); });
     });
 }
 
@@ -247,7 +252,7 @@ int moe_ep_expert_matmul(const moe_ep_matmul_args *args, void *stream)
             return bad("x_scales, w_scales and offsets must be 4-byte aligned device pointers");
         if (!good(a.out, (uintptr_t)item_bytes(a.out_type)))
             return bad("out must be an aligned device pointer");
-        return launched(launch_expert_matmul(a, static_cast<hipStream_t>(stream)), "expert matmul");
+        return launched("expert matmul", [&] { return launch_expert_matmul(a, static_cast<hipStream_t>(stream)); });
     });
 }
 
@@ -269,7 +274,7 @@ int moe_ep_silu_mul_quantize(const moe_ep_silu_args *args, void *stream)
             return bad("x and out must be 16-byte aligned device pointers");
         if (!good(a.out_scales, 4) || (a.num_valid && !aligned(a.num_valid, 4)))
             return bad("out_scales and num_valid must be 4-byte aligned device pointers");
-        return launched(launch_silu_mul_quantize(a, static_cast<hipStream_t>(stream)), "silu_mul_quantize");
+        return launched("silu_mul_quantize", [&] { return launch_silu_mul_quantize(a, static_cast<hipStream_t>(stream)); });
     });
 }
 
@@ -303,7 +308,7 @@ int moe_ep_add_rms_norm(const moe_ep_norm_args *args, void *stream)
             return bad("out must be a 16-byte aligned device pointer");
         if (!good(a.scales, a.format == MOE_EP_NORM_MXFP8 ? 1 : 4))
             return bad("scales must be an aligned device pointer");
-        return launched(launch_add_rms_norm(a, static_cast<hipStream_t>(stream)), "add_rms_norm");
+        return launched("add_rms_norm", [&] { return launch_add_rms_norm(a, static_cast<hipStream_t>(stream)); });
     });
 }
 

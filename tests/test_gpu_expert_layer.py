@@ -274,6 +274,20 @@ def test_calls_from_several_threads(X):
     assert not wrong, wrong
 
 
+def test_an_earlier_error_is_not_this_calls(X):
+    """An error that a runtime call of this thread left behind (a device that does not exist) fails no launch."""
+    import ctypes
+    import re
+    path = re.search(r"\S*libamdhip64\S*", open("/proc/self/maps").read()).group(0)
+    hip = ctypes.CDLL(path)
+    st = _state(None, 5, S=700)
+    want = X.expert_sort(st["ids"], st["rows"], 4)
+    torch.cuda.synchronize()
+    assert hip.hipSetDevice(1 << 20) != 0
+    got = X.expert_sort(st["ids"], st["rows"], 4)
+    assert torch.equal(got.position, want.position)
+
+
 def test_gradients_on_a_captured_stream(X):
     """Autograd through the sort and the unsort while a captured graph of the
     same operators' gradients, made of their functional forms, is replayed."""
