@@ -48,6 +48,12 @@ __device__ __forceinline__ void expert_rows(const moe_ep_matmul_args &a, int e, 
     }
 }
 
+// Tiles of up to bm rows for rows [lo, hi); hi - lo + bm may pass 2^31.
+__device__ __forceinline__ int row_tiles(int lo, int hi, int bm)
+{
+    return (int)(((uint32_t)(hi - lo) + (uint32_t)bm - 1) / (uint32_t)bm);
+}
+
 constexpr int kBand = 4;
 constexpr int kUnit = 64; // tiles begin this many rows apart, or a multiple
 
@@ -76,8 +82,8 @@ struct TileFinder {
         float rows = 0.0f;
         for (int i = 0; i < share; ++i) {
             expert_rows(a, lane * share + i, lo, hi);
-            n += (hi - lo + BM - 1) / BM;
-            tall += (hi - lo + TALL - 1) / TALL;
+            n += row_tiles(lo, hi, BM);
+            tall += row_tiles(lo, hi, TALL);
             rows += (float)(hi - lo);
         }
         int sum = prefix_sum(n, lane);
@@ -120,7 +126,7 @@ struct TileFinder {
             elo = ehi = 0;
             if (lane < share)
                 expert_rows(a, base + lane, elo, ehi);
-            en = (ehi - elo + bm - 1) / bm;
+            en = row_tiles(elo, ehi, bm);
             estart += (prefix_sum(en, lane) - en) * ntiles;
             hit = __ballot(at >= estart && at < estart + en * ntiles);
             if (!hit)
@@ -518,7 +524,7 @@ hipError_t tile_launch(const moe_ep_matmul_args &a, hipStream_t s)
     const int64_t ntiles = (a.n + S::BN - 1) / S::BN;
     constexpr int TALL = largest(S::BM, MORE::BM...);
     const int64_t tiles = most_tiles(a, TALL > 256 ? 256 : TALL) * ntiles;
-    if (tiles > INT32_MAX - 8) // they are numbered in 32 bits
+    if (tiles > INT32_MAX - 4096) // they are numbered in 32 bits, a run's last number and a step behind it too
         return hipErrorInvalidConfiguration;
     const int64_t run = (tiles + 7) / 8, resident = 32 * (160 * 1024 / kLds);
     const dim3 grid((unsigned)(8 * (run < resident ? run : resident))), block(S::THREADS);
@@ -541,8 +547,8 @@ hipError_t tile_launch(const moe_ep_matmul_args &a, hipStream_t s)
 //    1024 rows 532 / 644; E 32, 4096 x 1024: 256 rows 53 / 58, 512 rows
 //    104 / 127; E 1, 7168 x 7168, 1024 rows (112 tiles) 78 / 57.  Not for
 //    k below 1024: E 32, 2048 x 512, 192 rows 21 / 19, 512 rows 37 / 35.
-//    (Up to 256 rows only: E 32, 4096 x 4096, 256 rows 215, 512 rows 297;
-//    an expert somewhat above 256 rows then takes two tiles.);
+//    With tiles of up to 256 rows only, an expert somewhat above that takes
+//    two: E 32, 4096 x 4096, 256 rows 167 / 215, 512 rows 280 / 297;
 //  - up to 128 x 128, four waves, two workgroups a CU; for at most 32 rows an
 //    expert its 64-row shape with three stages in place of two: E 32,
 //    4096 x 4096, 1 row 66 / 76, but 64 rows 114 / 105;

@@ -112,6 +112,27 @@ def test_extreme_codes(X, M):
     assert bool((y[:, 0] == 16384.0 * K).all()) and bool((y[:, 1] == float(np.float32(-16256 * K))).all())
 
 
+def test_most_rows(X):
+    """As many rows as a call takes: the last ones and the first have their products."""
+    M, K = 2 ** 31 - 1, 16
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GiB of free device memory")
+    log(f"product M{M} N1 K{K}")
+    x = torch.zeros((M, K), dtype=torch.int8, device="cuda")
+    sx = torch.ones(M, device="cuda")
+    w = torch.arange(1, K + 1, dtype=torch.int8, device="cuda").view(1, K)
+    for at in (slice(0, 300), slice(M - 300, M)):
+        x[at] = torch.arange(300, device="cuda").remainder(120).to(torch.int8)[:, None]
+    want = torch.arange(300, device="cuda").remainder(120).float() * (K * (K + 1) // 2)
+    for offsets in (None, torch.tensor([0, M], dtype=torch.int32, device="cuda")):
+        y = torch.full((M, 1), 3.0, device="cuda")
+        X.expert_matmul(x, sx, w if offsets is None else w[None], sx[:1] if offsets is None else sx[None, :1],
+                        offsets=offsets, out=y)
+        assert torch.equal(y[:300, 0], want) and torch.equal(y[-300:, 0], want)
+        assert not bool(y[300:-300].any())
+        del y
+
+
 def test_offsets_beyond_the_rows(X):
     """Offsets past the rows are taken as their number, descending ones as empty: nothing is written out of range."""
     rng = np.random.default_rng(5)
