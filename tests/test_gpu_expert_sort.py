@@ -285,3 +285,27 @@ def test_gradient_with_dropped_rows(X):
     y = X.expert_unsort(s.position, s.rows.detach(), w)
     y.sum().backward()
     assert w.grad[0, 2].tolist() == [float(x.detach()[0, 2].sum()), 0.0]
+
+
+def test_most_pairs(X):
+    """2^31 - 8 pairs, the most that a call takes: id j % 4 for every slot's pair j, so that every place is known."""
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GiB of free device memory")
+    S, k, E, H = 2 ** 28 - 1, 8, 4, 8
+    log(f"sort S{S} k{k}")
+    ids = (torch.arange(k, device="cuda", dtype=torch.int32) % E).expand(1, S, k).contiguous()
+    rows = torch.arange(S, device="cuda", dtype=torch.int32).remainder_(251).to(BF)[None, :, None].expand(1, S, H).contiguous()
+    s = X.expert_sort(ids, rows, E)
+    del ids
+    assert s.counts.tolist() == [2 * S] * E and s.offsets.tolist() == [2 * S * e for e in range(E + 1)]
+    q = torch.arange(S, device="cuda", dtype=torch.int32)
+    for j in range(k):
+        assert torch.equal(s.position[0, :, j], 2 * S * (j % E) + 2 * q + j // E)
+    for e in range(E):
+        for b in range(2):
+            assert torch.equal(s.rows.view(E, S, 2, H)[e, :, b], rows[0])
+    out = X.expert_unsort(s.position, s.rows)
+    assert torch.equal(out, rows * 8)
+    gr, gw = X.expert_unsort_backward(s.position, rows, s.rows, grad_rows=s.rows, need_weights=False)
+    for e in range(E):
+        assert torch.equal(gr.view(E, S, 2, H)[e, :, 1], rows[0])
