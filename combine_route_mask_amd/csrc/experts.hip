@@ -519,13 +519,15 @@ __global__ __launch_bounds__(kPlanBlock) void sort_plan_kernel(moe_ep_sort_args 
 
 constexpr int kGatherBlock = 256;
 constexpr int kGatherVectors = 2;
+constexpr int kShortBlock = 128; // for quantised rows of up to 32 elements a thread
 
 // Offsets from the counts, by one workgroup.
+template <int BS>
 __device__ __forceinline__ void write_offsets(const moe_ep_sort_args &a)
 {
-    __shared__ int32_t sums[kGatherBlock / 64];
+    __shared__ int32_t sums[BS / 64];
     const int E = a.ranks * a.experts_per_rank, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int per = (E + kGatherBlock - 1) / kGatherBlock, lo = min(E, (int)threadIdx.x * per), hi = min(E, lo + per);
+    const int per = (E + BS - 1) / BS, lo = min(E, (int)threadIdx.x * per), hi = min(E, lo + per);
     int sum = 0;
     for (int e = lo; e < hi; ++e)
         sum += a.counts[e];
@@ -553,16 +555,16 @@ __device__ __forceinline__ void write_offsets(const moe_ep_sort_args &a)
 // row is one chunk).  PLANNED: the places are the plan's, within the rank; the
 // first chunk writes them out, and the workgroup behind the last item the
 // offsets.
-template <typename T, bool QUANT, bool PLANNED>
-__global__ __launch_bounds__(kGatherBlock) void sort_gather_kernel(moe_ep_sort_args a, int g, uint32_t nchunk,
+template <typename T, bool QUANT, bool PLANNED, int BS>
+__global__ __launch_bounds__(BS) void sort_gather_kernel(moe_ep_sort_args a, int g, uint32_t nchunk,
                                                                    uint32_t items)
 {
-    constexpr int BS = kGatherBlock, VPT = kGatherVectors;
+    constexpr int VPT = kGatherVectors;
     __shared__ uint32_t red[BS / 64];
     const int64_t nslots = (int64_t)a.ranks * a.slots;
     const int k = a.top_k, lane = threadIdx.x & 63;
     if (PLANNED && blockIdx.x == gridDim.x - 1) {
-        write_offsets(a);
+        write_offsets<BS>(a);
         return;
     }
     const uint32_t step = PLANNED ? gridDim.x - 1 : gridDim.x;
@@ -890,24 +892,36 @@ hipError_t launch_expert_sort(const moe_ep_sort_args &a, hipStream_t s)
     }
     dim3 grid = grid_of(items);
     grid.x += planned;
-    const dim3 block(kGatherBlock);
-#define MOE_EP_GATHER(T, QUANT, PLANNED) \
-    hipLaunchKernelGGL((sort_gather_kernel<T, QUANT, PLANNED>), grid, block, 0, s, a, g, nchunk, (uint32_t)items)
+    // More rows in flight for smaller workgroups: 8 ranks of 2048 slots, top_k
+    // 4, rows of 4096: 27.7 us with the plan, 31.0 with 256 threads; 8 of 4096
+    // slots, rows of 1024: 28.5 / 35.4 (one rank, 4096 slots that are all full,
+    // top_k 8, rows of 4096: 44 / 43).
+    const bool shorter = a.quantize && a.row_bytes / (a.row_type == MOE_EP_BF16_ROWS ? 2 : 4) <= 32 * kShortBlock;
+    const dim3 block(shorter ? kShortBlock : kGatherBlock);
+#define MOE_EP_GATHER(T, QUANT, PLANNED)                                                                              \
+    if (QUANT && shorter)                                                                                             \
+        hipLaunchKernelGGL((sort_gather_kernel<T, QUANT, PLANNED, QUANT ? kShortBlock : kGatherBlock>), grid, block,  \
+                           0, s, a, g, nchunk, (uint32_t)items);                                                      \
+    else                                                                                                              \
+        hipLaunchKernelGGL((sort_gather_kernel<T, QUANT, PLANNED, kGatherBlock>), grid, block, 0, s, a, g, nchunk,    \
+                           (uint32_t)items)
     const bool bf16 = a.row_type == MOE_EP_BF16_ROWS;
     if (planned) {
-        if (!a.quantize)
+        if (!a.quantize) {
             MOE_EP_GATHER(Bf16, false, true);
-        else if (bf16)
+        } else if (bf16) {
             MOE_EP_GATHER(Bf16, true, true);
-        else
+        } else {
             MOE_EP_GATHER(Fp32, true, true);
+        }
     } else {
-        if (!a.quantize)
+        if (!a.quantize) {
             MOE_EP_GATHER(Bf16, false, false);
-        else if (bf16)
+        } else if (bf16) {
             MOE_EP_GATHER(Bf16, true, false);
-        else
+        } else {
             MOE_EP_GATHER(Fp32, true, false);
+        }
     }
 #undef MOE_EP_GATHER
     return hipGetLastError();
