@@ -227,6 +227,7 @@ def _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, stream, a
     row_type = _row_type(rows, "rows") if quantize else 0
     masked = 0
     if active_rank_mask is not None:
+        active_rank_mask = int(active_rank_mask)
         if not 0 <= active_rank_mask < 1 << R:
             _refuse(f"active_rank_mask must be a mask of {R} ranks, got {active_rank_mask:#x}")
         masked = active_rank_mask ^ (1 << R) - 1

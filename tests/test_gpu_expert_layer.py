@@ -110,7 +110,7 @@ def test_layer_between_dispatch_and_combine(X, P, T, E, k, H, I, mask):
     ex8.destroy()
 
 
-@pytest.mark.parametrize("P,T,E,k", [(4, 9, 16, 4), (4, 130, 16, 4), (8, 700, 32, 2), (4, 2200, 16, 4)])
+@pytest.mark.parametrize("P,T,E,k", [(4, 9, 16, 4), (4, 130, 16, 4), (8, 700, 32, 2), (4, 2200, 16, 4), (64, 5, 64, 2)])
 def test_masked_ranks_hold_no_pairs(X, P, T, E, k):
     """A dispatch leaves a masked-off rank's region as the step before left
     it (at first: whatever the workspace held): its ids are no pairs, at every
