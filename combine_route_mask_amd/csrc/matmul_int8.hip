@@ -54,6 +54,12 @@ __device__ __forceinline__ int row_tiles(int lo, int hi, int bm)
     return (int)(((uint32_t)(hi - lo) + (uint32_t)bm - 1) / (uint32_t)bm);
 }
 
+// Tiles of bn of the n channels; n + bn may pass 2^31.
+__host__ __device__ __forceinline__ int channel_tiles(int n, int bn)
+{
+    return (int)(((uint32_t)n + (uint32_t)bn - 1) / (uint32_t)bn);
+}
+
 constexpr int kBand = 4;
 constexpr int kUnit = 64; // tiles begin this many rows apart, or a multiple
 
@@ -353,7 +359,7 @@ __device__ __forceinline__ Operands<S> find_operands(const moe_ep_matmul_args &a
     // two apart would otherwise have all workgroups read the same few memory
     // channels at a time (64 rows, 32 experts, N = K = 4096: 106 us all from
     // k = 0, 79 us)
-    o.start = (int)((uint32_t)(t.expert * ((a.n + S::BN - 1) / S::BN) + t.n) % (uint32_t)o.steps);
+    o.start = (int)(((uint32_t)t.expert * (uint32_t)channel_tiles(a.n, S::BN) + (uint32_t)t.n) % (uint32_t)o.steps);
     return o;
 }
 
@@ -443,12 +449,12 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
 #pragma unroll
             for (int e = 0; e < 4 * V; ++e)
                 y[e] = (float)acc[i + e / 4][j][e % 4] * (sx[j] * sw[i + e / 4][e % 4]);
-            if (n + 4 * V <= a.n) {
+            if (a.n - n >= 4 * V) { // the last channels' n + 4 V may pass 2^31
                 *reinterpret_cast<AnyAligned *>(out + 16 * i * RowType<T>::kBytes) = RowType<T>::pack(y);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4 * V; ++e)
-                    if (n + e < a.n)
+                    if (e < a.n - n)
                         store_element<T>(out + (16 * i + e) * RowType<T>::kBytes, y[e]);
             }
         }
@@ -521,7 +527,7 @@ template <typename S, typename... MORE>
 hipError_t tile_launch(const moe_ep_matmul_args &a, hipStream_t s)
 {
     constexpr int kLds = largest(S::STAGES * S::BYTES, (MORE::STAGES * MORE::BYTES)...) + 2 * tile_scales<S, MORE...>();
-    const int64_t ntiles = (a.n + S::BN - 1) / S::BN;
+    const int64_t ntiles = channel_tiles(a.n, S::BN);
     constexpr int TALL = largest(S::BM, MORE::BM...);
     const int64_t tiles = most_tiles(a, TALL > 256 ? 256 : TALL) * ntiles;
     if (tiles > INT32_MAX - 4096) // they are numbered in 32 bits, a run's last number and a step behind it too

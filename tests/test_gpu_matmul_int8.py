@@ -152,3 +152,30 @@ def test_row_scales_carry_nan(X):
     x[7] = 0
     y = X.expert_matmul(x.cuda(), sx.cuda(), w[0].cuda(), sw[0].cuda()).cpu()
     assert bool(y[7].isnan().all()) and int(y.isnan().sum()) == 40
+
+
+def test_most_channels(X):
+    """As many channels as a call takes: the first and the last have their products, and nothing is written behind them."""
+    M, N, K = 2, 2 ** 31 - 1, 16
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GiB of free device memory")
+    log(f"product M{M} N{N} K{K}")
+    x = torch.arange(1, K + 1, dtype=torch.int8, device="cuda").repeat(M, 1)
+    x[1] *= -1
+    sx = torch.ones(M, device="cuda")
+    sw = torch.ones(N, device="cuda")
+    w = torch.zeros((N, K), dtype=torch.int8, device="cuda")
+    ramp = torch.arange(300, device="cuda").remainder(120)
+    for at in (slice(0, 300), slice(N - 300, N)):
+        w[at] = ramp.to(torch.int8)[:, None]
+    want = (ramp.float() * (K * (K + 1) // 2)).to(BF)
+    for offsets in (None, torch.tensor([0, M], dtype=torch.int32, device="cuda")):
+        room = torch.full((M * N + 64,), 3.0, dtype=BF, device="cuda")
+        y = room[:M * N].view(M, N)
+        X.expert_matmul(x, sx, w if offsets is None else w[None], sw if offsets is None else sw[None],
+                        offsets=offsets, out=y)
+        for m, sign in enumerate((1, -1)):
+            assert torch.equal(y[m, :300], sign * want) and torch.equal(y[m, -300:], sign * want)
+            assert not bool(y[m, 300:-300].any())
+        assert bool((room[M * N:] == 3).all())
+        del room, y
