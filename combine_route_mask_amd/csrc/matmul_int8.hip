@@ -241,14 +241,17 @@ struct Fragments {
     i32x4 x[2][S::FM], w[2 * S::FN];
 };
 
+// A fragment out of a stage.  Nothing else touches the stage within a read, and
+// __restrict__ says so: without it each read would be made to wait for all loads
+// on their way to LDS, wherever to.
 template <typename S>
-__device__ __forceinline__ void read_x(const uint8_t *stage, const Operands<S> &o, Fragments<S> &f, int h, int j)
+__device__ __forceinline__ void read_x(const uint8_t *__restrict__ stage, const Operands<S> &o, Fragments<S> &f, int h, int j)
 {
     f.x[h][j] = *reinterpret_cast<const i32x4 *>(stage + o.xat[h] + 16 * j * kTileK);
 }
 
 template <typename S>
-__device__ __forceinline__ void read_w(const uint8_t *stage, const Operands<S> &o, Fragments<S> &f, int i)
+__device__ __forceinline__ void read_w(const uint8_t *__restrict__ stage, const Operands<S> &o, Fragments<S> &f, int i)
 {
     f.w[i] = *reinterpret_cast<const i32x4 *>(stage + o.wat[i / S::FN] + 16 * (i % S::FN) * kTileK);
 }
@@ -267,14 +270,12 @@ constexpr int kAhead = 2; // weight fragments are read this many products before
 // The products of stage `cur`, groups of FM.  The first kAhead fragments are
 // in registers already; the last groups run behind the barrier and read the
 // first of `next`, so that neither LDS nor the barrier leaves the matrix
-// cores idle for long.  Behind it `fill`, which is `cur`, takes the loads for
-// STAGES steps on: they have at least a whole step to arrive.  The stages are
-// distinct objects to the compiler, so that a read of one does not wait for
-// loads into another; wait_barrier() does, for those that have to have
-// arrived.
+// cores idle for long.  Behind it `cur`, which no wave reads again, takes the
+// loads for STAGES steps on: they have at least a whole step to arrive.
+// wait_barrier() orders them behind the reads before it, and waits for the loads
+// that the reads behind it need.
 template <typename S, typename ACC>
-__device__ __forceinline__ void tile_step(const uint8_t *__restrict__ cur, const uint8_t *__restrict__ next,
-                                          uint8_t *__restrict__ fill, int k, uint32_t past, const Operands<S> &o,
+__device__ __forceinline__ void tile_step(uint8_t *cur, const uint8_t *next, int k, uint32_t past, const Operands<S> &o,
                                           Fragments<S> &f, ACC &acc, Fragments<S> &g)
 {
     constexpr int G = 2 * S::FN, L = S::LN + S::LM, FIRST = S::FN - S::FM - kAhead + 1;
@@ -298,7 +299,7 @@ __device__ __forceinline__ void tile_step(const uint8_t *__restrict__ cur, const
 #pragma unroll
             for (int u = 0; u < L; ++u)
                 if (u * kAhead / L == i - (G - kAhead))
-                    load_part<S>(fill, o, u, k, past);
+                    load_part<S>(cur, o, u, k, past);
         }
 #pragma unroll
         for (int j = 0; j < S::FM; ++j)
@@ -418,7 +419,7 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
     // the loads behind the last step are not read, nor do they reach memory
     for (int i = 0; i < steps; ++i) {
         const uint32_t past = i >= steps - S::STAGES ? kPastEnd : at == steps - 1 ? o.end : 0;
-        tile_step<S>(cur, next, cur, at * kTileK, past, o, f, acc, g);
+        tile_step<S>(cur, next, at * kTileK, past, o, f, acc, g);
         at = at + 1 == steps ? 0 : at + 1;
         cur = next;
         next = next == lds + (S::STAGES - 1) * S::BYTES ? lds : next + S::BYTES;
