@@ -14,7 +14,8 @@ synchronisation; outputs that are not given are allocated on that stream, and
 given ones are checked and written in place.  Tensors that live on another
 stream must be ordered by the caller.  Calls may be captured into a HIP
 graph.  A refused call raises ``MoeEpArgError`` (or ``MoeEpError`` with the
-library's code) and launches nothing.
+library's code) and launches nothing.  Under grad mode an input that asks for
+a gradient is refused where the operator has none for it.
 """
 from __future__ import annotations
 
@@ -203,7 +204,8 @@ def expert_sort(ids, rows, experts_per_rank: int, *, scales=None, capacity: Opti
 
     Differentiable in ``rows`` (bf16 or fp32; not with ``quantize``, ``out``
     or ``stream``: autograd orders its work by the current stream); the rows
-    behind the last pair are then zeros."""
+    behind the last pair are then zeros.  ``scales`` have no gradient."""
+    _no_grad(scales)
     if rows.requires_grad and torch.is_grad_enabled():
         _need(not quantize and out is None and stream is None and rows.dtype in _ROW_TYPES,
               "only a sort of bf16 or fp32 rows into a new tensor, on the current stream, has a gradient")
@@ -237,7 +239,6 @@ def _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, stream, a
         _refuse("capacity may not be negative")
     scales_stride = scale_bytes = 0
     if scales is not None:
-        _no_grad(scales)
         if quantize:
             _refuse("quantised rows take no scale rows")
         scales_stride = _plane(scales, "scales", dev)
@@ -278,6 +279,7 @@ def _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, stream, a
 def expert_sort_backward(position, grad_rows, *, out=None, stream=None):
     """Gradient of the sort's rows: [R, S, H], each slot the sum of its
     pairs' rows of ``grad_rows`` [capacity, H] (zeros without a pair)."""
+    _no_grad(grad_rows)
     return _unsort(position, grad_rows, None, out, False, stream)
 
 
@@ -371,6 +373,7 @@ def expert_unsort_backward(position, grad_out, rows=None, weights=None, *, grad_
     grad_rows' rows that no pair names are left as they were, in a given
     ``grad_rows``, or zeros.  ``rows``, the unsort's input, is needed for
     grad_weights; without it give ``grad_rows``."""
+    _no_grad(grad_out, rows, weights)
     dev = _device(grad_out, "grad_out")
     if stream is not None or dev.index != _device_now():
         with _On(dev, stream):

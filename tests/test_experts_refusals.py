@@ -173,3 +173,22 @@ def test_cpu_tensors_are_refused(X, m):
                  lambda: X.add_rms_norm(rows[0], None, rows[0, 0], format="fp4")):
         with pytest.raises(m.MoeEpArgError):
             call()
+
+
+def test_gradients_are_not_dropped_in_silence(X, m):
+    """Scale rows have no gradient, next to differentiable rows either; neither have the gradients' own calls."""
+    ids = torch.zeros((1, 2, 2), dtype=torch.int32)
+    rows = torch.zeros((1, 2, 16), requires_grad=True)
+    scales = torch.zeros((1, 2, 4), requires_grad=True)
+    flat, w = torch.zeros((2, 16), requires_grad=True), torch.zeros((1, 2, 2), requires_grad=True)
+    plain, plain_w = flat.detach(), w.detach()
+    for call in (lambda: X.expert_sort(ids, rows, 4, scales=scales),
+                 lambda: X.expert_sort(ids, rows.detach(), 4, scales=scales),
+                 lambda: X.expert_sort_backward(ids, flat),
+                 lambda: X.expert_unsort_backward(ids, rows, plain, plain_w),
+                 lambda: X.expert_unsort_backward(ids, rows.detach(), flat, plain_w),
+                 lambda: X.expert_unsort_backward(ids, rows.detach(), plain, w)):
+        with pytest.raises(m.MoeEpArgError, match="no gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(m.MoeEpArgError, match="GPU tensor"):
+            call()
