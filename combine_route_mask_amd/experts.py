@@ -141,6 +141,13 @@ def _no_grad(*tensors):
         _refuse("this call has no gradient: detach its inputs or call it under torch.no_grad()")
 
 
+def _whole(grad):
+    """A gradient as autograd hands it over (expanded, a part of a larger buffer) as the kernels read it:
+    contiguous, from a 16-byte boundary on."""
+    grad = grad.contiguous()
+    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
+
+
 def _empty(shape, strides, dtype, dev):
     """A contiguous tensor; 0.4 us less of a call than ``torch.empty``."""
     return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
@@ -297,7 +304,7 @@ class _SortFunction(torch.autograd.Function):
     def backward(ctx, grad, *_):
         if grad is None:
             return (None,) * 7
-        return (expert_sort_backward(ctx.saved_tensors[0], grad.contiguous()),) + (None,) * 6
+        return (expert_sort_backward(ctx.saved_tensors[0], _whole(grad)),) + (None,) * 6
 
 
 # ----------------------------------------------------------------------------
@@ -431,7 +438,7 @@ class _UnsortFunction(torch.autograd.Function):
         g = None
         if rows is None:
             g = torch.zeros(ctx.rows_shape, dtype=grad.dtype, device=grad.device)
-        gr, gw = expert_unsort_backward(position, grad.contiguous(), rows, weights, grad_rows=g, need_rows=need_rows,
+        gr, gw = expert_unsort_backward(position, _whole(grad), rows, weights, grad_rows=g, need_rows=need_rows,
                                         need_weights=ctx.needs_input_grad[1])
         return gr, gw, None
 

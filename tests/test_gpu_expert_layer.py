@@ -506,3 +506,31 @@ def test_empty_calls(X):
     assert not bool(X.expert_unsort(s.position, s.rows).any())
     gr, gw = X.expert_unsort_backward(s.position, rows, s.rows)
     assert not bool(gr.any()) and not bool(gw.any())
+
+
+def test_gradients_at_any_address(X):
+    """Gradients that begin between 16-byte boundaries (parts of one flat buffer) or repeat one number are the same
+    gradients."""
+    st = _state(None, 13, S=60)
+    ids, w = st["ids"], st["w"]
+    x = st["rows"]
+    for dtype in (BF, F32):
+        xl, wl = x.to(dtype).requires_grad_(), w.clone().requires_grad_()
+        s = X.expert_sort(ids, xl, 4)
+        y = X.expert_unsort(s.position, s.rows, wl)
+        go, gs = torch.randn_like(y), torch.randn_like(s.rows)
+        for shift in (1, 3):
+            odd = []
+            for g in (go, gs):
+                flat = torch.empty(g.numel() + shift, dtype=dtype, device="cuda")
+                odd.append(flat[shift:].view(g.shape))
+                odd[-1].copy_(g)
+                assert odd[-1].data_ptr() % 16 and odd[-1].is_contiguous()
+            want = torch.autograd.grad((y, s.rows), (xl, wl), (go, gs), retain_graph=True)
+            got = torch.autograd.grad((y, s.rows), (xl, wl), tuple(odd), retain_graph=True)
+            assert _same(got, want)
+            # each operator's own
+            assert _same(torch.autograd.grad(s.rows, xl, odd[1], retain_graph=True),
+                         torch.autograd.grad(s.rows, xl, gs, retain_graph=True))
+        got = torch.autograd.grad(y.sum(), (xl, wl), retain_graph=True)
+        assert _same(got, torch.autograd.grad(y, (xl, wl), torch.ones_like(y)))
