@@ -447,12 +447,15 @@ class _UnsortFunction(torch.autograd.Function):
 # products and row-wise operators
 # ----------------------------------------------------------------------------
 
-def expert_matmul(x, x_scales, weight, weight_scales, *, offsets=None, out=None, dtype=torch.bfloat16, stream=None):
+def expert_matmul(x, x_scales, weight, weight_scales, *, offsets=None, out=None, dtype=None, stream=None):
     """Product of int8 rows [M, K] (fp32 scales [M]) with each expert's int8
     weights [E, N, K] (fp32 channel scales [E, N]): rows
     offsets[e]..offsets[e + 1] - 1 meet expert e's, other rows of the result
     [M, N] are left as they were, in ``out`` or uninitialised.  Dense: weight
-    [N, K], scales [N], no offsets.  The sum is exact; bf16 or fp32 result."""
+    [N, K], scales [N], no offsets.  The sum is exact; the result is of
+    ``dtype`` (bf16 or fp32), by default ``out``'s, bf16 without ``out``."""
+    if out is not None and dtype not in (None, out.dtype):
+        _refuse(f"out is {out.dtype}, the result's dtype {dtype}")
     dev = _device(x, "x")
     if stream is not None or dev.index != _device_now():
         with _On(dev, stream):
@@ -477,7 +480,7 @@ def expert_matmul(x, x_scales, weight, weight_scales, *, offsets=None, out=None,
         _flat(weight, "weight", dev, torch.int8, (N, K))
         _flat(weight_scales, "weight_scales", dev, torch.float32, (N,))
     if out is None:
-        out = _empty((M, N), (N, 1), dtype, dev)
+        out = _empty((M, N), (N, 1), dtype or torch.bfloat16, dev)
     else:
         _flat(out, "out", dev, out.dtype, (M, N))
         _written(out)

@@ -192,3 +192,14 @@ def test_gradients_are_not_dropped_in_silence(X, m):
             call()
         with torch.no_grad(), pytest.raises(m.MoeEpArgError, match="GPU tensor"):
             call()
+
+
+def test_product_type_and_output_agree(X, m):
+    """A result type that is not the given output's is refused."""
+    q, s = torch.zeros((2, 16), dtype=torch.int8), torch.zeros(2)
+    for given, dtype in ((torch.float32, torch.bfloat16), (torch.bfloat16, torch.float32), (torch.float32, torch.float16)):
+        with pytest.raises(m.MoeEpArgError, match="dtype"):
+            X.expert_matmul(q, s, q, s, out=torch.zeros((2, 2), dtype=given), dtype=dtype)
+    for dtype in (None, torch.float32):
+        with pytest.raises(m.MoeEpArgError, match="GPU tensor"):
+            X.expert_matmul(q, s, q, s, out=torch.zeros((2, 2)), dtype=dtype)
