@@ -15,7 +15,8 @@ given ones are checked and written in place.  Tensors that live on another
 stream must be ordered by the caller.  Calls may be captured into a HIP
 graph.  A refused call raises ``MoeEpArgError`` (or ``MoeEpError`` with the
 library's code) and launches nothing.  Under grad mode an input that asks for
-a gradient is refused where the operator has none for it.
+a gradient is refused where the operator has none for it, and so is a given
+output that does.
 """
 from __future__ import annotations
 
@@ -138,7 +139,7 @@ def _no_grad(*tensors):
                 break
         else:
             return
-        _refuse("this call has no gradient: detach its inputs or call it under torch.no_grad()")
+        _refuse("this call has no gradient: detach its tensors or call it under torch.no_grad()")
 
 
 def _whole(grad):
@@ -212,7 +213,7 @@ def expert_sort(ids, rows, experts_per_rank: int, *, scales=None, capacity: Opti
     Differentiable in ``rows`` (bf16 or fp32; not with ``quantize``, ``out``
     or ``stream``: autograd orders its work by the current stream); the rows
     behind the last pair are then zeros.  ``scales`` have no gradient."""
-    _no_grad(scales)
+    _no_grad(scales, out, out_scales)
     if rows.requires_grad and torch.is_grad_enabled():
         _need(not quantize and out is None and stream is None and rows.dtype in _ROW_TYPES,
               "only a sort of bf16 or fp32 rows into a new tensor, on the current stream, has a gradient")
@@ -286,7 +287,7 @@ def _sort(ids, rows, epr, scales, capacity, quantize, out, out_scales, stream, a
 def expert_sort_backward(position, grad_rows, *, out=None, stream=None):
     """Gradient of the sort's rows: [R, S, H], each slot the sum of its
     pairs' rows of ``grad_rows`` [capacity, H] (zeros without a pair)."""
-    _no_grad(grad_rows)
+    _no_grad(grad_rows, out)
     return _unsort(position, grad_rows, None, out, False, stream)
 
 
@@ -323,6 +324,7 @@ def expert_unsort(position, rows, weights=None, *, out=None, keep_empty: bool = 
 
     Differentiable in ``rows`` and ``weights`` (without ``out`` or
     ``stream``)."""
+    _no_grad(out)
     if (rows.requires_grad or (weights is not None and weights.requires_grad)) and torch.is_grad_enabled():
         _need(out is None and not keep_empty and stream is None,
               "only an unsort into a new tensor, on the current stream, has a gradient")
@@ -380,7 +382,7 @@ def expert_unsort_backward(position, grad_out, rows=None, weights=None, *, grad_
     grad_rows' rows that no pair names are left as they were, in a given
     ``grad_rows``, or zeros.  ``rows``, the unsort's input, is needed for
     grad_weights; without it give ``grad_rows``."""
-    _no_grad(grad_out, rows, weights)
+    _no_grad(grad_out, rows, weights, grad_rows)
     dev = _device(grad_out, "grad_out")
     if stream is not None or dev.index != _device_now():
         with _On(dev, stream):
@@ -456,11 +458,11 @@ def expert_matmul(x, x_scales, weight, weight_scales, *, offsets=None, out=None,
     ``dtype`` (bf16 or fp32), by default ``out``'s, bf16 without ``out``."""
     if out is not None and dtype not in (None, out.dtype):
         _refuse(f"out is {out.dtype}, the result's dtype {dtype}")
+    _no_grad(x_scales, weight_scales, out)
     dev = _device(x, "x")
     if stream is not None or dev.index != _device_now():
         with _On(dev, stream):
             return expert_matmul(x, x_scales, weight, weight_scales, offsets=offsets, out=out, dtype=dtype)
-    _no_grad(x_scales, weight_scales)
     if x.dim() != 2 or weight.dim() not in (2, 3):
         _refuse(f"x must be [M, K] and weight [E, N, K] or [N, K], got {list(x.shape)} and {list(weight.shape)}")
     M, K = x.shape
@@ -495,7 +497,7 @@ def silu_mul_quantize(x, *, offsets=None, out=None, out_scales=None, stream=None
     """silu(x[:, :I]) * x[:, I:] of bf16 or fp32 rows [M, 2 I] as int8 codes
     [M, I] with scales = amax / 127.  With the sort's ``offsets`` only its
     offsets[-1] rows are computed, the others left as they were."""
-    _no_grad(x)
+    _no_grad(x, out_scales)
     dev = _device(x, "x")
     if stream is not None or dev.index != _device_now():
         with _On(dev, stream):
@@ -535,7 +537,7 @@ def add_rms_norm(x, residual, weight, eps: float = 1e-6, *, format: str = "mxfp8
     x, residual [M, H] and weight [H], all bf16 or all fp32.  The returned
     residual is s rounded to x's type, written to ``residual_out`` (which may
     be ``residual`` or ``x``) or a new tensor; without a residual it is x."""
-    _no_grad(x, residual, weight)
+    _no_grad(x, residual, weight, out, out_scales, residual_out)
     if format not in _NORMS:
         _refuse(f"format must be one of {sorted(_NORMS)}, got {format!r}")
     code, block, row_dtype, scale_dtype = _NORMS[format]

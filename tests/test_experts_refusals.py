@@ -203,3 +203,25 @@ def test_product_type_and_output_agree(X, m):
     for dtype in (None, torch.float32):
         with pytest.raises(m.MoeEpArgError, match="GPU tensor"):
             X.expert_matmul(q, s, q, s, out=torch.zeros((2, 2)), dtype=dtype)
+
+
+def test_outputs_with_a_gradient_are_refused(X, m):
+    """Written in place, an output that autograd follows would keep the history of what it no longer holds."""
+    ids = torch.zeros((1, 2, 2), dtype=torch.int32)
+    rows, flat = torch.zeros((1, 2, 16)), torch.zeros((2, 16))
+    q, s = torch.zeros((2, 16), dtype=torch.int8), torch.zeros(2)
+    wt = torch.zeros(16)
+    grad = lambda *shape: (torch.zeros(shape, requires_grad=True) * 1)  # noqa: E731
+    for call in (lambda: X.expert_sort(ids, rows, 4, out=grad(4, 16)),
+                 lambda: X.expert_sort(ids, rows, 4, quantize=True, out_scales=grad(4)),
+                 lambda: X.expert_sort_backward(ids, flat, out=grad(1, 2, 16)),
+                 lambda: X.expert_unsort(ids, flat, out=grad(1, 2, 16)),
+                 lambda: X.expert_unsort_backward(ids, rows, flat, grad_rows=grad(2, 16)),
+                 lambda: X.expert_matmul(q, s, q, s, out=grad(2, 2)),
+                 lambda: X.silu_mul_quantize(torch.zeros((2, 32)), out_scales=grad(2)),
+                 lambda: X.add_rms_norm(flat, None, wt, format="int8", out_scales=grad(2)),
+                 lambda: X.add_rms_norm(flat, flat, wt, format="int8", residual_out=grad(2, 16))):
+        with pytest.raises(m.MoeEpArgError, match="no gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(m.MoeEpArgError, match="GPU tensor"):
+            call()
