@@ -435,6 +435,8 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
     for (int j = 0; j < FM; ++j)
         sx[j] = *reinterpret_cast<const float *>(scales + 4 * (S::BN + wm + 16 * j + l16));
     ahead();
+    // The sum meets its channel's scale first: the scales' own product may lie
+    // outside fp32 (rows of any magnitude) where the result does not.
     // Rows of any n start at any element: 16-byte stores need no more than an
     // element's alignment.
 #pragma unroll
@@ -449,7 +451,7 @@ __device__ __forceinline__ void multiply_tile(const moe_ep_matmul_args &a, const
             float y[4 * V];
 #pragma unroll
             for (int e = 0; e < 4 * V; ++e)
-                y[e] = (float)acc[i + e / 4][j][e % 4] * (sx[j] * sw[i + e / 4][e % 4]);
+                y[e] = ((float)acc[i + e / 4][j][e % 4] * sw[i + e / 4][e % 4]) * sx[j];
             if (a.n - n >= 4 * V) { // the last channels' n + 4 V may pass 2^31
                 *reinterpret_cast<AnyAligned *>(out + 16 * i * RowType<T>::kBytes) = RowType<T>::pack(y);
             } else {

@@ -417,7 +417,8 @@ int moe_ep_expert_unsort_backward(const moe_ep_unsort_grad_args *args, void *str
  * Product of int8 rows with each expert's int8 weights:
  *  out[m][n] = x_scales[m] * w_scales[e][n] * sum over k of x[m][k] * w[e][n][k]
  * for the rows offsets[e] <= m < offsets[e+1] of every expert e, the sum
- * exact in int32, the scaling in fp32, one rounding to out_type.  offsets
+ * exact in int32, the scaling in fp32 ((sum * w_scale) * x_scale, so that rows
+ * of any magnitude keep their result), one rounding to out_type.  offsets
  * [E + 1] ascends and is read on the device, each entry taken as at most
  * num_rows; rows outside every expert's range are left alone.  offsets NULL:
  * a dense product, num_experts = 1 and every row.  k a multiple of 16 and at

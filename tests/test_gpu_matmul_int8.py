@@ -179,3 +179,25 @@ def test_most_channels(X):
             assert not bool(y[m, 300:-300].any())
         assert bool((room[M * N:] == 3).all())
         del room, y
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,N,K", [(5, 24, 64), (130, 40, 1040)])
+def test_scales_of_extreme_rows(X, M, N, K, dtype):
+    """Rows of any magnitude that fp32 holds: the scales' own product may be below fp32 (rows of about 2^-130) or past
+    it (2^125 by channels of 2^4) where the result is not, and a sum of zero stays zero beside it."""
+    rng = np.random.default_rng(M)
+    x, w, sx, sw = _inputs(rng, M, 1, N, K)
+    sw = sw * 2.0 ** -10
+    exponent = torch.tensor([-135.0, -126.0, -118.0, 95.0, 0.0])[torch.arange(M) % 5]
+    sx = sx.double().mul(torch.exp2(exponent.double())).float()
+    w[0, 7] = 0          # sums of zero, with scales whose product with the rows' is past fp32
+    sw[0, 7] = 2.0 ** 100
+    ref = _reference(x, w, sx, sw, [0, M])
+    assert bool((ref[:, 7] == 0).all()) and float(ref.abs().max()) < 2.0 ** 127
+    got = X.expert_matmul(x.cuda(), sx.cuda(), w[0].cuda(), sw[0].cuda(), dtype=dtype)
+    # three roundings and the last one's; among the smallest numbers the last fp32 one is off by up to half of
+    # 2^-149 and the one to bf16 by up to half of 2^-133
+    bound = ((U.unit(dtype) + 3.01 * U.U32 * (1 + U.unit(dtype))) * ref.abs() + 2.0 ** -150 +
+             (2.0 ** -134 if dtype == BF else 0.0))
+    U.check_close(got, ref, bound, "scaled product")
