@@ -192,7 +192,7 @@ __global__ __launch_bounds__(BS) void add_rms_norm_kernel(moe_ep_norm_args a)
                         codes = kNanCodes;
                     if (head)
                         static_cast<float *>(a.scales)[(first + i) >> kLog] =
-                            t >= kInfinity ? __uint_as_float(0x7FC00000u) : m * (1.0f / 448.0f);
+                            t >= kInfinity ? __uint_as_float(0x7FC00000u) : m / 448.0f;
                 }
                 store_codes(a.out, first + i, codes);
             }

@@ -474,8 +474,9 @@ int moe_ep_silu_mul_quantize(const moe_ep_silu_args *args, void *stream);
  *    block's magnitudes within 448 (b = 0 for a block of zeros; the FP8
  *    combine's rule: nothing saturates), code = y / scale to nearest even; a
  *    block with a NaN or an infinity in y has b = 255 and codes 0x7F
- *   DEEPSEEK_FP8: scale = amax / 448 (0 and codes 0 for a block of zeros;
- *    NaN and codes 0x7F for one with a NaN or an infinity)
+ *   DEEPSEEK_FP8: scale = amax / 448, code = y * (448 / amax), product and
+ *    quotient each rounded to fp32, to nearest even (scale 0 and codes 0 for
+ *    a block of zeros; NaN and codes 0x7F for one with a NaN or an infinity)
  * A row in which s holds a NaN or an infinity, or whose sum of squares passes
  * fp32, has y = NaN throughout; a row of zeros with eps = 0 too.
  * H a multiple of 16 (INT8), 32, 128, at most 32768.  residual_out may be

@@ -169,3 +169,32 @@ def test_silu_rows_and_special_values(X):
     offsets[3] = 1000
     got = X.silu_mul_quantize(x, offsets=offsets)
     assert np.array_equal(U.bits(got.rows), U.bits(want.rows))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("fmt", ["int8", "mxfp8", "deepseek_fp8"])
+def test_scales_and_codes_are_the_definitions(X, fmt, dtype):
+    """Rows of 1 and -1 have the norm 1, so that y is the weight with their signs: the scales are the quotients of
+    the largest magnitudes, correctly rounded, and the codes those of the values by the format's rule, exactly."""
+    log(f"norm definitions {fmt} {dtype}")
+    H, M = 4096, 5
+    rng = np.random.default_rng(17)
+    w = torch.from_numpy((rng.standard_normal(H) * np.exp2(rng.integers(-60, 60, size=H // 128).repeat(128))).astype(
+        np.float32)).to(dtype)
+    x = torch.from_numpy(rng.choice(np.float32([-1, 1]), size=(M, H))).to(dtype)
+    n = X.add_rms_norm(x.cuda(), None, w.cuda(), 0.0, format=fmt)
+    y = (x.float() * w.float()).view(M, -1, {"int8": H, "mxfp8": 32, "deepseek_fp8": 128}[fmt])
+    top = y.abs().amax(2, keepdim=True)
+    codes, scales = n.rows.cpu().float().view(y.shape), n.scales.cpu().view(top.shape)
+    if fmt == "int8":
+        assert torch.equal(scales, top / 127)
+        q = 127 * y.double() / top.double()
+        assert bool(((codes - q).abs() <= 0.5 + 2.0 ** -15).all())
+    elif fmt == "mxfp8":
+        e = torch.ceil(torch.log2(top.double() / 448))  # none of the largest magnitudes is 448 times a power of two
+        assert torch.equal(scales.view(torch.uint8).double(), e + 127)
+        assert torch.equal(codes, (y.double() / torch.exp2(e)).float().to(torch.float8_e4m3fn).float())
+    else:
+        assert torch.equal(scales, top / 448)
+        # y * (448 / amax), each rounded to fp32 (torch takes `448 / top` as a reciprocal times 448, rounded twice)
+        assert torch.equal(codes, (y * (torch.full_like(top, 448.0) / top)).to(torch.float8_e4m3fn).float())
