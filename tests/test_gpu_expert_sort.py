@@ -309,3 +309,38 @@ def test_most_pairs(X):
     gr, gw = X.expert_unsort_backward(s.position, rows, s.rows, grad_rows=s.rows, need_weights=False)
     for e in range(E):
         assert torch.equal(gr.view(E, S, 2, H)[e, :, 1], rows[0])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("H", [16, 1056])
+def test_more_slots_than_workgroups(X, H, dtype):
+    """A workgroup's second slot is what it is in a call of its own (2^22 workgroups at most), in the quantising
+    sort, the weighted way back and both gradients; small whole numbers make every sum exact."""
+    S, E = (1 << 22) + 77, 3
+    log(f"slots past the grid S{S} H{H} {dtype}")
+    if torch.cuda.mem_get_info()[0] < 120 << 30:
+        pytest.skip("needs 120 GiB of free device memory")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(H)
+    ids = torch.randint(0, E, (1, S, 1), generator=g, device="cuda", dtype=torch.int32)
+    x = torch.randint(-8, 9, (1, S, H), generator=g, device="cuda", dtype=torch.int8).to(dtype)
+    s = X.expert_sort(ids, x, E, quantize=True)
+    p = s.position[0, :, 0].long()
+    assert torch.equal(p[torch.argsort(ids.view(-1), stable=True)], torch.arange(S, device="cuda"))
+    for part in (slice(0, S // 2), slice(S // 2, S)):
+        t = X.expert_sort(ids[:, part].contiguous(), x[:, part].contiguous(), E, quantize=True)
+        q = t.position[0, :, 0].long()
+        assert torch.equal(s.scales[p[part]], t.scales[q])
+        assert torch.equal(s.rows[p[part]], t.rows[q])
+        del t, q
+    position = s.position
+    del s
+    w = torch.exp2(torch.randint(-2, 3, (1, S, 1), generator=g, device="cuda").float())
+    rows = torch.empty_like(x[0])
+    rows[p] = x[0]
+    out = X.expert_unsort(position, rows, w)
+    assert torch.equal(out, (x.float() * w).to(dtype))
+    go = out.mul_(2)  # some other whole or binary fractions
+    gr, gw = X.expert_unsort_backward(position, go, rows, w)
+    assert torch.equal(gw[0, :, 0], (x[0].float() * go[0].float()).sum(1))
+    assert torch.equal(gr[p], (w[0] * go[0].float()).to(dtype))

@@ -198,3 +198,61 @@ def test_scales_and_codes_are_the_definitions(X, fmt, dtype):
         assert torch.equal(scales, top / 448)
         # y * (448 / amax), each rounded to fp32 (torch takes `448 / top` as a reciprocal times 448, rounded twice)
         assert torch.equal(codes, (y * (torch.full_like(top, 448.0) / top)).to(torch.float8_e4m3fn).float())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("fmt", ["int8", "mxfp8", "deepseek_fp8"])
+@pytest.mark.parametrize("M,H", [(1, 128), (1025, 128), (4099, 256), (700, 1152), (300, 4224)])
+def test_add_rms_norm_of_many_rows(X, M, H, fmt, dtype):
+    """Every row and block against the 64-bit reference, no block of zeros."""
+    log(f"norm of many rows M{M} H{H} {fmt} {dtype}")
+    rng = np.random.default_rng(M * H)
+    draw = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32))  # noqa: E731
+    x, res, w = draw(M, H).to(dtype), (4 * draw(M, H)).to(dtype), (1 + 0.2 * draw(H)).to(dtype)
+    s, y = _reference(x, res, w, 1e-5)
+    n = X.add_rms_norm(x.cuda(), res.cuda(), w.cuda(), 1e-5, format=fmt)
+    U.check_close(n.residual, s, (U.unit(dtype) + U.U32) * s.abs() * 1.001, "residual")
+    if fmt == "int8":
+        U.check_int8(n.rows, n.scales, y, Y_REL, "int8")
+        assert bool((n.scales > 0).all())
+        # the largest value of a row has the code 127 or -127
+        assert bool((n.rows.abs().amax(1) == 127).all())
+    else:
+        _check_blocks(n.rows, n.scales, y, fmt, Y_REL)
+
+
+def test_codes_of_zero_rows_are_zeros(X):
+    """Where the scale is 0 the codes are: rows of zeros, and a weight of zeros."""
+    x = torch.randn(70, 128, device="cuda")
+    x[::3] = 0
+    n = X.add_rms_norm(x, None, torch.ones(128, device="cuda"), format="int8")
+    assert torch.equal(n.scales == 0, (x == 0).all(1)) and not bool(n.rows[::3].any()) and bool(n.rows[1::3].any())
+    q = X.silu_mul_quantize(x)
+    assert torch.equal(q.scales == 0, (x == 0).all(1)) and not bool(q.rows[::3].any()) and bool(q.rows[1::3].any())
+    for fmt in ("int8", "mxfp8", "deepseek_fp8"):
+        n = X.add_rms_norm(x, None, torch.zeros(128, device="cuda"), format=fmt)
+        assert not bool(n.rows.float().any()) and not bool(n.scales.view(torch.uint8).any())
+
+
+@pytest.mark.parametrize("H", [128, 1024, 4096])
+def test_more_rows_than_workgroups(X, H):
+    """A workgroup's second row is what it is in a call of its own (2^20 workgroups at most; 64, 128 and 256 threads)."""
+    M, half = (1 << 20) + 77, 1 << 19
+    log(f"rows past the grid M{M} H{H}")
+    g = torch.Generator(device="cuda")
+    g.manual_seed(H)
+    x = torch.randn((M, H), generator=g, device="cuda", dtype=BF)
+    w = torch.randn(H, generator=g, device="cuda", dtype=BF)
+    parts = [slice(0, half), slice(half, 2 * half), slice(2 * half, M)]
+    for fmt in ("int8", "mxfp8", "deepseek_fp8"):
+        n = X.add_rms_norm(x, x, w, format=fmt)
+        for p in parts:
+            m = X.add_rms_norm(x[p], x[p], w, format=fmt)
+            assert torch.equal(n.rows[p].view(torch.uint8), m.rows.view(torch.uint8)), fmt
+            assert torch.equal(n.scales[p].view(torch.uint8), m.scales.view(torch.uint8)), fmt
+            assert torch.equal(n.residual[p], m.residual), fmt
+        del n, m
+    a = X.silu_mul_quantize(x)
+    for p in parts:
+        b = X.silu_mul_quantize(x[p])
+        assert torch.equal(a.rows[p], b.rows) and torch.equal(a.scales[p], b.scales)
