@@ -168,7 +168,8 @@ class _On:
             self.contexts.append(torch.cuda.device(dev))
         if stream is not None:
             if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=dev)
+                # torch takes 0 for "some stream of the pool", not for the default stream's handle
+                stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
             if stream.device != dev:
                 _refuse(f"the stream is on {stream.device}, the tensors on {dev}")
             self.contexts.append(torch.cuda.stream(stream))

@@ -534,3 +534,31 @@ def test_gradients_at_any_address(X):
                          torch.autograd.grad(s.rows, xl, gs, retain_graph=True))
         got = torch.autograd.grad(y.sum(), (xl, wl), retain_graph=True)
         assert _same(got, torch.autograd.grad(y, (xl, wl), torch.ones_like(y)))
+
+
+def test_the_default_streams_raw_handle(X):
+    """stream=0 is the default stream (the handle of torch's current stream at first): a call waits for the inputs
+    that it is still making, and work there waits for the call."""
+    rng = np.random.default_rng(6)
+    weights = _weights(rng, 8, 256, 96) + (torch.ones(256, dtype=BF, device="cuda"),)
+    assert torch.cuda.current_stream().cuda_stream == 0
+    a, b = _state(rng, 21, S=600), _state(rng, 22, S=600)
+    want = [_layer(X, st, weights) for st in (a, b)]
+    held = {k: v.clone() for k, v in a.items()}
+    for turn in range(4):
+        torch.cuda._sleep(10_000_000)
+        for k, v in held.items():
+            v.copy_((a, b)[turn & 1][k])
+        got = [t.clone() for t in _layer(X, held, weights, stream=torch.cuda.current_stream().cuda_stream)]
+        torch.cuda.synchronize()
+        assert _same(got, want[turn & 1]), turn
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # the argument, not the current stream, says where
+        out = X.expert_sort(held["ids"], held["rows"], 4, stream=0)
+    assert torch.equal(out.position, X.expert_sort(held["ids"], held["rows"], 4).position)
+    on = X._On(held["rows"].device, 0)
+    with torch.cuda.stream(side):
+        with on:
+            assert torch.cuda.current_stream().cuda_stream == 0
+        assert torch.cuda.current_stream().cuda_stream == side.cuda_stream
