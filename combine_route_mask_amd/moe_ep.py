@@ -146,7 +146,8 @@ def _torch_stream(stream):
     if stream is None:
         return torch.cuda.current_stream()
     if isinstance(stream, int):
-        return torch.cuda.ExternalStream(stream)
+        # torch takes 0 for "some stream of the pool", not for the default stream's handle
+        return torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
     return stream
 
 

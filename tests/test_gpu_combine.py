@@ -343,3 +343,22 @@ def test_combine_fp8_landing_above_256mib():
     ex.destroy()
     del eo, y, ex
     torch.cuda.empty_cache()
+
+
+def test_combine_on_the_default_streams_raw_handle():
+    """stream=0 is the default stream, where the output that combine allocates is also filled: the step equals
+    the one without a stream argument, behind unfinished work too."""
+    from combine_route_mask_amd import moe_ep
+    w = W.TINY
+    c, ex, valid = _dispatch(w, 17)
+    eo = _poison(W.draw_expert_output(w.P, w.T, w.H, 17, device="cuda"), valid)
+    want = ex.combine(eo).clone()
+    assert moe_ep._torch_stream(0).cuda_stream == 0
+    held = torch.zeros_like(eo)
+    for _ in range(3):
+        torch.cuda._sleep(10_000_000)
+        held.copy_(eo)
+        got = ex.combine(held, stream=0)
+        assert np.array_equal(bits16(got), bits16(want))
+        held.zero_()
+    ex.destroy()
