@@ -68,8 +68,8 @@ constexpr int kUnit = 64; // tiles begin this many rows apart, or a multiple
 // know them).  Tiles are numbered by expert, band of kBand row tiles, channel
 // tile, row tile, and each of the eight XCDs (workgroup number modulo 8) takes
 // a run of them: the tiles that run at a time on its 32 CUs are 4 x 8, which
-// read the least through its L2 (8192 x 8192 x 8192: 444 us; in columns of all
-// row tiles 512 us, bands of 6 and 8 456).  An expert's row tiles are of even
+// read the least through its L2 (8192 x 8192 x 8192: 429 us; bands of 6 423, of
+// 8 441, columns of all row tiles 462).  An expert's row tiles are of even
 // height.  Of BM and TALL the finder takes what the CUs are done with first:
 // a tile takes about as long as 76 rows and its own.
 template <int BM, int TALL>
@@ -557,7 +557,9 @@ hipError_t tile_launch(const moe_ep_matmul_args &a, hipStream_t s)
 //    104 / 127; E 1, 7168 x 7168, 1024 rows (112 tiles) 78 / 57.  Not for
 //    k below 1024: E 32, 2048 x 512, 192 rows 21 / 19, 512 rows 37 / 35.
 //    With tiles of up to 256 rows only, an expert somewhat above that takes
-//    two: E 32, 4096 x 4096, 256 rows 167 / 215, 512 rows 280 / 297;
+//    two: E 32, 4096 x 4096, 256 rows 167 / 215, 512 rows 280 / 297.  The
+//    320-row shape takes all 256 registers and spills 5 or 6 of them (24 or 28
+//    bytes of scratch a lane); without it the kernel has 220 and spills none;
 //  - up to 128 x 128, four waves, two workgroups a CU; for at most 32 rows an
 //    expert its 64-row shape with three stages in place of two: E 32,
 //    4096 x 4096, 1 row 66 / 76, but 64 rows 114 / 105;

@@ -254,12 +254,11 @@ hipError_t norm_launch(const moe_ep_norm_args &a, hipStream_t s)
 }
 
 // Two units a thread keep more waves on a row than four: 32768 rows of 7168
-// bf16 to DeepSeekFp8 took 319 us with 512 threads of two units, 344 with 256
-// of four, 364 with 128 of seven, 334 with 1024 of one, and one row 4.1 / 5.8
-// / 8.5 / 3.6 us (before the lanes' maxima moved from LDS shuffles to DPP,
-// which took the 319 us to 278: 5.9 TB/s; MXFP8 269 us, int8 298).  One
-// workgroup a row: 2048 workgroups that loop over rows gained 4% there but
-// lost 6% on int8.
+// bf16 to DeepSeekFp8 take 266 us (6.2 TB/s) with 512 threads of two units, 277
+// with 256 of four, 325 with 128 of seven, 296 with 1024 of one; to int8 262 /
+// 273 / 318 / 301, to MXFP8 266.  A call of one row takes 8 us in every shape.
+// One workgroup a row: 2048 workgroups that loop over the rows take 285 us for
+// each format.
 template <typename T, int FMT>
 hipError_t norm_shape(const moe_ep_norm_args &a, hipStream_t s)
 {

@@ -283,7 +283,9 @@ int moe_ep_reduce_scatterv(int32_t ep_size, const int32_t *sizes, int32_t hidden
  * captured into a HIP graph.  Buffers belong to the current HIP device; an
  * output overlaps no other buffer of its call unless stated otherwise.
  * Calls whose output, workspace or index buffers overlap must be ordered by
- * the caller; calls on buffers of their own may run at the same time.
+ * the caller; calls on buffers of their own may run at the same time.  A call
+ * that launches clears an error that an earlier HIP call of its thread left
+ * pending (hipGetLastError), and does not report it as its own.
  * Every call takes one argument block, all pointers device pointers.
  * --------------------------------------------------------------------- */
 
@@ -445,8 +447,10 @@ int moe_ep_expert_matmul(const moe_ep_matmul_args *args, void *stream);
  * Gated activation between the two expert products: for the first
  * min(*num_valid, num_rows) rows (num_valid NULL: all; offsets + E of the
  * sort), a = silu(x[:, :I]) * x[:, I:] in fp32, as int8 codes and one scale
- * a row (as the quantising sort's); other rows are left alone.  I a multiple
- * of 16, at most 32768.
+ * a row (as the quantising sort's); other rows are left alone.  silu(g) is
+ * g / (1 + exp(-g)), relative error up to (2 |g| + 10) * 2^-24; where exp(-g)
+ * passes fp32 (g below -88.7) it is -0, and NaN for g = -infinity.  I a
+ * multiple of 16, at most 32768.
  */
 typedef struct moe_ep_silu_args {
     const void *x;               /* [num_rows][2 * I] row_type               */
@@ -478,7 +482,8 @@ int moe_ep_silu_mul_quantize(const moe_ep_silu_args *args, void *stream);
  *    quotient each rounded to fp32, to nearest even (scale 0 and codes 0 for
  *    a block of zeros; NaN and codes 0x7F for one with a NaN or an infinity)
  * A row in which s holds a NaN or an infinity, or whose sum of squares passes
- * fp32, has y = NaN throughout; a row of zeros with eps = 0 too.
+ * fp32, has y = NaN throughout; a row of zeros with eps = 0 too.  Squares lose
+ * bits below 2^-126 and vanish below 2^-150, which only an eps near 0 shows.
  * H a multiple of 16 (INT8), 32, 128, at most 32768.  residual_out may be
  * residual or x itself; NULL: not written.
  */
