@@ -241,17 +241,14 @@ struct Fragments {
     i32x4 x[2][S::FM], w[2 * S::FN];
 };
 
-// A fragment out of a stage.  Nothing else touches the stage within a read, and
-// __restrict__ says so: without it each read would be made to wait for all loads
-// on their way to LDS, wherever to.
 template <typename S>
-__device__ __forceinline__ void read_x(const uint8_t *__restrict__ stage, const Operands<S> &o, Fragments<S> &f, int h, int j)
+__device__ __forceinline__ void read_x(const uint8_t *stage, const Operands<S> &o, Fragments<S> &f, int h, int j)
 {
     f.x[h][j] = *reinterpret_cast<const i32x4 *>(stage + o.xat[h] + 16 * j * kTileK);
 }
 
 template <typename S>
-__device__ __forceinline__ void read_w(const uint8_t *__restrict__ stage, const Operands<S> &o, Fragments<S> &f, int i)
+__device__ __forceinline__ void read_w(const uint8_t *stage, const Operands<S> &o, Fragments<S> &f, int i)
 {
     f.w[i] = *reinterpret_cast<const i32x4 *>(stage + o.wat[i / S::FN] + 16 * (i % S::FN) * kTileK);
 }
