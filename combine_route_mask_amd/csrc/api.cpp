@@ -10,7 +10,7 @@
 #include <string>
 #include <unordered_set>
 
-#include "experts_internal.h"
+#include "api_checks.h"
 #include "moe_ep.h"
 #include "moe_ep_internal.h"
 
@@ -165,7 +165,6 @@ int check_params(const moe_ep_params *pp, Layout *lay)
     return MOE_EP_OK;
 }
 
-bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 bool live_handle(const moe_ep_handle *h)
 {

@@ -5,6 +5,7 @@
 #include <cmath>
 #include <string>
 
+#include "api_checks.h"
 #include "experts_internal.h"
 
 using namespace moe_ep;
@@ -12,43 +13,6 @@ using namespace moe_ep;
 namespace {
 
 constexpr int64_t kMaxRowBytes = 1 << 24;
-
-bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-int bad(const char *msg) { return fail(MOE_EP_ERR_INVALID_ARG, msg); }
-
-// A required device pointer: present and aligned.
-bool good(const void *p, uintptr_t a) { return p && aligned(p, a); }
-
-template <typename F>
-int guarded(F f)
-{
-    try {
-        return f();
-    } catch (...) {
-        return MOE_EP_ERR_HIP; // no memory for a message
-    }
-}
-
-// Launches; an error that an earlier call of the thread left behind is not
-// this call's.
-template <typename F>
-int launched(const char *what, F launch)
-{
-    (void)hipGetLastError();
-    const hipError_t e = launch();
-    if (e == hipErrorInvalidConfiguration) // the launchers' own limit
-        return fail(MOE_EP_ERR_CAPACITY, std::string(what) + " needs more workgroups than a launch holds");
-    if (e != hipSuccess)
-        return fail(MOE_EP_ERR_HIP, std::string(what) + " launch failed: " + hipGetErrorString(e));
-    return ok();
-}
-
-// Bytes of one element, 0 for an unknown type.
-int64_t item_bytes(int32_t row_type)
-{
-    return row_type == MOE_EP_BF16_ROWS ? 2 : row_type == MOE_EP_FP32_ROWS ? 4 : 0;
-}
 
 int check_slots(int32_t ranks, int32_t slots, int32_t top_k)
 {

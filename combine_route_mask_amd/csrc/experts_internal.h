@@ -6,15 +6,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <string>
-
 #include "moe_ep.h"
 
 namespace moe_ep {
-
-// Message and code of the calling thread's last call (api.cpp).
-int fail(int code, const std::string &msg);
-int ok();
 
 // A sort's ids are cut into tiles of this many pairs (whole slots).
 constexpr int kSortTilePairs = 1024;

@@ -68,22 +68,6 @@ __device__ __forceinline__ u32x2 int8_codes(const Int8Row &rule, const float *f)
     return u32x2{rule.codes4(f), rule.codes4(f + 4)};
 }
 
-// e4m3 codes of f * by, round to nearest even; every product is within 448
-// times 1 + 2^-22, which rounds to 448.
-__device__ __forceinline__ u32x2 e4m3_codes(const float *f, float up, float by)
-{
-    u32x2 v;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        int p = __builtin_amdgcn_cvt_pk_fp8_f32((f[4 * h] * up) * by, (f[4 * h + 1] * up) * by, 0, false);
-        p = __builtin_amdgcn_cvt_pk_fp8_f32((f[4 * h + 2] * up) * by, (f[4 * h + 3] * up) * by, p, true);
-        v[h] = (uint32_t)p;
-    }
-    return v;
-}
-
-constexpr u32x2 kNanCodes = {0x7F7F7F7Fu, 0x7F7F7F7Fu};
-
 // Rows r, r + grid, ...: thread t holds the 8-element units t, t + BS, ...
 template <typename T, int FMT, int BS, int VPT>
 __global__ __launch_bounds__(BS) void add_rms_norm_kernel(moe_ep_norm_args a)
@@ -174,10 +158,7 @@ __global__ __launch_bounds__(BS) void add_rms_norm_kernel(moe_ep_norm_args a)
                 const bool head = (threadIdx.x & ((1 << kLog) - 1)) == 0;
                 u32x2 codes;
                 if (FMT == MOE_EP_NORM_MXFP8) {
-                    // 448 = 1.75 * 2^8: t = 1.m * 2^E needs 2^(E - 8), or
-                    // 2^(E - 7) when 1.m > 1.75
-                    int e = (int)(t >> 23) - 127 - 8 + ((t & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-                    e = (t >> 23) == 0 || e < -127 ? -127 : e;
+                    const int e = mx_exponent(t);
                     codes = e4m3_codes(f[u], 1.0f, __uint_as_float((uint32_t)(127 - e) << 23));
                     if (t >= kInfinity)
                         codes = kNanCodes;

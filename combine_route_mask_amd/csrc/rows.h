@@ -189,4 +189,58 @@ struct Int8Row {
     }
 };
 
+// e4m3 codes of f * by, round to nearest even; every product is within 448
+// times 1 + 2^-22, which rounds to 448.
+__device__ __forceinline__ u32x2 e4m3_codes(const float *f, float up, float by)
+{
+    u32x2 v;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        int p = __builtin_amdgcn_cvt_pk_fp8_f32((f[4 * h] * up) * by, (f[4 * h + 1] * up) * by, 0, false);
+        p = __builtin_amdgcn_cvt_pk_fp8_f32((f[4 * h + 2] * up) * by, (f[4 * h + 3] * up) * by, p, true);
+        v[h] = (uint32_t)p;
+    }
+    return v;
+}
+
+constexpr u32x2 kNanCodes = {0x7F7F7F7Fu, 0x7F7F7F7Fu};
+
+// Exponent of an MXFP8 block's scale for the bits of its largest magnitude:
+// 448 = 1.75 * 2^8, so 1.m * 2^E needs 2^(E - 8), or 2^(E - 7) when 1.m > 1.75.
+__device__ __forceinline__ int mx_exponent(uint32_t top)
+{
+    const int e = (int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return (top >> 23) == 0 || e < -127 ? -127 : e;
+}
+
+// The MXFP8 codes of 8 elements whose block's largest magnitude is `top`, and
+// the block's scale byte.  A block with a NaN or an infinity is NaN.
+__device__ __forceinline__ u32x2 mx_codes(const float *f, uint32_t top, uint8_t &scale)
+{
+    const int e = mx_exponent(top);
+    scale = top >= kInfinity ? 0xFF : (uint8_t)(e + 127);
+    return top >= kInfinity ? kNanCodes : e4m3_codes(f, 1.0f, __uint_as_float((uint32_t)(127 - e) << 23));
+}
+
+// 2^(b - 127) of an e8m0 byte; NaN for 255.
+__device__ __forceinline__ float e8m0_value(uint32_t b)
+{
+    return __uint_as_float(b == 255 ? 0x7FC00000u : b == 0 ? 0x00400000u : b << 23);
+}
+
+// 8 e4m3 codes times a scale.
+__device__ __forceinline__ void mx_values(u32x2 codes, float scale, float *f)
+{
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes[h], false);
+        const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes[h], true);
+        f[4 * h] = a[0] * scale;
+        f[4 * h + 1] = a[1] * scale;
+        f[4 * h + 2] = b[0] * scale;
+        f[4 * h + 3] = b[1] * scale;
+    }
+}
+
 } // namespace moe_ep

@@ -40,7 +40,10 @@ EXPORTS = ("moe_ep_is_supported", "moe_ep_workspace_bytes", "moe_ep_create", "mo
            "moe_ep_combine", "moe_ep_combine_noalloc", "moe_ep_destroy", "moe_ep_allgatherv",
            "moe_ep_reduce_scatterv", "moe_ep_expert_sort_workspace_bytes", "moe_ep_expert_sort",
            "moe_ep_expert_unsort", "moe_ep_expert_unsort_backward", "moe_ep_expert_matmul",
-           "moe_ep_silu_mul_quantize", "moe_ep_add_rms_norm", "moe_ep_last_error")
+           "moe_ep_silu_mul_quantize", "moe_ep_add_rms_norm", "moe_ep_route_top_k",
+           "moe_ep_route_top_k_backward", "moe_ep_checkpoint_rows", "moe_ep_restore_rows", "moe_ep_expert_product",
+           "moe_ep_gated_product", "moe_ep_gated_product_backward", "moe_ep_product_weight_grad",
+           "moe_ep_four_bit_product", "moe_ep_last_error")
 STATIC_SCRATCH_BYTES = 64 << 20  # MOE_EP_STATIC_SCRATCH_BYTES
 
 
@@ -106,9 +109,12 @@ def _load(path: str = LIB_PATH):
     L.moe_ep_reduce_scatterv.restype = C.c_int
     L.moe_ep_expert_sort_workspace_bytes.argtypes = [i32, i32, i32, i32]
     L.moe_ep_expert_sort_workspace_bytes.restype = i64
-    # the expert layer's calls take one packed argument block each (experts.py)
+    # the expert layer's calls take one packed argument block each (experts.py, ffn.py, router.py)
     for name in ("moe_ep_expert_sort", "moe_ep_expert_unsort", "moe_ep_expert_unsort_backward",
-                 "moe_ep_expert_matmul", "moe_ep_silu_mul_quantize", "moe_ep_add_rms_norm"):
+                 "moe_ep_expert_matmul", "moe_ep_silu_mul_quantize", "moe_ep_add_rms_norm", "moe_ep_route_top_k",
+                 "moe_ep_route_top_k_backward", "moe_ep_checkpoint_rows", "moe_ep_restore_rows",
+                 "moe_ep_expert_product", "moe_ep_gated_product", "moe_ep_gated_product_backward",
+                 "moe_ep_product_weight_grad", "moe_ep_four_bit_product"):
         getattr(L, name).argtypes = [C.c_char_p, vp]
         getattr(L, name).restype = C.c_int
     L.moe_ep_last_error.argtypes = []

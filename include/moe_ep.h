@@ -504,6 +504,215 @@ typedef struct moe_ep_norm_args {
 
 int moe_ep_add_rms_norm(const moe_ep_norm_args *args, void *stream);
 
+/* ---------------------------------------------------------------------
+ * The trainable expert layer: the router, the gated feed-forward block of
+ * experts in bf16 with its backward pass, 8-bit checkpoints of what the
+ * backward pass reads, and products with 4-bit weights.  The rules of the
+ * expert layer above hold: no handle, no state, nothing allocated, the
+ * caller's buffers and stream, one argument block of device pointers.
+ * offsets [E + 1] ascends and is read on the device, each entry taken as at
+ * most num_rows (the expert sort's): expert e's rows are offsets[e] ..
+ * offsets[e+1] - 1, other rows are never read and, unless stated otherwise,
+ * left alone in outputs.  offsets NULL: num_experts = 1 and every row.
+ * --------------------------------------------------------------------- */
+
+#define MOE_EP_MAX_ROUTED_EXPERTS 4096
+
+/*
+ * Router: the top_k largest of each token's num_experts logits and their
+ * weights.  Equal logits (0 and -0 are equal) go by ascending expert.  An
+ * expert whose logit is -infinity or NaN is never chosen: a place without an
+ * expert holds the id num_experts, which a dispatch routes nowhere, and the
+ * weight 0.  weights = scale * softmax in fp32, over the chosen experts
+ * (renormalize = 1) or over all (0).  A row with a NaN or +infinity has
+ * NaN weights in the places that hold an expert.  logits fp32 or bf16.
+ */
+typedef struct moe_ep_route_args {
+    const void *logits;          /* [tokens][num_experts] row_type           */
+    int32_t *ids;                /* [tokens][top_k]                          */
+    float *weights;              /* [tokens][top_k]                          */
+    int64_t tokens;
+    int32_t num_experts;         /* 1..4096                                  */
+    int32_t top_k;               /* 1..64, at most num_experts               */
+    int32_t renormalize;
+    int32_t row_type;            /* MOE_EP_*_ROWS                            */
+    float scale;                 /* finite                                   */
+    int32_t reserved;            /* 0                                        */
+} moe_ep_route_args;
+
+int moe_ep_route_top_k(const moe_ep_route_args *args, void *stream);
+
+/*
+ * Gradient of the router's weights for the logits, ids as the router chose
+ * them: with p the softmax that the weights came from (over the chosen
+ * experts or over all) and g = grad_weights,
+ *  grad_logits[i] = scale * p[i] * (g at i's place (0 without one) - sum over
+ *  places j of p[ids[j]] g[j]),
+ * 0 outside the softmax.  Places whose id is outside [0, num_experts) have no
+ * part in it.  An id may appear once a token.  fp32 sums in an order that the
+ * shape alone fixes, rounded once.
+ */
+typedef struct moe_ep_route_grad_args {
+    const void *logits;          /* [tokens][num_experts] row_type           */
+    const int32_t *ids;          /* [tokens][top_k]                          */
+    const float *grad_weights;   /* [tokens][top_k]                          */
+    void *grad_logits;           /* [tokens][num_experts] row_type           */
+    int64_t tokens;
+    int32_t num_experts;
+    int32_t top_k;
+    int32_t renormalize;
+    int32_t row_type;
+    float scale;
+    int32_t reserved;            /* 0                                        */
+} moe_ep_route_grad_args;
+
+int moe_ep_route_top_k_backward(const moe_ep_route_grad_args *args, void *stream);
+
+/*
+ * 8-bit checkpoint of rows: the MXFP8 payload's codes and scales (e4m3, an
+ * e8m0 scale 2^(b - 127) for 32 elements, the smallest power of two that
+ * keeps the block's magnitudes within 448; b = 0 for zeros, b = 255 and codes
+ * 0x7F for a block with a NaN or an infinity), and back.  restore: code *
+ * scale, which bf16 and fp32 hold exactly down to 2^-126.
+ * hidden_size a multiple of 32, at most 2^20.
+ */
+typedef struct moe_ep_checkpoint_args {
+    void *rows;                  /* [num_rows][H] row_type: read, or written by restore */
+    uint8_t *codes;              /* [num_rows][H]                            */
+    uint8_t *scales;             /* [num_rows][H / 32]                       */
+    int64_t num_rows;
+    int32_t hidden_size;
+    int32_t row_type;
+} moe_ep_checkpoint_args;
+
+int moe_ep_checkpoint_rows(const moe_ep_checkpoint_args *args, void *stream);
+int moe_ep_restore_rows(const moe_ep_checkpoint_args *args, void *stream);
+
+/*
+ * Product of bf16 rows with each expert's bf16 weights:
+ *  out[m][j] = sum over i of x[m][i] * w[e][j][i]   (transposed = 0, w [E][n][k])
+ *  out[m][j] = sum over i of x[m][i] * w[e][i][j]   (transposed = 1, w [E][k][n])
+ * in fp32, rounded once to bf16.  The order of the sum depends on the shape
+ * alone.  n and k multiples of 8, at most 131072.  zero_rest = 1: rows from
+ * the last expert's last on become zeros.
+ */
+typedef struct moe_ep_product_args {
+    const void *x;               /* [num_rows][k] bf16                       */
+    const void *w;               /* [E][n][k] or [E][k][n] bf16              */
+    const int32_t *offsets;      /* [E + 1] or NULL                          */
+    void *out;                   /* [num_rows][n] bf16                       */
+    int64_t num_rows;
+    int32_t num_experts;         /* 1..4096                                  */
+    int32_t n;
+    int32_t k;
+    int32_t transposed;
+    int32_t zero_rest;
+    int32_t reserved;            /* 0                                        */
+} moe_ep_product_args;
+
+int moe_ep_expert_product(const moe_ep_product_args *args, void *stream);
+
+#define MOE_EP_SAVE_NONE 0
+#define MOE_EP_SAVE_BF16 1   /* pre [num_rows][2 I] bf16                    */
+#define MOE_EP_SAVE_MXFP8 2  /* pre [num_rows][2 I] e4m3, pre_scales [num_rows][2 I / 32] */
+
+/*
+ * The gated block's first product and its activation: for pre = x w^T with w
+ * [E][2 I][k] (gate channels first), gate = pre[:I], up = pre[I:],
+ *  out = silu(gate) * up
+ * in fp32 from the unrounded sums, rounded once to bf16.  save: pre as the
+ * backward pass reads it, rounded to bf16 or as an 8-bit checkpoint (as
+ * moe_ep_checkpoint_rows makes of the unrounded sums; I a multiple of 32).
+ * I and k multiples of 8, at most 65536 and 131072.
+ */
+typedef struct moe_ep_gated_args {
+    const void *x;               /* [num_rows][k] bf16                       */
+    const void *w;               /* [E][2 * I][k] bf16                       */
+    const int32_t *offsets;      /* [E + 1] or NULL                          */
+    void *out;                   /* [num_rows][I] bf16                       */
+    void *pre;                   /* as `save` says, or NULL                  */
+    uint8_t *pre_scales;         /* MXFP8 only                               */
+    int64_t num_rows;
+    int32_t num_experts;
+    int32_t inter_size;          /* I                                        */
+    int32_t k;
+    int32_t save;                /* MOE_EP_SAVE_*                            */
+} moe_ep_gated_args;
+
+int moe_ep_gated_product(const moe_ep_gated_args *args, void *stream);
+
+/*
+ * Backward of the gated block down to its first product: for grad_out
+ * [num_rows][n] and the second weights w [E][n][I], with d = grad_out w and
+ * gate, up what `pre` holds, s = 1 / (1 + exp(-gate)),
+ *  grad_pre = [d * up * s * (1 + gate * (1 - s)), d * gate * s]
+ *  out      = gate * s * up   (the activation again, for the weights' gradient)
+ * in fp32, each rounded once to bf16.
+ */
+typedef struct moe_ep_gated_grad_args {
+    const void *grad_out;        /* [num_rows][n] bf16                       */
+    const void *w;               /* [E][n][I] bf16                           */
+    const int32_t *offsets;      /* [E + 1] or NULL                          */
+    const void *pre;             /* as `save` says                           */
+    const uint8_t *pre_scales;   /* MXFP8 only                               */
+    void *grad_pre;              /* [num_rows][2 * I] bf16                   */
+    void *out;                   /* [num_rows][I] bf16, or NULL              */
+    int64_t num_rows;
+    int32_t num_experts;
+    int32_t inter_size;          /* I                                        */
+    int32_t n;
+    int32_t save;                /* MOE_EP_SAVE_BF16 or _MXFP8               */
+} moe_ep_gated_grad_args;
+
+int moe_ep_gated_product_backward(const moe_ep_gated_grad_args *args, void *stream);
+
+/*
+ * Gradient of an expert product's weights:
+ *  grad_w[e][j][i] = sum over e's rows m of grad_out[m][j] * x[m][i]
+ * in fp32, in ascending blocks of rows, rounded once to bf16; zeros for an
+ * expert without rows.
+ */
+typedef struct moe_ep_weight_grad_args {
+    const void *grad_out;        /* [num_rows][n] bf16                       */
+    const void *x;               /* [num_rows][k] bf16                       */
+    const int32_t *offsets;      /* [E + 1] or NULL                          */
+    void *grad_w;                /* [E][n][k] bf16                           */
+    int64_t num_rows;
+    int32_t num_experts;
+    int32_t n;
+    int32_t k;
+    int32_t reserved;            /* 0                                        */
+} moe_ep_weight_grad_args;
+
+int moe_ep_product_weight_grad(const moe_ep_weight_grad_args *args, void *stream);
+
+/*
+ * Product of bf16 rows with each expert's 4-bit weights, made for a few rows
+ * an expert: out[m][j] = sum over i of x[m][i] * w[e][j][i], w = code * scale
+ * with e2m1 codes (two a byte, the even element in the low half) and an e8m0
+ * scale 2^(b - 127) for 32 elements of a row (MXFP4).  code * scale is exact
+ * in bf16 for b in 2..251; the sum is fp32 in an order that the shape fixes,
+ * rounded once to out_type.  gated = 1: n = 2 I channels, gate first, and
+ * out [num_rows][I] = silu(gate) * up from the unrounded sums.  b = 255 is
+ * NaN.  k a multiple of 32, at most 131072; n >= 1, even when gated, below 2^30.
+ */
+typedef struct moe_ep_four_bit_args {
+    const void *x;               /* [num_rows][k] bf16                       */
+    const uint8_t *w;            /* [E][n][k / 2]                            */
+    const uint8_t *w_scales;     /* [E][n][k / 32]                           */
+    const int32_t *offsets;      /* [E + 1] or NULL                          */
+    void *out;                   /* [num_rows][n], or [num_rows][n / 2]      */
+    int64_t num_rows;
+    int32_t num_experts;         /* 1..4096                                  */
+    int32_t n;
+    int32_t k;
+    int32_t gated;
+    int32_t out_type;            /* MOE_EP_*_ROWS                            */
+    int32_t reserved;            /* 0                                        */
+} moe_ep_four_bit_args;
+
+int moe_ep_four_bit_product(const moe_ep_four_bit_args *args, void *stream);
+
 /* Message of the calling thread's last failed call ("" if none). */
 const char *moe_ep_last_error(void);
 
