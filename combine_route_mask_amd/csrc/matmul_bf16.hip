@@ -5,7 +5,13 @@
 // v_mfma_f32_16x16x32_bf16: lane l holds 8 elements of row l % 16 at
 // k = 8 * (l / 16) of either matrix; of the result, element i is left row
 // 4 * (l / 16) + i and right row l % 16.  The left matrix is the channels',
-// the right one the rows'.
+// the right one the rows' (of the weights' gradient: x's columns and
+// grad_out's columns, summed over the rows).
+//
+// All of them are one loop over tiles whose operands lie in memory either
+// along k (an operand's row after another, k next to k) or across it (a k
+// after another).  An operand across k goes into LDS as it lies and is turned
+// by the transposing LDS read.
 #include "ffn_internal.h"
 #include "rows.h"
 #include "tiles.h"
@@ -15,70 +21,285 @@ namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 enum Epilogue { kStore, kGated, kGatedBackward };
 
 struct Job {
-    const uint16_t *x, *w;
+    const uint8_t *x, *w; // bf16
     const int32_t *offsets;
-    uint16_t *out;      // product, activation
-    void *pre;          // what the gated block saves or reads
+    uint16_t *out;        // product, activation
+    void *pre;            // what the gated block saves or reads
     uint8_t *pre_scales;
     uint16_t *grad_pre;
     int64_t num_rows;
     int num_experts, n, k, save;
 };
 
-constexpr int kEdge = 64, kDepth = 32, kPitch = kDepth + 8;
+// A workgroup takes BN channels and BM rows, 64 elements of k at a time,
+// through STAGES of LDS: the next stages go from memory straight into LDS
+// while this one is multiplied.  NW x MW waves, each FN x FM results of
+// 16 x 16.
+constexpr int kDepth = 64, kDepthBytes = 2 * kDepth;
 
-// [kEdge] rows of 32 elements into LDS: of rows that lie one after another
-// (ACROSS = false: element (i, k) at i * stride + k) or k after k (true).
-template <bool ACROSS, typename ROW>
-__device__ __forceinline__ void stage(uint16_t (*to)[kPitch], const uint16_t *from, int64_t stride, int k, int depth,
-                                      ROW row)
-{
-    const int t = threadIdx.x;
-    u32x4 v = {};
-    if (!ACROSS) {
-        const int i = t / 4, c = t % 4 * 8;
-        const int64_t r = row(i);
-        if (r >= 0 && k + c < depth)
-            v = *reinterpret_cast<const u32x4 *>(from + r * stride + k + c);
-        *reinterpret_cast<u32x4 *>(&to[i][c]) = v;
-    } else {
-        const int i = t / 8, c = t % 8 * 8;
-        const int64_t r = row(c);
-        if (k + i < depth && r >= 0)
-            v = *reinterpret_cast<const u32x4 *>(from + (k + i) * stride + r);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            to[c + e][i] = (uint16_t)(v[e / 2] >> (e % 2 * 16));
+template <int NW_, int MW_, int FN_, int FM_, int STAGES_>
+struct TileShape {
+    static constexpr int NW = NW_, MW = MW_, FN = FN_, FM = FM_, STAGES = STAGES_, W = NW * MW;
+    static constexpr int BN = NW * FN * 16, BM = MW * FM * 16, THREADS = 64 * W;
+    static constexpr int LN = BN / (8 * W), LM = BM / (8 * W); // loads of a thread and stage, 1024 bytes a wave
+    static constexpr int BYTES = (BN + BM) * kDepthBytes;
+    static_assert(BN % (8 * W) == 0 && BM % (8 * W) == 0);
+};
+
+// Where a tile's operand of EDGE rows lies in memory, for this thread's L loads
+// of a stage, and in LDS, for its fragments.
+//
+// Along k: an LDS row is 128 bytes of k of one operand row, all on the same
+// banks: chunk c (16 bytes) of row r lies at place c ^ (r & 7), so that 8 rows'
+// reads of one chunk cover all banks.
+//
+// Across k: an LDS row is one k of all EDGE operand rows.  A transposing read
+// takes, for 16 operand rows (32 bytes), four consecutive k in each 16 lanes;
+// unit u (32 bytes) of row r lies at place u ^ turn(r), so that the rows of a
+// read lie on different banks.
+//
+// HALF (along): LDS rows go by turns of HALF rows to two parts of the operand,
+// `second` bytes apart.
+template <bool ACROSS, int EDGE, int L, int W, int HALF = 0>
+struct Operand {
+    static_assert(HALF % 8 == 0);
+    static constexpr int kPitch = 2 * EDGE; // bytes of an LDS row across k
+    const uint8_t *base;
+    uint32_t offset[L];
+    uint32_t stride;  // bytes of a memory row
+    int64_t second;
+    uint32_t end;     // along: kPastEnd where the lane's chunk of the last step is past the end of k
+    int depth;        // across: elements of k
+    uint32_t at[2];   // along: the first fragment's place of either half of a step; across: at[0], its row's
+    int fragment, turned; // across: the wave's first unit, the lane's turn
+
+    static __device__ __forceinline__ int turn(int k)
+    {
+        if constexpr (EDGE % 128 == 0)
+            return (k & 3) | ((k >> 3) & 1) << 2;
+        else if constexpr (EDGE % 64 == 0)
+            return ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
+        else
+            return (k >> 3) & 1;
     }
-}
 
-__device__ __forceinline__ void multiply(uint16_t (*a)[kPitch], uint16_t (*b)[kPitch], f32x4 (*acc)[2])
-{
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, l4 = lane >> 4;
+    // `first`: of the operand's row 0 at k = 0.  `rows` of them there are, and
+    // `map(r)` is the row that LDS row (or column) r holds; rows past the last
+    // read another one's, and their results are not stored.  `fragment`: the
+    // wave's first one.
+    template <typename MAP>
+    __device__ __forceinline__ void find(const uint8_t *first, uint32_t stride_, int k, int wave, int fragment_, MAP map)
+    {
+        const int lane = threadIdx.x & 63, l16 = lane & 15, l4 = lane >> 4;
+        base = first;
+        stride = stride_;
+        depth = k;
+        end = 0;
+        fragment = fragment_;
+        turned = 0;
+        if constexpr (!ACROSS) {
+            const int sub = lane / 8;
+            const uint32_t chunk = (uint32_t)((lane % 8) ^ sub) * 16;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const bf16x8 u = *reinterpret_cast<const bf16x8 *>(&a[(wave & 1) * 32 + i * 16 + l16][8 * l4]);
+            for (int i = 0; i < L; ++i)
+                offset[i] = (uint32_t)map((i * W + wave) * 8 + sub) * stride + chunk;
+            const int steps = (k + kDepth - 1) / kDepth;
+            end = (steps - 1) * kDepthBytes + chunk < (uint32_t)(2 * k) ? 0 : kPastEnd;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const bf16x8 v = *reinterpret_cast<const bf16x8 *>(&b[(wave >> 1) * 32 + j * 16 + l16][8 * l4]);
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(u, v, acc[i][j], 0, 0, 0);
+            for (int h = 0; h < 2; ++h)
+                at[h] = (uint32_t)(((h * 4 + l4) ^ (l16 & 7)) * 16 + (16 * fragment + l16) * kDepthBytes);
+        } else {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const int byte = (i * W + wave) * 1024 + lane * 16, row = byte / kPitch;
+                const int chunk = (byte % kPitch / 16) ^ (2 * turn(row));
+                offset[i] = (uint32_t)row * stride + 16 * (uint32_t)map(chunk);
+            }
+            const int row = 8 * l4 + l16 / 4;
+            at[0] = (uint32_t)(row * kPitch + l16 % 4 * 8);
+            at[1] = 0;
+            turned = turn(row);
         }
     }
+
+    // Load i of step `step` (of `steps`; later ones bring nothing).
+    __device__ __forceinline__ void load(uint8_t *part, int wave, int i, int step, int steps, bool past) const
+    {
+#if defined(__HIP_DEVICE_COMPILE__) // the host compiler does not know the resource type
+        uint8_t *to = part + (i * W + wave) * 1024;
+        int64_t ahead = ACROSS ? (int64_t)step * kDepth * stride : (int64_t)step * kDepthBytes;
+        if constexpr (HALF > 0)
+            ahead += (i * W + wave) * 8 / HALF % 2 ? second : 0;
+        // rows of k past the end are beyond the buffer: zeros
+        const int left = ACROSS ? min(depth - step * kDepth, kDepth) * (int)stride : 0x7FFFFFFF;
+        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base + ahead), 0,
+                                                                              past ? 0 : left, 0x00027000);
+        const uint32_t tail = !ACROSS && step == steps - 1 ? end : 0;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void *)to, 16, offset[i] | tail, 0,
+                                                 0, 0);
+#endif
+    }
+
+    // Fragment i of the wave, half h of the step.  Nothing writes the stage
+    // within a read, and __restrict__ says so: without it each transposing read
+    // is made to wait for all loads on their way to LDS, wherever to.
+    // wait_barrier() orders reads and loads.
+    __device__ __forceinline__ bf16x8 read(const uint8_t *__restrict__ part, int h, int i) const
+    {
+        bf16x8 v = {};
+        if constexpr (!ACROSS) {
+            v = *reinterpret_cast<const bf16x8 *>(part + at[h] + 16 * i * kDepthBytes);
+        } else {
+#if defined(__HIP_DEVICE_COMPILE__)
+            typedef __attribute__((address_space(3))) s16x4 *lds;
+            const uint8_t *p = part + at[0] + ((fragment + i) ^ turned) * 32 + h * 32 * kPitch;
+            const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)p);
+            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p + 4 * kPitch));
+            v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+#endif
+        }
+        return v;
+    }
+};
+
+// A tile's operands: weights, or x's columns, and rows, or grad_out's columns.
+template <typename S, bool ACROSS_A, bool ACROSS_B, int HALF = 0>
+struct Operands {
+    Operand<ACROSS_A, S::BN, S::LN, S::W, HALF> a;
+    Operand<ACROSS_B, S::BM, S::LM, S::W> b;
+    int wave, steps, start; // steps of k, and the first of them
+
+    __device__ __forceinline__ void load_part(uint8_t *stage, int i, int step, bool past) const
+    {
+        if (i < S::LN)
+            a.load(stage, wave, i, step, steps, past);
+        else
+            b.load(stage + S::BN * kDepthBytes, wave, i - S::LN, step, steps, past);
+    }
+
+    __device__ __forceinline__ void load_first(uint8_t *lds) const
+    {
+#pragma unroll
+        for (int st = 0; st < S::STAGES; ++st)
+#pragma unroll
+            for (int i = 0; i < S::LN + S::LM; ++i)
+                load_part(lds + st * S::BYTES, i, (start + st) % steps, st >= steps);
+    }
+};
+
+template <typename S>
+struct Fragments {
+    bf16x8 b[2][S::FM], a[2 * S::FN];
+};
+
+constexpr int kAhead = 2; // left fragments are read this many products before they are used
+
+// The products of stage `cur`, groups of FM.  The first kAhead fragments are
+// in registers already; the last groups run behind the barrier and read the
+// first of `next`, so that neither LDS nor the barrier leaves the matrix
+// cores idle for long.  Behind it `cur`, which no wave reads again, takes the
+// loads for STAGES steps on: they have at least a whole step to arrive.
+// wait_barrier() orders them behind the reads before it, and waits for the loads
+// that the reads behind it need.
+template <typename S, typename O>
+__device__ __forceinline__ void tile_step(uint8_t *cur, const uint8_t *next, int step, bool past, const O &o,
+                                          Fragments<S> &f, f32x4 (&acc)[S::FN][S::FM], Fragments<S> &g)
+{
+    constexpr int G = 2 * S::FN, L = S::LN + S::LM, FIRST = S::FN - S::FM - kAhead + 1, B = S::BN * kDepthBytes;
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+        if (i + kAhead < G)
+            f.a[i + kAhead] = o.a.read(cur, (i + kAhead) / S::FN, (i + kAhead) % S::FN);
+#pragma unroll
+        for (int j = 0; j < S::FM; ++j) // the second half's rows, spread before its first product
+            if (i == (FIRST + j > 0 ? FIRST + j : 0))
+                f.b[1][j] = o.b.read(cur + B, 1, j);
+        if (i == G - kAhead)
+            wait_barrier<(S::STAGES - 2) * L>(); // this stage is read, the next one has arrived
+        __builtin_amdgcn_sched_barrier(0);
+        if (i >= G - kAhead) {
+            g.a[i - (G - kAhead)] = o.a.read(next, (i - (G - kAhead)) / S::FN, (i - (G - kAhead)) % S::FN);
+#pragma unroll
+            for (int j = 0; j < S::FM; ++j)
+                if (j % kAhead == i - (G - kAhead))
+                    g.b[0][j] = o.b.read(next + B, 0, j);
+#pragma unroll
+            for (int u = 0; u < L; ++u)
+                if (u * kAhead / L == i - (G - kAhead))
+                    o.load_part(cur, u, step, past);
+        }
+#pragma unroll
+        for (int j = 0; j < S::FM; ++j)
+            acc[i % S::FN][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.a[i], f.b[i / S::FN][j], acc[i % S::FN][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    // the fragments read ahead
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        f.a[i] = g.a[i];
+#pragma unroll
+    for (int j = 0; j < S::FM; ++j)
+        f.b[0][j] = g.b[0][j];
 }
 
-// The tile's sums, row m of the right matrix at [m].
-__device__ __forceinline__ void put(float (*tile)[kEdge + 4], f32x4 (*acc)[2])
+// The sums of a tile whose first stages are on their way.  Behind it all waves
+// are done with LDS, and nothing is on its way there.
+template <typename S, typename O>
+__device__ __forceinline__ void multiply(const O &o, uint8_t *lds, f32x4 (&acc)[S::FN][S::FM])
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, l4 = lane >> 4;
+    Fragments<S> f, g;
+    uint8_t *cur = lds, *next = lds + S::BYTES;
+    wait_barrier<(S::STAGES - 1) * (S::LN + S::LM)>();
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < S::FM; ++j)
+        f.b[0][j] = o.b.read(cur + S::BN * kDepthBytes, 0, j);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            *reinterpret_cast<f32x4 *>(&tile[(wave >> 1) * 32 + j * 16 + l16][(wave & 1) * 32 + i * 16 + 4 * l4]) = acc[i][j];
+    for (int i = 0; i < kAhead; ++i)
+        f.a[i] = o.a.read(cur, i / S::FN, i % S::FN);
+    int at = (o.start + S::STAGES) % o.steps;
+    // the loads behind the last step are not read, nor do they reach memory
+    for (int i = 0; i < o.steps; ++i) {
+        tile_step<S>(cur, next, at, i >= o.steps - S::STAGES, o, f, acc, g);
+        at = at + 1 == o.steps ? 0 : at + 1;
+        cur = next;
+        next = next == lds + (S::STAGES - 1) * S::BYTES ? lds : next + S::BYTES;
+    }
+    wait_barrier<0>();
+}
+
+// Two neighbouring fragments' sums of a row as eight consecutive channels: a
+// lane holds channels 4 (l / 16) .. + 3 of either fragment, and exchanges four
+// with a lane of the next or the last 16.  They begin at channel eighth(lane)
+// of the 32.
+__device__ __forceinline__ void eight(const f32x4 &a, const f32x4 &b, float *f)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(a[e]), __float_as_uint(b[e]), false, false);
+        f[e] = __uint_as_float(s[0]);
+        f[4 + e] = __uint_as_float(s[1]);
+    }
+#endif
+}
+
+__device__ __forceinline__ int eighth(int lane) { return (lane >> 4 & 1) * 16 + (lane >> 5) * 8; }
+
+// The largest of the four lanes of a row, in all of them.
+__device__ __forceinline__ uint32_t row_max(uint32_t x)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    const auto s = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = max(s[0], s[1]);
+    const auto t = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    x = max(t[0], t[1]);
+#endif
+    return x;
 }
 
 __device__ __forceinline__ void store8(uint16_t *to, const float *f)
@@ -86,98 +307,221 @@ __device__ __forceinline__ void store8(uint16_t *to, const float *f)
     *reinterpret_cast<u32x4 *>(to) = RowType<Bf16>::pack(f);
 }
 
-template <int EPI, bool ACROSS>
-__global__ __launch_bounds__(256) void product_kernel(Job a, int ntiles)
+__device__ __forceinline__ void load8(const void *from, int64_t i, float *f)
 {
-    __shared__ __align__(16) uint16_t aw[kEdge][kPitch], bx[kEdge][kPitch];
-    __shared__ __align__(16) float sums[kEdge][kEdge + 4];
-    constexpr int WIDE = EPI == kGated ? kEdge / 2 : kEdge; // channels of the output in a tile
-    const int N = EPI == kGated ? a.n / 2 : a.n;
-    const TileFinder<kEdge, kEdge> find(a, ntiles);
-    for (int slot = (int)(blockIdx.x >> 3);; slot += (int)(gridDim.x >> 3)) {
-        const Tile t = find.tile(a, slot);
-        if (t.expert < 0)
-            return;
-        const int n0 = t.n * WIDE;
-        f32x4 acc[2][2] = {};
-        const uint16_t *w = a.w + (int64_t)t.expert * a.n * a.k;
-        for (int k = 0; k < a.k; k += kDepth) {
-            __syncthreads();
-            stage<ACROSS>(aw, w, ACROSS ? a.n : a.k, k, a.k, [&](int i) -> int64_t {
-                const int n = n0 + i % WIDE;
-                return n < N ? n + i / WIDE * N : -1;
-            });
-            stage<false>(bx, a.x, a.k, k, a.k, [&](int i) { return t.first + i < t.last ? t.first + i : -1; });
-            __syncthreads();
-            multiply(aw, bx, acc);
-        }
-        put(sums, acc);
-        __syncthreads();
-        const int m = threadIdx.x / 4;
-        const int64_t row = t.first + m;
-        for (int c = threadIdx.x % 4 * 8; c < WIDE; c += 32) {
-            const int n = n0 + c;
-            const bool in = row < t.last && n < N;
-            const float *f = &sums[m][c];
-            if (EPI == kStore) {
+    RowType<Bf16>::unpack(*reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(from) + i), f);
+}
+
+// Eight channels `at` of the first product's row as the backward pass reads
+// them; the four lanes of a row hold a block of 32.
+__device__ __forceinline__ void save8(const Job &a, int64_t at, const float *f, bool in)
+{
+    if (a.save == MOE_EP_SAVE_BF16) {
+        if (in)
+            store8(static_cast<uint16_t *>(a.pre) + at, f);
+        return;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        top = max(top, magnitude(f[i]));
+    top = row_max(top);
+    uint8_t scale;
+    const u32x2 codes = mx_codes(f, top, scale);
+    if (!in)
+        return;
+    *reinterpret_cast<u32x2 *>(static_cast<uint8_t *>(a.pre) + at) = codes;
+    if (at % 32 == 0)
+        a.pre_scales[at / 32] = scale;
+}
+
+__device__ __forceinline__ void saved8(const Job &a, int64_t at, float *f)
+{
+    if (a.save == MOE_EP_SAVE_BF16)
+        load8(a.pre, at, f);
+    else
+        mx_values(*reinterpret_cast<const u32x2 *>(static_cast<const uint8_t *>(a.pre) + at), e8m0_value(a.pre_scales[at / 32]),
+                  f);
+}
+
+// ------------------------------------------------------------ rows times weights
+
+// A gated wave's first fragments are gate channels, the others the same
+// channels of up.
+template <int EPI, bool ACROSS, typename S>
+using ProductOperands = Operands<S, ACROSS, false, EPI == kGated ? 8 * S::FN : 0>;
+
+template <int EPI, bool ACROSS, typename S>
+__device__ __forceinline__ ProductOperands<EPI, ACROSS, S> find_operands(const Job &a, const Tile &t)
+{
+    ProductOperands<EPI, ACROSS, S> o;
+    o.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint8_t *w = a.w + (int64_t)t.expert * a.n * a.k * 2;
+    const int wn = o.wave % S::NW, wm = o.wave / S::NW;
+    if constexpr (EPI == kGated) {
+        constexpr int HALF = S::FN * 8;
+        const int I = a.n / 2, n0 = t.n * (S::BN / 2), last = I - n0 - 1;
+        o.a.find(w + (int64_t)n0 * a.k * 2, 2 * a.k, a.k, o.wave, wn * S::FN,
+                 [&](int r) { return min(r / (2 * HALF) * HALF + r % HALF, last); });
+        o.a.second = (int64_t)I * a.k * 2;
+    } else {
+        const int n0 = t.n * S::BN, last = a.n - n0 - 1;
+        if constexpr (ACROSS)
+            o.a.find(w + 2 * n0, 2 * a.n, a.k, o.wave, wn * S::FN, [&](int c) { return min(c, last / 8); });
+        else
+            o.a.find(w + (int64_t)n0 * a.k * 2, 2 * a.k, a.k, o.wave, wn * S::FN, [&](int r) { return min(r, last); });
+    }
+    const int last = (int)(t.last - t.first) - 1;
+    o.b.find(a.x + t.first * a.k * 2, 2 * a.k, a.k, o.wave, wm * S::FM, [&](int r) { return min(r, last); });
+    o.steps = (a.k + kDepth - 1) / kDepth;
+    // k starts elsewhere in each channel tile and goes round: rows a power of
+    // two apart would otherwise have all workgroups read the same few memory
+    // channels at a time
+    o.start = (int)(((uint32_t)t.expert * (uint32_t)channel_tiles(a.n, S::BN) + (uint32_t)t.n) % (uint32_t)o.steps);
+    return o;
+}
+
+template <int EPI, bool ACROSS, typename S, typename AHEAD>
+__device__ __forceinline__ void multiply_tile(const Job &a, const Tile &t, uint8_t *lds, AHEAD ahead)
+{
+    const auto o = find_operands<EPI, ACROSS, S>(a, t);
+    f32x4 acc[S::FN][S::FM] = {};
+    multiply<S>(o, lds, acc);
+    ahead();
+    const int lane = threadIdx.x & 63, wn = o.wave % S::NW, wm = o.wave / S::NW;
+    constexpr int F = EPI == kGated ? S::FN / 2 : S::FN; // fragments of channels of the output
+    const int N = EPI == kGated ? a.n / 2 : a.n, n0 = (t.n * S::NW + wn) * F * 16 + eighth(lane);
+#pragma unroll
+    for (int j = 0; j < S::FM; ++j) {
+        const int64_t m = t.first + (wm * S::FM + j) * 16 + (lane & 15);
+#pragma unroll
+        for (int i = 0; i < F; i += 2) {
+            const int n = n0 + 16 * i;
+            const bool in = m < t.last && n < N;
+            float f[8];
+            eight(acc[i][j], acc[i + 1][j], f);
+            if constexpr (EPI == kStore) {
                 if (in)
-                    store8(a.out + row * N + n, f);
-            } else if (EPI == kGated) {
-                const float *g = f + WIDE;
-                float y[8];
+                    store8(a.out + m * N + n, f);
+            } else if constexpr (EPI == kGated) {
+                float u[8], y[8];
+                eight(acc[F + i][j], acc[F + i + 1][j], u);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    y[i] = f[i] / (1.0f + __expf(-f[i])) * g[i];
+                for (int e = 0; e < 8; ++e)
+                    y[e] = f[e] / (1.0f + __expf(-f[e])) * u[e];
                 if (in)
-                    store8(a.out + row * N + n, y);
-                if (a.save == MOE_EP_SAVE_BF16 && in) {
-                    store8(static_cast<uint16_t *>(a.pre) + row * a.n + n, f);
-                    store8(static_cast<uint16_t *>(a.pre) + row * a.n + N + n, g);
-                } else if (a.save == MOE_EP_SAVE_MXFP8) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float *p = h ? g : f;
-                        uint32_t top = 0;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            top = max(top, magnitude(p[i]));
-                        top = max4(top);
-                        uint8_t scale;
-                        const u32x2 codes = mx_codes(p, top, scale);
-                        const int64_t at = row * a.n + h * N + n;
-                        if (in) {
-                            *reinterpret_cast<u32x2 *>(static_cast<uint8_t *>(a.pre) + at) = codes;
-                            if (threadIdx.x % 4 == 0)
-                                a.pre_scales[at / 32] = scale;
-                        }
-                    }
+                    store8(a.out + m * N + n, y);
+                if (a.save != MOE_EP_SAVE_NONE) {
+                    save8(a, m * 2 * N + n, f, in);
+                    save8(a, m * 2 * N + N + n, u, in);
                 }
             } else if (in) {
                 float g[8], u[8], y[8], dg[8], du[8];
-                const int64_t at = row * 2 * N + n;
-                if (a.save == MOE_EP_SAVE_BF16) {
-                    load_elements<Bf16, 8>(reinterpret_cast<const uint8_t *>(static_cast<uint16_t *>(a.pre) + at), g);
-                    load_elements<Bf16, 8>(reinterpret_cast<const uint8_t *>(static_cast<uint16_t *>(a.pre) + at + N), u);
-                } else {
-                    const uint8_t *p = static_cast<uint8_t *>(a.pre);
-                    mx_values(load8_nt(p + at), e8m0_value(a.pre_scales[at / 32]), g);
-                    mx_values(load8_nt(p + at + N), e8m0_value(a.pre_scales[(at + N) / 32]), u);
-                }
+                const int64_t at = m * 2 * N + n;
+                saved8(a, at, g);
+                saved8(a, at + N, u);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float s = 1.0f / (1.0f + __expf(-g[i]));
-                    y[i] = g[i] * s * u[i];
-                    du[i] = f[i] * g[i] * s;
-                    dg[i] = f[i] * u[i] * s * (1.0f + g[i] * (1.0f - s));
+                for (int e = 0; e < 8; ++e) {
+                    const float s = 1.0f / (1.0f + __expf(-g[e]));
+                    y[e] = g[e] * s * u[e];
+                    du[e] = f[e] * g[e] * s;
+                    dg[e] = f[e] * u[e] * s * (1.0f + g[e] * (1.0f - s));
                 }
                 store8(a.grad_pre + at, dg);
                 store8(a.grad_pre + at + N, du);
                 if (a.out)
-                    store8(a.out + row * N + n, y);
+                    store8(a.out + m * N + n, y);
             }
         }
-        __syncthreads();
     }
+}
+
+// The tile's rows choose among the shapes, smallest first: the last rows of
+// an expert do not pay for rows that are not there.
+template <typename S, typename... MORE, typename F>
+__device__ __forceinline__ void with_shape(const Tile &t, F f)
+{
+    if constexpr (sizeof...(MORE) == 0) {
+        f(S{});
+    } else {
+        if (t.last - t.first <= S::BM)
+            f(S{});
+        else
+            with_shape<MORE...>(t, f);
+    }
+}
+
+constexpr int largest(int x) { return x; }
+
+template <typename... MORE>
+constexpr int largest(int x, MORE... more)
+{
+    return x > largest(more...) ? x : largest(more...);
+}
+
+// A workgroup takes the tiles `slot`, slot + (workgroups of the XCD), ... of
+// its XCD's run, and sends off the next one's first stages before it stores.
+template <int EPI, bool ACROSS, typename S, typename... MORE>
+__global__ __launch_bounds__(S::THREADS, 2) void product_kernel(Job a, int ntiles)
+{
+    __shared__ __align__(256) uint8_t lds[largest(S::STAGES * S::BYTES, (MORE::STAGES * MORE::BYTES)...)];
+    constexpr int BM = largest(S::BM, MORE::BM...);
+    const TileFinder<BM, BM> find(a, ntiles);
+    int slot = (int)(blockIdx.x >> 3);
+    Tile t = find.tile(a, slot);
+    if (t.expert < 0)
+        return;
+    with_shape<S, MORE...>(t, [&](auto shape) { find_operands<EPI, ACROSS, decltype(shape)>(a, t).load_first(lds); });
+    while (t.expert >= 0) {
+        slot += (int)(gridDim.x >> 3);
+        const Tile next = find.tile(a, slot);
+        with_shape<S, MORE...>(t, [&](auto shape) {
+            multiply_tile<EPI, ACROSS, decltype(shape)>(a, t, lds, [&] {
+                if (next.expert >= 0)
+                    with_shape<S, MORE...>(next, [&](auto after) {
+                        find_operands<EPI, ACROSS, decltype(after)>(a, next).load_first(lds);
+                    });
+            });
+        });
+        t = next;
+    }
+}
+
+// As many workgroups as the LDS of 256 CUs holds, at most one a tile, in
+// eight runs of the same length.
+template <int EPI, bool ACROSS, typename S, typename... MORE>
+hipError_t product_launch(const Job &a, hipStream_t s)
+{
+    constexpr int kLds = largest(S::STAGES * S::BYTES, (MORE::STAGES * MORE::BYTES)...);
+    const int64_t ntiles = channel_tiles(a.n, S::BN);
+    const int64_t tiles = most_tiles(a, largest(S::BM, MORE::BM...)) * ntiles;
+    if (tiles > INT32_MAX - 4096) // they are numbered in 32 bits, a run's last number and a step behind it too
+        return hipErrorInvalidConfiguration;
+    const int64_t run = (tiles + 7) / 8, resident = 32 * (160 * 1024 / kLds);
+    hipLaunchKernelGGL((product_kernel<EPI, ACROSS, S, MORE...>), dim3((unsigned)(8 * (run < resident ? run : resident))),
+                       dim3(S::THREADS), 0, s, a, (int)ntiles);
+    return hipGetLastError();
+}
+
+// The shape follows from the average rows of an expert and from how many tiles
+// there are for 256 CUs.
+template <int EPI, bool ACROSS>
+hipError_t product_shape(const Job &a, hipStream_t s)
+{
+    const int64_t average = (a.num_rows + a.num_experts - 1) / a.num_experts;
+    const auto tiles = [&](int64_t size) {
+        return a.num_experts * ((average + size - 1) / size) * ((a.n + size - 1) / size);
+    };
+    if (tiles(128) < 200 || (average <= 8 && a.k >= 2048)) {
+        if constexpr (EPI == kGated) // a wave needs two fragments of either half
+            return product_launch<EPI, ACROSS, TileShape<1, 2, 4, 1, 4>, TileShape<1, 2, 4, 2, 3>>(a, s);
+        else
+            return product_launch<EPI, ACROSS, TileShape<2, 2, 2, 1, 4>, TileShape<2, 2, 2, 2, 3>>(a, s);
+    }
+    if (average >= 112 && tiles(256) >= 200 && a.k >= 512)
+        return product_launch<EPI, ACROSS, TileShape<4, 2, 4, 2, 2>, TileShape<4, 2, 4, 4, 2>, TileShape<2, 4, 8, 3, 2>,
+                              TileShape<2, 4, 8, 4, 2>>(a, s);
+    return product_launch<EPI, ACROSS, TileShape<2, 2, 4, 2, 2>, TileShape<2, 2, 4, 4, 2>>(a, s);
 }
 
 // Rows from the last expert's last on become zeros.
@@ -189,42 +533,110 @@ __global__ __launch_bounds__(256) void zero_rest_kernel(Job a)
         reinterpret_cast<u32x4 *>(a.out)[i] = u32x4{0, 0, 0, 0};
 }
 
-__global__ __launch_bounds__(256) void weight_grad_kernel(moe_ep_weight_grad_args a, int ntiles, int ktiles)
-{
-    __shared__ __align__(16) uint16_t ax[kEdge][kPitch], bg[kEdge][kPitch];
-    __shared__ __align__(16) float sums[kEdge][kEdge + 4];
-    const int e = (int)(blockIdx.x / (unsigned)(ntiles * ktiles)), in = (int)(blockIdx.x % (unsigned)(ntiles * ktiles));
-    const int n0 = in / ktiles * kEdge, k0 = in % ktiles * kEdge;
-    int lo, hi;
-    expert_rows(a, e, lo, hi);
-    f32x4 acc[2][2] = {};
-    for (int m = lo; m < hi; m += kDepth) {
-        __syncthreads();
-        stage<true>(ax, static_cast<const uint16_t *>(a.x), a.k, m, hi,
-                    [&](int i) -> int64_t { return k0 + i < a.k ? k0 + i : -1; });
-        stage<true>(bg, static_cast<const uint16_t *>(a.grad_out), a.n, m, hi,
-                    [&](int i) -> int64_t { return n0 + i < a.n ? n0 + i : -1; });
-        __syncthreads();
-        multiply(ax, bg, acc);
+// ------------------------------------------------------------ the weights' gradient
+
+struct GradTile {
+    int expert, n, k; // expert -1: no such tile
+};
+
+// Each XCD (workgroup number modulo 8) takes an eighth of every expert's
+// tiles, which are numbered by band of kBand n tiles, k tile, n tile: the tiles
+// that run at a time on its 32 CUs read the least through its L2.
+struct GradFinder {
+    int experts, ntiles, ktiles, share;
+
+    __device__ __forceinline__ GradTile tile(int slot) const
+    {
+        GradTile t = {-1, 0, 0};
+        const int e = slot / share, at = (int)(blockIdx.x & 7) * share + slot % share;
+        if (e >= experts || at >= ntiles * ktiles)
+            return t;
+        const int band = at / (kBand * ktiles), height = min(kBand, ntiles - band * kBand), in = at - band * kBand * ktiles;
+        t.expert = e;
+        t.n = band * kBand + in % height;
+        t.k = in / height;
+        return t;
     }
-    put(sums, acc);
-    __syncthreads();
-    const int n = n0 + threadIdx.x / 4;
-    for (int c = threadIdx.x % 4 * 8; c < kEdge; c += 32)
-        if (n < a.n && k0 + c < a.k)
-            store8(static_cast<uint16_t *>(a.grad_w) + ((int64_t)e * a.n + n) * a.k + k0 + c, &sums[threadIdx.x / 4][c]);
+};
+
+template <typename S>
+__device__ __forceinline__ Operands<S, true, true> find_operands(const moe_ep_weight_grad_args &a, const GradTile &t)
+{
+    Operands<S, true, true> o;
+    o.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int lo, hi;
+    expert_rows(a, t.expert, lo, hi);
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+    const int k0 = t.k * S::BN, n0 = t.n * S::BM;
+    o.a.find(static_cast<const uint8_t *>(a.x) + ((int64_t)lo * a.k + k0) * 2, 2 * a.k, hi - lo, o.wave,
+             o.wave % S::NW * S::FN, [&](int c) { return min(c, (a.k - k0) / 8 - 1); });
+    o.b.find(static_cast<const uint8_t *>(a.grad_out) + ((int64_t)lo * a.n + n0) * 2, 2 * a.n, hi - lo, o.wave,
+             o.wave / S::NW * S::FM, [&](int c) { return min(c, (a.n - n0) / 8 - 1); });
+    o.steps = (int)(((int64_t)hi - lo + kDepth - 1) / kDepth);
+    o.start = 0;
+    return o;
 }
 
-template <int EPI, bool ACROSS>
-hipError_t product_launch(const Job &a, int wide, hipStream_t s)
+template <typename S>
+__global__ __launch_bounds__(S::THREADS, 2) void weight_grad_kernel(moe_ep_weight_grad_args a, GradFinder find)
 {
-    const int64_t ntiles = channel_tiles(EPI == kGated ? a.n / 2 : a.n, wide);
-    const int64_t tiles = most_tiles(a, kEdge) * ntiles;
-    if (tiles > INT32_MAX - 4096)
+    __shared__ __align__(256) uint8_t lds[S::STAGES * S::BYTES];
+    // the next tile of the XCD's that there is, from `slot` on
+    const int slots = find.experts * find.share, lane = threadIdx.x & 63;
+    const auto seek = [&](int &slot) {
+        GradTile t = {-1, 0, 0};
+        for (; slot < slots && t.expert < 0; slot += (int)(gridDim.x >> 3))
+            t = find.tile(slot);
+        return t;
+    };
+    int slot = (int)(blockIdx.x >> 3);
+    GradTile t = seek(slot);
+    if (t.expert < 0)
+        return;
+    {
+        const auto o = find_operands<S>(a, t);
+        if (o.steps)
+            o.load_first(lds);
+    }
+    while (t.expert >= 0) {
+        const GradTile next = seek(slot);
+        const auto o = find_operands<S>(a, t);
+        f32x4 acc[S::FN][S::FM] = {};
+        if (o.steps)
+            multiply<S>(o, lds, acc);
+        if (next.expert >= 0) {
+            const auto after = find_operands<S>(a, next);
+            if (after.steps)
+                after.load_first(lds);
+        }
+        const int k0 = (t.k * S::NW + o.wave % S::NW) * S::FN * 16 + eighth(lane);
+#pragma unroll
+        for (int j = 0; j < S::FM; ++j) {
+            const int n = (t.n * S::MW + o.wave / S::NW) * S::FM * 16 + j * 16 + (lane & 15);
+#pragma unroll
+            for (int i = 0; i < S::FN; i += 2) {
+                float f[8];
+                eight(acc[i][j], acc[i + 1][j], f);
+                if (n < a.n && k0 + 16 * i < a.k)
+                    store8(static_cast<uint16_t *>(a.grad_w) + ((int64_t)t.expert * a.n + n) * a.k + k0 + 16 * i, f);
+            }
+        }
+        t = next;
+    }
+}
+
+template <typename S>
+hipError_t weight_grad_launch(const moe_ep_weight_grad_args &a, hipStream_t s)
+{
+    GradFinder find = {a.num_experts, channel_tiles(a.n, S::BM), channel_tiles(a.k, S::BN), 0};
+    const int64_t tiles = (int64_t)find.ntiles * find.ktiles, share = (tiles + 7) / 8;
+    if (share * a.num_experts > INT32_MAX / 8 - 4096)
         return hipErrorInvalidConfiguration;
-    const int64_t run = (tiles + 7) / 8, resident = 32 * 4;
-    hipLaunchKernelGGL((product_kernel<EPI, ACROSS>), dim3((unsigned)(8 * (run < resident ? run : resident))), dim3(256), 0,
-                       s, a, (int)ntiles);
+    find.share = (int)share;
+    const int64_t run = share * a.num_experts, resident = 32 * (160 * 1024 / (S::STAGES * S::BYTES));
+    hipLaunchKernelGGL(weight_grad_kernel<S>, dim3((unsigned)(8 * (run < resident ? run : resident))), dim3(S::THREADS), 0, s,
+                       a, find);
     return hipGetLastError();
 }
 
@@ -233,15 +645,15 @@ hipError_t product_launch(const Job &a, int wide, hipStream_t s)
 hipError_t launch_expert_product(const moe_ep_product_args &a, hipStream_t s)
 {
     Job j = {};
-    j.x = static_cast<const uint16_t *>(a.x);
-    j.w = static_cast<const uint16_t *>(a.w);
+    j.x = static_cast<const uint8_t *>(a.x);
+    j.w = static_cast<const uint8_t *>(a.w);
     j.offsets = a.offsets;
     j.out = static_cast<uint16_t *>(a.out);
     j.num_rows = a.num_rows;
     j.num_experts = a.num_experts;
     j.n = a.n;
     j.k = a.k;
-    const hipError_t e = a.transposed ? product_launch<kStore, true>(j, kEdge, s) : product_launch<kStore, false>(j, kEdge, s);
+    const hipError_t e = a.transposed ? product_shape<kStore, true>(j, s) : product_shape<kStore, false>(j, s);
     if (e != hipSuccess || !a.zero_rest || !a.offsets)
         return e;
     hipLaunchKernelGGL(zero_rest_kernel, dim3(256), dim3(256), 0, s, j);
@@ -251,8 +663,8 @@ hipError_t launch_expert_product(const moe_ep_product_args &a, hipStream_t s)
 hipError_t launch_gated_product(const moe_ep_gated_args &a, hipStream_t s)
 {
     Job j = {};
-    j.x = static_cast<const uint16_t *>(a.x);
-    j.w = static_cast<const uint16_t *>(a.w);
+    j.x = static_cast<const uint8_t *>(a.x);
+    j.w = static_cast<const uint8_t *>(a.w);
     j.offsets = a.offsets;
     j.out = static_cast<uint16_t *>(a.out);
     j.pre = a.pre;
@@ -262,14 +674,14 @@ hipError_t launch_gated_product(const moe_ep_gated_args &a, hipStream_t s)
     j.n = 2 * a.inter_size;
     j.k = a.k;
     j.save = a.save;
-    return product_launch<kGated, false>(j, kEdge / 2, s);
+    return product_shape<kGated, false>(j, s);
 }
 
 hipError_t launch_gated_product_backward(const moe_ep_gated_grad_args &a, hipStream_t s)
 {
     Job j = {};
-    j.x = static_cast<const uint16_t *>(a.grad_out);
-    j.w = static_cast<const uint16_t *>(a.w);
+    j.x = static_cast<const uint8_t *>(a.grad_out);
+    j.w = static_cast<const uint8_t *>(a.w);
     j.offsets = a.offsets;
     j.out = static_cast<uint16_t *>(a.out);
     j.pre = const_cast<void *>(a.pre);
@@ -280,17 +692,19 @@ hipError_t launch_gated_product_backward(const moe_ep_gated_grad_args &a, hipStr
     j.n = a.inter_size;
     j.k = a.n;
     j.save = a.save;
-    return product_launch<kGatedBackward, true>(j, kEdge, s);
+    return product_shape<kGatedBackward, true>(j, s);
 }
 
 hipError_t launch_product_weight_grad(const moe_ep_weight_grad_args &a, hipStream_t s)
 {
-    const int ntiles = channel_tiles(a.n, kEdge), ktiles = channel_tiles(a.k, kEdge);
-    const int64_t grid = (int64_t)a.num_experts * ntiles * ktiles;
-    if (grid > INT32_MAX)
-        return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(weight_grad_kernel, dim3((unsigned)grid), dim3(256), 0, s, a, ntiles, ktiles);
-    return hipGetLastError();
+    const auto tiles = [&](int64_t size) {
+        return a.num_experts * ((a.n + size - 1) / size) * ((a.k + size - 1) / size);
+    };
+    if (tiles(256) >= 200)
+        return weight_grad_launch<TileShape<2, 4, 8, 4, 2>>(a, s);
+    if (tiles(128) >= 200)
+        return weight_grad_launch<TileShape<2, 2, 4, 4, 2>>(a, s);
+    return weight_grad_launch<TileShape<2, 2, 2, 2, 3>>(a, s);
 }
 
 } // namespace moe_ep
