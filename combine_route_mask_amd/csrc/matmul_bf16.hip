@@ -48,7 +48,7 @@ struct TileShape {
     static constexpr int BN = NW * FN * 16, BM = MW * FM * 16, THREADS = 64 * W;
     static constexpr int LN = BN / (8 * W), LM = BM / (8 * W); // loads of a thread and stage, 1024 bytes a wave
     static constexpr int BYTES = (BN + BM) * kDepthBytes;
-    static_assert(BN % (8 * W) == 0 && BM % (8 * W) == 0);
+    static_assert(BN % (8 * W) == 0 && BM % (8 * W) == 0 && (FN & (FN - 1)) == 0);
 };
 
 // Where a tile's operand of EDGE rows lies in memory, for this thread's L loads
@@ -75,17 +75,15 @@ struct Operand {
     int64_t second;
     uint32_t end;     // along: kPastEnd where the lane's chunk of the last step is past the end of k
     int depth;        // across: elements of k
-    uint32_t at[2];   // along: the first fragment's place of either half of a step; across: at[0], its row's
-    int fragment, turned; // across: the wave's first unit, the lane's turn
+    uint32_t at[2];   // along: the first fragment's place of either half of a step; across: at[0]
 
     static __device__ __forceinline__ int turn(int k)
     {
+        static_assert(!ACROSS || EDGE % 64 == 0);
         if constexpr (EDGE % 128 == 0)
             return (k & 3) | ((k >> 3) & 1) << 2;
-        else if constexpr (EDGE % 64 == 0)
+        else // two rows of k are 256 bytes
             return ((k >> 1) & 1) | ((k >> 3) & 1) << 1;
-        else
-            return (k >> 3) & 1;
     }
 
     // `first`: of the operand's row 0 at k = 0.  `rows` of them there are, and
@@ -93,15 +91,13 @@ struct Operand {
     // read another one's, and their results are not stored.  `fragment`: the
     // wave's first one.
     template <typename MAP>
-    __device__ __forceinline__ void find(const uint8_t *first, uint32_t stride_, int k, int wave, int fragment_, MAP map)
+    __device__ __forceinline__ void find(const uint8_t *first, uint32_t stride_, int k, int wave, int fragment, MAP map)
     {
         const int lane = threadIdx.x & 63, l16 = lane & 15, l4 = lane >> 4;
         base = first;
         stride = stride_;
         depth = k;
         end = 0;
-        fragment = fragment_;
-        turned = 0;
         if constexpr (!ACROSS) {
             const int sub = lane / 8;
             const uint32_t chunk = (uint32_t)((lane % 8) ^ sub) * 16;
@@ -121,9 +117,8 @@ struct Operand {
                 offset[i] = (uint32_t)row * stride + 16 * (uint32_t)map(chunk);
             }
             const int row = 8 * l4 + l16 / 4;
-            at[0] = (uint32_t)(row * kPitch + l16 % 4 * 8);
+            at[0] = (uint32_t)(row * kPitch + l16 % 4 * 8 + (fragment ^ turn(row)) * 32);
             at[1] = 0;
-            turned = turn(row);
         }
     }
 
@@ -145,11 +140,22 @@ struct Operand {
 #endif
     }
 
+    // Across: at[0] as something new in each step, so that the fragments'
+    // places, which differ in the bits of their unit, are made anew and take no
+    // registers.
+    __device__ __forceinline__ uint32_t place() const
+    {
+        uint32_t x = at[0];
+        if constexpr (ACROSS)
+            asm volatile("" : "+v"(x));
+        return x;
+    }
+
     // Fragment i of the wave, half h of the step.  Nothing writes the stage
     // within a read, and __restrict__ says so: without it each transposing read
     // is made to wait for all loads on their way to LDS, wherever to.
     // wait_barrier() orders reads and loads.
-    __device__ __forceinline__ bf16x8 read(const uint8_t *__restrict__ part, int h, int i) const
+    __device__ __forceinline__ bf16x8 read(const uint8_t *__restrict__ part, uint32_t place, int h, int i) const
     {
         bf16x8 v = {};
         if constexpr (!ACROSS) {
@@ -157,7 +163,7 @@ struct Operand {
         } else {
 #if defined(__HIP_DEVICE_COMPILE__)
             typedef __attribute__((address_space(3))) s16x4 *lds;
-            const uint8_t *p = part + at[0] + ((fragment + i) ^ turned) * 32 + h * 32 * kPitch;
+            const uint8_t *p = part + (place ^ 32 * i) + h * 32 * kPitch;
             const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)p);
             const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds)(p + 4 * kPitch));
             v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -211,23 +217,24 @@ __device__ __forceinline__ void tile_step(uint8_t *cur, const uint8_t *next, int
                                           Fragments<S> &f, f32x4 (&acc)[S::FN][S::FM], Fragments<S> &g)
 {
     constexpr int G = 2 * S::FN, L = S::LN + S::LM, FIRST = S::FN - S::FM - kAhead + 1, B = S::BN * kDepthBytes;
+    const uint32_t pa = o.a.place(), pb = o.b.place();
 #pragma unroll
     for (int i = 0; i < G; ++i) {
         if (i + kAhead < G)
-            f.a[i + kAhead] = o.a.read(cur, (i + kAhead) / S::FN, (i + kAhead) % S::FN);
+            f.a[i + kAhead] = o.a.read(cur, pa, (i + kAhead) / S::FN, (i + kAhead) % S::FN);
 #pragma unroll
         for (int j = 0; j < S::FM; ++j) // the second half's rows, spread before its first product
             if (i == (FIRST + j > 0 ? FIRST + j : 0))
-                f.b[1][j] = o.b.read(cur + B, 1, j);
+                f.b[1][j] = o.b.read(cur + B, pb, 1, j);
         if (i == G - kAhead)
             wait_barrier<(S::STAGES - 2) * L>(); // this stage is read, the next one has arrived
         __builtin_amdgcn_sched_barrier(0);
         if (i >= G - kAhead) {
-            g.a[i - (G - kAhead)] = o.a.read(next, (i - (G - kAhead)) / S::FN, (i - (G - kAhead)) % S::FN);
+            g.a[i - (G - kAhead)] = o.a.read(next, pa, (i - (G - kAhead)) / S::FN, (i - (G - kAhead)) % S::FN);
 #pragma unroll
             for (int j = 0; j < S::FM; ++j)
                 if (j % kAhead == i - (G - kAhead))
-                    g.b[0][j] = o.b.read(next + B, 0, j);
+                    g.b[0][j] = o.b.read(next + B, pb, 0, j);
 #pragma unroll
             for (int u = 0; u < L; ++u)
                 if (u * kAhead / L == i - (G - kAhead))
@@ -257,10 +264,10 @@ __device__ __forceinline__ void multiply(const O &o, uint8_t *lds, f32x4 (&acc)[
     wait_barrier<(S::STAGES - 1) * (S::LN + S::LM)>();
 #pragma unroll
     for (int j = 0; j < S::FM; ++j)
-        f.b[0][j] = o.b.read(cur + S::BN * kDepthBytes, 0, j);
+        f.b[0][j] = o.b.read(cur + S::BN * kDepthBytes, o.b.at[0], 0, j);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-        f.a[i] = o.a.read(cur, i / S::FN, i % S::FN);
+        f.a[i] = o.a.read(cur, o.a.at[0], i / S::FN, i % S::FN);
     int at = (o.start + S::STAGES) % o.steps;
     // the loads behind the last step are not read, nor do they reach memory
     for (int i = 0; i < o.steps; ++i) {
@@ -459,14 +466,32 @@ constexpr int largest(int x, MORE... more)
     return x > largest(more...) ? x : largest(more...);
 }
 
+// The heights that the finder may take: with more than two shapes each of them
+// but the smallest, else the tallest.
+template <typename S, typename... MORE>
+struct Heights {
+    using Finder = TileFinder<largest(S::BM, MORE::BM...)>;
+    static constexpr int kLeast = largest(S::BM, MORE::BM...);
+};
+
+template <typename S, typename A, typename B, typename... MORE>
+struct Heights<S, A, B, MORE...> {
+    using Finder = TileFinder<A::BM, B::BM, MORE::BM...>;
+    static constexpr int kLeast = A::BM;
+};
+
+template <typename... S>
+using Finder = typename Heights<S...>::Finder;
+
+constexpr float kEdgeRows = 24.0f; // a tile's beginning and end take as long as this many of its rows
+
 // A workgroup takes the tiles `slot`, slot + (workgroups of the XCD), ... of
 // its XCD's run, and sends off the next one's first stages before it stores.
 template <int EPI, bool ACROSS, typename S, typename... MORE>
 __global__ __launch_bounds__(S::THREADS, 2) void product_kernel(Job a, int ntiles)
 {
     __shared__ __align__(256) uint8_t lds[largest(S::STAGES * S::BYTES, (MORE::STAGES * MORE::BYTES)...)];
-    constexpr int BM = largest(S::BM, MORE::BM...);
-    const TileFinder<BM, BM> find(a, ntiles);
+    const Finder<S, MORE...> find(a, ntiles, kEdgeRows);
     int slot = (int)(blockIdx.x >> 3);
     Tile t = find.tile(a, slot);
     if (t.expert < 0)
@@ -494,7 +519,7 @@ hipError_t product_launch(const Job &a, hipStream_t s)
 {
     constexpr int kLds = largest(S::STAGES * S::BYTES, (MORE::STAGES * MORE::BYTES)...);
     const int64_t ntiles = channel_tiles(a.n, S::BN);
-    const int64_t tiles = most_tiles(a, largest(S::BM, MORE::BM...)) * ntiles;
+    const int64_t tiles = most_tiles(a, Heights<S, MORE...>::kLeast) * ntiles;
     if (tiles > INT32_MAX - 4096) // they are numbered in 32 bits, a run's last number and a step behind it too
         return hipErrorInvalidConfiguration;
     const int64_t run = (tiles + 7) / 8, resident = 32 * (160 * 1024 / kLds);
@@ -520,7 +545,7 @@ hipError_t product_shape(const Job &a, hipStream_t s)
     }
     if (average >= 112 && tiles(256) >= 200 && a.k >= 512)
         return product_launch<EPI, ACROSS, TileShape<4, 2, 4, 2, 2>, TileShape<4, 2, 4, 4, 2>, TileShape<2, 4, 8, 3, 2>,
-                              TileShape<2, 4, 8, 4, 2>>(a, s);
+                              TileShape<2, 4, 8, 4, 2>, TileShape<2, 4, 8, 5, 2>>(a, s);
     return product_launch<EPI, ACROSS, TileShape<2, 2, 4, 2, 2>, TileShape<2, 2, 4, 4, 2>>(a, s);
 }
 

@@ -7,6 +7,8 @@
 // channels of one token.  v_mfma_i32_16x16x64_i8: lane l holds 16 bytes of
 // row l % 16 at k = 16 * (l / 16) of either matrix; of the result, element i
 // is channel 4 * (l / 16) + i of token l % 16.
+#include <type_traits>
+
 #include "experts_internal.h"
 #include "rows.h"
 #include "tiles.h"
@@ -327,7 +329,7 @@ __global__ __launch_bounds__(S::THREADS, 2) void matmul_tile_kernel(moe_ep_matmu
     // this tile's and the next one's
     __shared__ __align__(16) uint8_t scales[2][tile_scales<S, MORE...>()];
     constexpr int TALL = largest(S::BM, MORE::BM...), BM = TALL > 256 ? 256 : TALL;
-    const TileFinder<BM, TALL> find(a, ntiles);
+    const std::conditional_t<BM == TALL, TileFinder<BM>, TileFinder<BM, TALL>> find(a, ntiles, 76.0f);
     int slot = (int)(blockIdx.x >> 3);
     Tile t = find.tile(a, slot);
     if (t.expert < 0)

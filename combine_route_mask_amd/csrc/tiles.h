@@ -62,38 +62,47 @@ constexpr int kUnit = 64; // tiles begin this many rows apart, or a multiple
 // a run of them: the tiles that run at a time on its 32 CUs are 4 x 8, which
 // read the least through its L2 (8192 x 8192 x 8192: 429 us; bands of 6 423, of
 // 8 441, columns of all row tiles 462).  An expert's row tiles are of even
-// height.  Of BM and TALL the finder takes what the CUs are done with first:
-// a tile takes about as long as 76 rows and its own.
-template <int BM, int TALL>
+// height.  Of the tallest tiles BM and OTHERS the finder takes what the CUs are
+// done with first: a tile takes about as long as `edge` rows and its own.
+template <int BM, int... OTHERS>
 struct TileFinder {
+    static constexpr int kHeights[] = {BM, OTHERS...};
     int lane, ntiles, share, per, total, first, bm;
     int lo, hi, n, start; // of the lane's experts
 
     // lane l sums the experts l * share ..; a tile's lane is then looked
     // into, one expert a lane
     template <typename A>
-    __device__ __forceinline__ TileFinder(const A &a, int ntiles_) : ntiles(ntiles_)
+    __device__ __forceinline__ TileFinder(const A &a, int ntiles_, float edge) : ntiles(ntiles_)
     {
         lane = threadIdx.x & 63;
         share = (a.num_experts + 63) / 64;
-        n = 0;
-        int tall = 0;
+        constexpr int H = 1 + sizeof...(OTHERS);
+        int count[H] = {};
         float rows = 0.0f;
         for (int i = 0; i < share; ++i) {
             expert_rows(a, lane * share + i, lo, hi);
-            n += row_tiles(lo, hi, BM);
-            tall += row_tiles(lo, hi, TALL);
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+                count[h] += row_tiles(lo, hi, kHeights[h]);
             rows += (float)(hi - lo);
         }
+        n = count[0];
         int sum = prefix_sum(n, lane);
         bm = BM;
-        if (TALL != BM) {
-            const int sum_tall = prefix_sum(tall, lane);
+        if (H > 1) {
             rows = wave_sum(rows);
-            if (time_of(__builtin_amdgcn_readlane(sum_tall, 63), rows) < time_of(__builtin_amdgcn_readlane(sum, 63), rows)) {
-                bm = TALL;
-                n = tall;
-                sum = sum_tall;
+            float best = time_of(__builtin_amdgcn_readlane(sum, 63), rows, edge);
+#pragma unroll
+            for (int h = 1; h < H; ++h) {
+                const int other = prefix_sum(count[h], lane);
+                const float time = time_of(__builtin_amdgcn_readlane(other, 63), rows, edge);
+                if (time < best) {
+                    best = time;
+                    bm = kHeights[h];
+                    n = count[h];
+                    sum = other;
+                }
             }
         }
         total = __builtin_amdgcn_readlane(sum, 63) * ntiles;
@@ -103,9 +112,9 @@ struct TileFinder {
     }
 
     // Rounds of 256 CUs times a tile.
-    __device__ __forceinline__ float time_of(int tiles, float rows) const
+    __device__ __forceinline__ float time_of(int tiles, float rows, float edge) const
     {
-        return tiles ? (float)((tiles * ntiles + 255) / 256) * (76.0f + rows / (float)tiles) : 0.0f;
+        return tiles ? (float)((tiles * ntiles + 255) / 256) * (edge + rows / (float)tiles) : 0.0f;
     }
 
     template <typename A>
