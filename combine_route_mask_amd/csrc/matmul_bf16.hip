@@ -12,6 +12,9 @@
 // along k (an operand's row after another, k next to k) or across it (a k
 // after another).  An operand across k goes into LDS as it lies and is turned
 // by the transposing LDS read.
+#include <algorithm>
+#include <cmath>
+
 #include "ffn_internal.h"
 #include "rows.h"
 #include "tiles.h"
@@ -297,6 +300,57 @@ __device__ __forceinline__ void eight(const f32x4 &a, const f32x4 &b, float *f)
 
 __device__ __forceinline__ int eighth(int lane) { return (lane >> 4 & 1) * 16 + (lane >> 5) * 8; }
 
+// Two such pairs of fragments, 32 channels apart, as whole lines of memory: p
+// becomes the first eight rows' 64 channels, the lanes l % 16 >= 8 holding the
+// second pair's, and q the last eight rows'.
+__device__ __forceinline__ void whole_lines(float *p, float *q)
+{
+    constexpr int kRotate8 = 0x128; // within 16 lanes
+    const bool low = (threadIdx.x & 8) == 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float other = dpp<kRotate8>(low ? q[e] : p[e]);
+        p[e] = low ? p[e] : other;
+        q[e] = low ? other : q[e];
+    }
+}
+
+// Row and channel (of the wave's) of a lane's eight number i of j.
+template <bool LINES>
+__device__ __forceinline__ void eight_place(int i, int j, int &row, int &channel)
+{
+    const int lane = threadIdx.x & 63;
+    row = 16 * j + (LINES ? i % 2 * 8 + (lane & 7) : lane & 15);
+    channel = (LINES ? i / 2 * 64 + (lane & 8) * 4 : 32 * i) + eighth(lane);
+}
+
+// The sums of fragments [from, from + F) of j as calls f(row, channel, eight
+// values).  LINES: F is a multiple of 4, and a store of all lanes' values fills
+// whole lines.
+template <int F, bool LINES, typename ACC, typename FN>
+__device__ __forceinline__ void each_eight(ACC &acc, int from, int j, FN f)
+{
+    const int lane = threadIdx.x & 63;
+    float p[8], q[8];
+    if constexpr (!LINES) {
+#pragma unroll
+        for (int i = 0; i < F; i += 2) {
+            eight(acc[from + i][j], acc[from + i + 1][j], p);
+            f(16 * j + (lane & 15), 16 * i + eighth(lane), p);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < F; i += 4) {
+            eight(acc[from + i][j], acc[from + i + 1][j], p);
+            eight(acc[from + i + 2][j], acc[from + i + 3][j], q);
+            whole_lines(p, q);
+            const int channel = 16 * i + (lane & 8) * 4 + eighth(lane);
+            f(16 * j + (lane & 7), channel, p);
+            f(16 * j + 8 + (lane & 7), channel, q);
+        }
+    }
+}
+
 // The largest of the four lanes of a row, in all of them.
 __device__ __forceinline__ uint32_t row_max(uint32_t x)
 {
@@ -314,9 +368,14 @@ __device__ __forceinline__ void store8(uint16_t *to, const float *f)
     *reinterpret_cast<u32x4 *>(to) = RowType<Bf16>::pack(f);
 }
 
-__device__ __forceinline__ void load8(const void *from, int64_t i, float *f)
+// Past the caches: the results of all workgroups of a round come at a time, and
+// whole lines leave L2 to the operands (gradient of 32 experts' weights of
+// 2048 x 4096: 366 -> 308 us; the gated backward of 8191 rows 174 -> 164 us; the
+// gated product, whose results the next product reads, is slower so, 249 -> 255
+// us).
+__device__ __forceinline__ void store8_nt(uint16_t *to, const float *f)
 {
-    RowType<Bf16>::unpack(*reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(from) + i), f);
+    store16_nt(to, RowType<Bf16>::pack(f));
 }
 
 // Eight channels `at` of the first product's row as the backward pass reads
@@ -342,14 +401,33 @@ __device__ __forceinline__ void save8(const Job &a, int64_t at, const float *f, 
         a.pre_scales[at / 32] = scale;
 }
 
-__device__ __forceinline__ void saved8(const Job &a, int64_t at, float *f)
-{
-    if (a.save == MOE_EP_SAVE_BF16)
-        load8(a.pre, at, f);
-    else
-        mx_values(*reinterpret_cast<const u32x2 *>(static_cast<const uint8_t *>(a.pre) + at), e8m0_value(a.pre_scales[at / 32]),
-                  f);
-}
+// Eight gate and eight up values of the first product as they were saved: bf16,
+// or codes and in the third word their scale.
+struct Saved {
+    u32x4 gate, up;
+    __device__ __forceinline__ void load(const Job &a, int64_t at, int I)
+    {
+        if (a.save == MOE_EP_SAVE_BF16) {
+            gate = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.pre) + at);
+            up = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.pre) + at + I);
+        } else {
+            const uint8_t *p = static_cast<const uint8_t *>(a.pre) + at;
+            const u32x2 g = *reinterpret_cast<const u32x2 *>(p), u = *reinterpret_cast<const u32x2 *>(p + I);
+            gate = u32x4{g[0], g[1], a.pre_scales[at / 32], 0};
+            up = u32x4{u[0], u[1], a.pre_scales[(at + I) / 32], 0};
+        }
+    }
+    __device__ __forceinline__ void values(const Job &a, float *g, float *u) const
+    {
+        if (a.save == MOE_EP_SAVE_BF16) {
+            RowType<Bf16>::unpack(gate, g);
+            RowType<Bf16>::unpack(up, u);
+        } else {
+            mx_values(u32x2{gate[0], gate[1]}, e8m0_value(gate[2]), g);
+            mx_values(u32x2{up[0], up[1]}, e8m0_value(up[2]), u);
+        }
+    }
+};
 
 // ------------------------------------------------------------ rows times weights
 
@@ -395,38 +473,68 @@ __device__ __forceinline__ void multiply_tile(const Job &a, const Tile &t, uint8
     f32x4 acc[S::FN][S::FM] = {};
     multiply<S>(o, lds, acc);
     ahead();
-    const int lane = threadIdx.x & 63, wn = o.wave % S::NW, wm = o.wave / S::NW;
     constexpr int F = EPI == kGated ? S::FN / 2 : S::FN; // fragments of channels of the output
-    const int N = EPI == kGated ? a.n / 2 : a.n, n0 = (t.n * S::NW + wn) * F * 16 + eighth(lane);
+    const int N = EPI == kGated ? a.n / 2 : a.n, n0 = (t.n * S::NW + o.wave % S::NW) * F * 16;
+    const int64_t m0 = t.first + o.wave / S::NW * S::FM * 16;
+    [[maybe_unused]] Saved saved[F / 2];
+    [[maybe_unused]] const auto load_saved = [&](int i, int j) {
+        int row, channel;
+        eight_place<F % 4 == 0>(i, j, row, channel);
+        // of rows and channels past the last, the last ones'
+        saved[i].load(a, min(m0 + row, t.last - 1) * 2 * N + min(n0 + channel, N - 8), N);
+    };
+    if constexpr (EPI == kGatedBackward) {
+#pragma unroll
+        for (int i = 0; i < F / 2; ++i)
+            load_saved(i, 0);
+    }
 #pragma unroll
     for (int j = 0; j < S::FM; ++j) {
-        const int64_t m = t.first + (wm * S::FM + j) * 16 + (lane & 15);
-#pragma unroll
-        for (int i = 0; i < F; i += 2) {
-            const int n = n0 + 16 * i;
-            const bool in = m < t.last && n < N;
-            float f[8];
-            eight(acc[i][j], acc[i + 1][j], f);
-            if constexpr (EPI == kStore) {
-                if (in)
-                    store8(a.out + m * N + n, f);
-            } else if constexpr (EPI == kGated) {
-                float u[8], y[8];
-                eight(acc[F + i][j], acc[F + i + 1][j], u);
+        if constexpr (EPI == kGated) {
+            // gate and up come one after the other
+            float gate[F][8];
+            int at = 0;
+            each_eight<F, false>(acc, 0, j, [&](int, int, const float *f) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    y[e] = f[e] / (1.0f + __expf(-f[e])) * u[e];
+                    gate[at][e] = f[e];
+                ++at;
+            });
+            at = 0;
+            each_eight<F, false>(acc, F, j, [&](int row, int channel, const float *u) {
+                const int64_t m = m0 + row;
+                const int n = n0 + channel;
+                const float *g = gate[at++];
+                const bool in = m < t.last && n < N;
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    y[e] = g[e] / (1.0f + __expf(-g[e])) * u[e];
                 if (in)
                     store8(a.out + m * N + n, y);
                 if (a.save != MOE_EP_SAVE_NONE) {
-                    save8(a, m * 2 * N + n, f, in);
+                    save8(a, m * 2 * N + n, g, in);
                     save8(a, m * 2 * N + N + n, u, in);
                 }
-            } else if (in) {
+            });
+        } else if constexpr (EPI == kStore) {
+            each_eight<F, F % 4 == 0>(acc, 0, j, [&](int row, int channel, const float *f) {
+                const int64_t m = m0 + row;
+                const int n = n0 + channel;
+                if (m < t.last && n < N)
+                    store8_nt(a.out + m * N + n, f);
+            });
+        } else {
+            int at = 0;
+            each_eight<F, F % 4 == 0>(acc, 0, j, [&](int row, int channel, const float *f) {
+                const int64_t m = m0 + row;
+                const int n = n0 + channel, i = at++;
                 float g[8], u[8], y[8], dg[8], du[8];
-                const int64_t at = m * 2 * N + n;
-                saved8(a, at, g);
-                saved8(a, at + N, u);
+                saved[i].values(a, g, u);
+                if (j + 1 < S::FM) // on its way while the others are stored
+                    load_saved(i, j + 1);
+                if (m >= t.last || n >= N)
+                    return;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float s = 1.0f / (1.0f + __expf(-g[e]));
@@ -434,11 +542,11 @@ __device__ __forceinline__ void multiply_tile(const Job &a, const Tile &t, uint8
                     du[e] = f[e] * g[e] * s;
                     dg[e] = f[e] * u[e] * s * (1.0f + g[e] * (1.0f - s));
                 }
-                store8(a.grad_pre + at, dg);
-                store8(a.grad_pre + at + N, du);
+                store8_nt(a.grad_pre + m * 2 * N + n, dg);
+                store8_nt(a.grad_pre + m * 2 * N + N + n, du);
                 if (a.out)
-                    store8(a.out + m * N + n, y);
-            }
+                    store8_nt(a.out + m * N + n, y);
+            });
         }
     }
 }
@@ -528,25 +636,77 @@ hipError_t product_launch(const Job &a, hipStream_t s)
     return hipGetLastError();
 }
 
-// The shape follows from the average rows of an expert and from how many tiles
-// there are for 256 CUs.
+// Which shape: the one that a model of the time of the busiest CU finds fastest,
+// from the number of tiles on 256 CUs and of 64-deep steps.  A step takes a
+// shape's workgroup `first` us alone on its CU (waits of LDS and barriers),
+// `more` us of a CU's time with others, `all` us of one of 256 where all
+// CUs are busy (the clock falls); a tile's beginning and end take `edge` us.
+// Fitted to, and checked against, each shape's time (us, best of the four and
+// the model's choice; rows x hidden x inter):
+//  - products: 1023 x 2064 x 1032 gated 26.2 (64 x 64) / 26.9 (128 x 64), down
+//    12.3 / 12.3 (128 x 128), through w1 23.6 / 23.6 (128 x 64); 64 x 4096 x 2048
+//    down 9.3 / 9.3 (64 x 64), others 12.7, 12.8, 19; 4000 x 4096 x 1024 through w1
+//    57 / 57 (256 x 256), others 117, 92, 69; 2000 rows over 16 experts x 2048 x 768
+//    gated 24.5 / 24.5 (128 x 64), others 30, 31, 33;
+//  - weights' gradient: 4000 rows of 2048 x 4096 66 / 66 (128 x 128), 256 x 256 85;
+//    8191 rows over 8 experts of 4096 x 4096 254 / 254 (256 x 256), 128 x 128 303;
+//    2000 rows over 16 of 2048 x 768 18 / 18 (128 x 128), 256 x 256 23, 64 x 64 30.
+// One to three more stages for the smaller shapes change nothing where a CU has
+// one workgroup and cost where it could have several.
+enum Shape { kTile64, kTile128x64, kTile128, kTile256 };
+
+struct ShapeTime {
+    int channels, rows;
+    float first, more, all, edge;
+};
+
+constexpr ShapeTime kShapeTimes[] = {{64, 64, 0.3f, 0.25f, 0.0f, 1.0f},
+                                     {128, 64, 0.42f, 0.365f, 0.0f, 1.5f},
+                                     {128, 128, 0.75f, 0.52f, 0.0f, 2.5f},
+                                     {256, 256, 1.0f, 1.0f, 1.65f, 9.0f}};
+
+// `tiles(shape)` are its tiles, `steps` those of one.
+template <typename F>
+Shape fastest_shape(float steps, F tiles)
+{
+    Shape best = kTile64;
+    float least = 0.0f;
+    for (const Shape s : {kTile64, kTile128x64, kTile128, kTile256}) {
+        const ShapeTime &t = kShapeTimes[s];
+        const float n = tiles(t), turns = std::ceil(n / 256.0f);
+        const float step = std::max(turns > 1.0f ? turns * t.more : t.first, t.all * n / 256.0f);
+        const float time = steps * step + turns * t.edge;
+        if (s == kTile64 || time < least) {
+            best = s;
+            least = time;
+        }
+    }
+    return best;
+}
+
 template <int EPI, bool ACROSS>
 hipError_t product_shape(const Job &a, hipStream_t s)
 {
-    const int64_t average = (a.num_rows + a.num_experts - 1) / a.num_experts;
-    const auto tiles = [&](int64_t size) {
-        return a.num_experts * ((average + size - 1) / size) * ((a.n + size - 1) / size);
-    };
-    if (tiles(128) < 200 || (average <= 8 && a.k >= 2048)) {
+    const float rows = (float)a.num_rows / (float)a.num_experts;
+    // ragged experts have some tiles more than experts of the average
+    const float more = a.num_experts > 1 ? 1.1f : 1.0f;
+    const Shape shape = fastest_shape((float)((a.k + 63) / 64), [&](const ShapeTime &t) {
+        return more * (float)a.num_experts * std::ceil(rows / (float)t.rows) * (float)channel_tiles(a.n, t.channels);
+    });
+    switch (shape) {
+    case kTile64:
         if constexpr (EPI == kGated) // a wave needs two fragments of either half
             return product_launch<EPI, ACROSS, TileShape<1, 2, 4, 1, 4>, TileShape<1, 2, 4, 2, 3>>(a, s);
         else
             return product_launch<EPI, ACROSS, TileShape<2, 2, 2, 1, 4>, TileShape<2, 2, 2, 2, 3>>(a, s);
-    }
-    if (average >= 112 && tiles(256) >= 200 && a.k >= 512)
+    case kTile128x64:
+        return product_launch<EPI, ACROSS, TileShape<2, 2, 4, 1, 4>, TileShape<2, 2, 4, 2, 3>>(a, s);
+    case kTile128:
+        return product_launch<EPI, ACROSS, TileShape<2, 2, 4, 2, 2>, TileShape<2, 2, 4, 4, 2>>(a, s);
+    default:
         return product_launch<EPI, ACROSS, TileShape<4, 2, 4, 2, 2>, TileShape<4, 2, 4, 4, 2>, TileShape<2, 4, 8, 3, 2>,
                               TileShape<2, 4, 8, 4, 2>, TileShape<2, 4, 8, 5, 2>>(a, s);
-    return product_launch<EPI, ACROSS, TileShape<2, 2, 4, 2, 2>, TileShape<2, 2, 4, 4, 2>>(a, s);
+    }
 }
 
 // Rows from the last expert's last on become zeros.
@@ -608,7 +768,7 @@ __global__ __launch_bounds__(S::THREADS, 2) void weight_grad_kernel(moe_ep_weigh
 {
     __shared__ __align__(256) uint8_t lds[S::STAGES * S::BYTES];
     // the next tile of the XCD's that there is, from `slot` on
-    const int slots = find.experts * find.share, lane = threadIdx.x & 63;
+    const int slots = find.experts * find.share;
     const auto seek = [&](int &slot) {
         GradTile t = {-1, 0, 0};
         for (; slot < slots && t.expert < 0; slot += (int)(gridDim.x >> 3))
@@ -619,34 +779,28 @@ __global__ __launch_bounds__(S::THREADS, 2) void weight_grad_kernel(moe_ep_weigh
     GradTile t = seek(slot);
     if (t.expert < 0)
         return;
-    {
-        const auto o = find_operands<S>(a, t);
-        if (o.steps)
-            o.load_first(lds);
-    }
+    auto o = find_operands<S>(a, t);
+    if (o.steps)
+        o.load_first(lds);
     while (t.expert >= 0) {
-        const GradTile next = seek(slot);
-        const auto o = find_operands<S>(a, t);
         f32x4 acc[S::FN][S::FM] = {};
         if (o.steps)
             multiply<S>(o, lds, acc);
+        const GradTile next = seek(slot);
         if (next.expert >= 0) {
-            const auto after = find_operands<S>(a, next);
-            if (after.steps)
-                after.load_first(lds);
+            o = find_operands<S>(a, next);
+            if (o.steps)
+                o.load_first(lds);
         }
-        const int k0 = (t.k * S::NW + o.wave % S::NW) * S::FN * 16 + eighth(lane);
+        const int k0 = (t.k * S::NW + o.wave % S::NW) * S::FN * 16, n0 = (t.n * S::MW + o.wave / S::NW) * S::FM * 16;
+        uint16_t *out = static_cast<uint16_t *>(a.grad_w) + (int64_t)t.expert * a.n * a.k;
 #pragma unroll
-        for (int j = 0; j < S::FM; ++j) {
-            const int n = (t.n * S::MW + o.wave / S::NW) * S::FM * 16 + j * 16 + (lane & 15);
-#pragma unroll
-            for (int i = 0; i < S::FN; i += 2) {
-                float f[8];
-                eight(acc[i][j], acc[i + 1][j], f);
-                if (n < a.n && k0 + 16 * i < a.k)
-                    store8(static_cast<uint16_t *>(a.grad_w) + ((int64_t)t.expert * a.n + n) * a.k + k0 + 16 * i, f);
-            }
-        }
+        for (int j = 0; j < S::FM; ++j)
+            each_eight<S::FN, S::FN % 4 == 0>(acc, 0, j, [&](int row, int channel, const float *f) {
+                const int n = n0 + row, k = k0 + channel;
+                if (n < a.n && k < a.k)
+                    store8_nt(out + (int64_t)n * a.k + k, f);
+            });
         t = next;
     }
 }
@@ -722,14 +876,16 @@ hipError_t launch_gated_product_backward(const moe_ep_gated_grad_args &a, hipStr
 
 hipError_t launch_product_weight_grad(const moe_ep_weight_grad_args &a, hipStream_t s)
 {
-    const auto tiles = [&](int64_t size) {
-        return a.num_experts * ((a.n + size - 1) / size) * ((a.k + size - 1) / size);
-    };
-    if (tiles(256) >= 200)
-        return weight_grad_launch<TileShape<2, 4, 8, 4, 2>>(a, s);
-    if (tiles(128) >= 200)
-        return weight_grad_launch<TileShape<2, 2, 4, 4, 2>>(a, s);
-    return weight_grad_launch<TileShape<2, 2, 2, 2, 3>>(a, s);
+    const float rows = (float)a.num_rows / (float)a.num_experts;
+    const Shape shape = fastest_shape(std::ceil(rows / 64.0f), [&](const ShapeTime &t) {
+        return (float)a.num_experts * (float)channel_tiles(a.n, t.rows) * (float)channel_tiles(a.k, t.channels);
+    });
+    switch (shape) {
+    case kTile64: return weight_grad_launch<TileShape<2, 2, 2, 2, 3>>(a, s);
+    case kTile128x64: return weight_grad_launch<TileShape<2, 2, 4, 2, 3>>(a, s);
+    case kTile128: return weight_grad_launch<TileShape<2, 2, 4, 4, 2>>(a, s);
+    default: return weight_grad_launch<TileShape<2, 4, 8, 4, 2>>(a, s);
+    }
 }
 
 } // namespace moe_ep

@@ -153,7 +153,9 @@ struct TileFinder {
         t.expert = base + l;
         const int begin = __builtin_amdgcn_readlane(elo, l), end = __builtin_amdgcn_readlane(ehi, l);
         const int units = (int)(((int64_t)end - begin + kUnit - 1) / kUnit), each = units / tiles, more = units % tiles;
-        const int row = band * kBand + in % height; // row tiles of each + 1 units, `more` of them, then of each
+        // row tiles of each + 1 units, `more` of them, then of each; a workgroup's
+        // next tile is of another height than its last
+        const int within = in % height, row = band * kBand + (within + (unsigned)(at - within) / 32) % height;
         t.first = begin + (int64_t)(row * each + min(row, more)) * kUnit;
         t.last = min((int64_t)end, t.first + (each + (row < more)) * kUnit);
         return t;
