@@ -225,7 +225,8 @@ __device__ __forceinline__ u32x2 mx_codes(const float *f, uint32_t top, uint8_t 
 // 2^(b - 127) of an e8m0 byte; NaN for 255.
 __device__ __forceinline__ float e8m0_value(uint32_t b)
 {
-    return __uint_as_float(b == 255 ? 0x7FC00000u : b == 0 ? 0x00400000u : b << 23);
+    const uint32_t bits = max(b << 23, 0x00400000u); // 2^-127 is subnormal
+    return __uint_as_float(b == 255 ? 0x7FC00000u : bits);
 }
 
 // 8 e4m3 codes times a scale.
