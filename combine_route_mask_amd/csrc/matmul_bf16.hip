@@ -351,18 +351,6 @@ __device__ __forceinline__ void each_eight(ACC &acc, int from, int j, FN f)
     }
 }
 
-// The largest of the four lanes of a row, in all of them.
-__device__ __forceinline__ uint32_t row_max(uint32_t x)
-{
-#if defined(__HIP_DEVICE_COMPILE__)
-    const auto s = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-    x = max(s[0], s[1]);
-    const auto t = __builtin_amdgcn_permlane32_swap(x, x, false, false);
-    x = max(t[0], t[1]);
-#endif
-    return x;
-}
-
 __device__ __forceinline__ void store8(uint16_t *to, const float *f)
 {
     *reinterpret_cast<u32x4 *>(to) = RowType<Bf16>::pack(f);
@@ -391,7 +379,7 @@ __device__ __forceinline__ void save8(const Job &a, int64_t at, const float *f, 
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         top = max(top, magnitude(f[i]));
-    top = row_max(top);
+    top = max_of_rows(top);
     uint8_t scale;
     const u32x2 codes = mx_codes(f, top, scale);
     if (!in)

@@ -345,13 +345,23 @@ hipError_t four_bit_launch(const moe_ep_four_bit_args &a, hipStream_t s)
     return hipGetLastError();
 }
 
+// Times in us, other side behind the stroke.  With at most two workgroups for
+// each CU four stages of two resident ones, else three of three: 8 rows over 8 of
+// 32 experts of 4096 x 7168 (512 workgroups) 27.5 / 35.8, 64 rows over 32 of
+// 4096 x 2048 28.5 / 32.5, 64 over 64 of 2048 x 1024 16.7 / 19.9.  For 17 rows or
+// more stages of 64 (one workgroup a CU).  Where 64 channels a workgroup leave
+// CUs without one, 16 channels straight into registers: 16 rows, dense 7168 x
+// 2048, 7.9 / 10.
 template <typename T, bool GATED>
 hipError_t four_bit_shape(const moe_ep_four_bit_args &a, hipStream_t s)
 {
     const int64_t rows = (a.num_rows + a.num_experts - 1) / a.num_experts, busy = std::min<int64_t>(a.num_rows, a.num_experts);
     if (rows > 16)
         return four_bit_launch<T, GATED, Stage<64, 3>>(a, s);
-    if (busy * channel_tiles(a.n, 64) >= 256)
+    const int64_t groups = busy * channel_tiles(a.n, 64);
+    if (groups > 512)
+        return four_bit_launch<T, GATED, Stage<16, 3>>(a, s);
+    if (groups >= 256)
         return four_bit_launch<T, GATED, Stage<16, 4>>(a, s);
     const int ntiles = channel_tiles(GATED ? a.n / 2 : a.n, 16);
     const int64_t tiles = (int64_t)ntiles * a.num_experts;

@@ -1,6 +1,10 @@
 // gfx950 kernels of the router: the largest logits of each token with their
-// softmax weights, and the gradient of the weights for the logits.  One wave a
-// token, its logits in LDS.
+// softmax weights, and the gradient of the weights for the logits.  Up to 512
+// experts 16 or 64 lanes hold a token's logits in registers, a few consecutive
+// ones each; beyond, a wave holds them in LDS.  Instructions bound large calls
+// (a round for each place), the launch small ones.
+#include <type_traits>
+
 #include "ffn_internal.h"
 #include "rows.h"
 
@@ -25,6 +29,232 @@ __device__ __forceinline__ void store_logit(void *base, int64_t i, float x)
 }
 
 __device__ __forceinline__ float nan_value() { return __uint_as_float(0x7FC00000u); }
+
+// ------------------------------------------------------------ a few logits a lane
+
+typedef u32x4 Words4 __attribute__((aligned(4)));
+typedef u32x2 Words2 __attribute__((aligned(2)));
+
+// V consecutive logits from i on, those from E on as `other`.
+template <typename T, int V>
+__device__ __forceinline__ void load_logits(const void *base, int64_t row, int i, int E, float other, float (&x)[V])
+{
+    if (V % 4 == 0 && i + V <= E) {
+        const uint8_t *p = static_cast<const uint8_t *>(base) + (row + i) * RowType<T>::kBytes;
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+            if (RowType<T>::kBytes == 2) {
+                const u32x2 w = *reinterpret_cast<const Words2 *>(p + 2 * v);
+                unpack_bf16x2(w[0], x[v % V], x[(v + 1) % V]);
+                unpack_bf16x2(w[1], x[(v + 2) % V], x[(v + 3) % V]);
+            } else {
+                const u32x4 w = *reinterpret_cast<const Words4 *>(p + 4 * v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[(v + e) % V] = __uint_as_float(w[e]);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        x[v] = i + v < E ? logit<T>(base, row + i + v) : other;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_logits(void *base, int64_t row, int i, int E, const float (&x)[V])
+{
+    if (V % 4 == 0 && i + V <= E) {
+        uint8_t *p = static_cast<uint8_t *>(base) + (row + i) * RowType<T>::kBytes;
+#pragma unroll
+        for (int v = 0; v < V; v += 4) {
+            const float f[8] = {x[v % V], x[(v + 1) % V], x[(v + 2) % V], x[(v + 3) % V], 0.0f, 0.0f, 0.0f, 0.0f};
+            const u32x4 w = RowType<T>::pack(f);
+            if (RowType<T>::kBytes == 2)
+                *reinterpret_cast<Words2 *>(p + 2 * v) = u32x2{w[0], w[1]};
+            else
+                *reinterpret_cast<Words4 *>(p + 4 * v) = w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (i + v < E)
+            store_logit<T>(base, row + i + v, x[v]);
+}
+
+// Over the LANES (16 or 64) lanes of a token, in all of them.
+template <int LANES>
+__device__ __forceinline__ uint32_t token_max(uint32_t x)
+{
+    return LANES == 64 ? wave_max(x) : max16(x);
+}
+
+template <int LANES>
+__device__ __forceinline__ float token_sum(float x)
+{
+    if (LANES == 64)
+        return wave_sum(x);
+    x += dpp<kDppXor1>(x);
+    x += dpp<kDppXor2>(x);
+    x += dpp<kDppMirror8>(x);
+    return x + dpp<kDppMirror16>(x);
+}
+
+// The value of the token's lane j.
+template <int LANES, typename X>
+__device__ __forceinline__ X of_lane(X x, int j)
+{
+    if (LANES == 64) // j is the same in all lanes
+        return __builtin_bit_cast(X, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), j));
+    return __shfl(x, j, 16);
+}
+
+// A logit as a number that orders like it, 0 where it is never chosen.
+__device__ __forceinline__ uint32_t order_of(float x)
+{
+    const uint32_t u = __float_as_uint(x + 0.0f); // -0 is 0
+    return x > -INFINITY ? u ^ ((uint32_t)((int)u >> 31) | 0x80000000u) : 0;
+}
+
+__device__ __forceinline__ float value_of(uint32_t k)
+{
+    return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// Each lane sorts its V logits once (neighbours change places only where the
+// later one is larger, so that equal ones keep their order); in a round the
+// lanes' first ones compete, the lowest lane wins of equal ones and moves up.
+// Lane j keeps place j.
+template <typename T, int LANES, int V>
+__global__ __launch_bounds__(256) void route_lanes_kernel(moe_ep_route_args a)
+{
+    constexpr int PER = 256 / LANES;
+    const int E = a.num_experts, lane = threadIdx.x % LANES;
+    for (int64_t t0 = (int64_t)blockIdx.x * PER; t0 < a.tokens; t0 += (int64_t)gridDim.x * PER) {
+        const int64_t mine = t0 + threadIdx.x / LANES, t = min(mine, a.tokens - 1); // lanes without a token do the last's again
+        float x[V];
+        load_logits<T, V>(a.logits, t * E, lane * V, E, -INFINITY, x);
+        uint32_t key[V], bad = 0;
+        int id[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            key[v] = order_of(x[v]);
+            id[v] = lane * V + v;
+            bad |= x[v] != x[v];
+        }
+#pragma unroll
+        for (int pass = 0; pass < V; ++pass)
+#pragma unroll
+            for (int v = pass % 2; v + 1 < V; v += 2) {
+                const bool turn = key[v + 1] > key[v];
+                const uint32_t k = key[v];
+                const int i = id[v];
+                key[v] = turn ? key[v + 1] : k;
+                id[v] = turn ? id[v + 1] : i;
+                key[v + 1] = turn ? k : key[v + 1];
+                id[v + 1] = turn ? i : id[v + 1];
+            }
+        uint32_t top = 0, kept = 0;
+        int place = E;
+        for (int j = 0; j < a.top_k; ++j) {
+            const uint32_t best = token_max<LANES>(key[0]);
+            const uint64_t ties = __ballot(key[0] == best);
+            const int winner = __builtin_ctzll(LANES == 64 ? ties : ties >> (threadIdx.x & 48));
+            const int chosen = of_lane<LANES>(id[0], winner);
+            if (j == 0)
+                top = best;
+            if (lane == j) {
+                kept = best;
+                place = best ? chosen : E;
+            }
+            const bool pop = lane == winner;
+#pragma unroll
+            for (int v = 0; v + 1 < V; ++v) {
+                key[v] = pop ? key[v + 1] : key[v];
+                id[v] = pop ? id[v + 1] : id[v];
+            }
+            key[V - 1] = pop ? 0 : key[V - 1];
+        }
+        const float peak = value_of(top);
+        const float e = kept ? expf(value_of(kept) - peak) : 0.0f;
+        float total = e;
+        if (!a.renormalize) {
+            total = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                total += expf(x[v] - peak);
+        }
+        total = token_sum<LANES>(total);
+        const bool nan = token_max<LANES>(bad) != 0;
+        if (lane < a.top_k && mine < a.tokens) {
+            a.ids[t * a.top_k + lane] = place;
+            a.weights[t * a.top_k + lane] = place == E ? 0.0f : nan ? nan_value() : a.scale * (e / total);
+        }
+    }
+}
+
+template <typename T, int LANES, int V>
+__global__ __launch_bounds__(256) void route_lanes_backward_kernel(moe_ep_route_grad_args a)
+{
+    constexpr int PER = 256 / LANES;
+    const int E = a.num_experts, lane = threadIdx.x % LANES;
+    for (int64_t t0 = (int64_t)blockIdx.x * PER; t0 < a.tokens; t0 += (int64_t)gridDim.x * PER) {
+        const int64_t mine = t0 + threadIdx.x / LANES, t = min(mine, a.tokens - 1);
+        int id = E;
+        float g = 0.0f;
+        if (lane < a.top_k) {
+            id = a.ids[t * a.top_k + lane];
+            g = a.grad_weights[t * a.top_k + lane];
+        }
+        const bool held = id >= 0 && id < E;
+        const float chosen = held ? logit<T>(a.logits, t * E + id) : -INFINITY;
+        float x[V];
+        float top = chosen;
+        if (!a.renormalize) {
+            load_logits<T, V>(a.logits, t * E, lane * V, E, -INFINITY, x);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                top = fmaxf(top, x[v]);
+        }
+        const uint32_t peak_key = token_max<LANES>(order_of(top));
+        const float peak = peak_key ? value_of(peak_key) : 0.0f;
+        const float e = held ? expf(chosen - peak) : 0.0f;
+        float total = e;
+        if (!a.renormalize) {
+            total = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                x[v] = expf(x[v] - peak);
+                total += x[v];
+            }
+        }
+        total = token_sum<LANES>(total);
+        const float by = total != 0.0f ? 1.0f / total : 0.0f;
+        const float mean = token_sum<LANES>(held ? e * by * g : 0.0f);
+        // what an expert's place gives: the gradient, or its part of it
+        const float gives = a.renormalize ? a.scale * (e * by) * (g - mean) : g;
+        float d[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            d[v] = 0.0f;
+        for (int j = 0; j < a.top_k; ++j) {
+            const int at = of_lane<LANES>(id, j) - lane * V;
+            const float y = of_lane<LANES>(gives, j);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                d[v] = at == v ? y : d[v];
+        }
+        if (!a.renormalize)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                d[v] = a.scale * (x[v] * by) * (d[v] - mean);
+        if (mine < a.tokens)
+            store_logits<T, V>(a.grad_logits, t * E, lane * V, E, d);
+    }
+}
+
+// ------------------------------------------------------------ logits in LDS
 
 template <typename T>
 __global__ __launch_bounds__(64) void route_kernel(moe_ep_route_args a)
@@ -146,24 +376,65 @@ inline dim3 tokens_grid(int64_t tokens)
     return dim3((unsigned)(tokens < cap ? tokens : cap));
 }
 
+// Calls f(lanes, logits a lane) for the kernels in registers, or returns false.
+template <typename F>
+bool with_lanes(int experts, int top_k, F f)
+{
+    using std::integral_constant;
+    if (experts <= 64 && top_k <= 16) {
+        if (experts <= 16)
+            f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+        else
+            f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+    } else if (experts <= 64) {
+        f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    } else if (experts <= 256) {
+        f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+    } else if (experts <= 512) {
+        f(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+    } else {
+        return false;
+    }
+    return true;
+}
+
+template <typename T>
+hipError_t route_launch(const moe_ep_route_args &a, hipStream_t s)
+{
+    if (!with_lanes(a.num_experts, a.top_k, [&](auto lanes, auto logits) {
+            constexpr int L = decltype(lanes)::value, V = decltype(logits)::value;
+            hipLaunchKernelGGL((route_lanes_kernel<T, L, V>), tokens_grid((a.tokens + 256 / L - 1) / (256 / L)), dim3(256), 0, s, a);
+        }))
+        hipLaunchKernelGGL(route_kernel<T>, tokens_grid(a.tokens), dim3(64), 4 * a.num_experts, s, a);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t route_backward_launch(const moe_ep_route_grad_args &a, hipStream_t s)
+{
+    // Over the chosen experts alone little is computed, and a wave's LDS takes the
+    // few places sooner than registers do (32768 tokens, 256 experts, 8 places:
+    // 13.0 / 15.1 us; over all experts 26.3 / 18.7).
+    const bool lds = a.renormalize && a.num_experts > 64;
+    if (lds || !with_lanes(a.num_experts, a.top_k, [&](auto lanes, auto logits) {
+            constexpr int L = decltype(lanes)::value, V = decltype(logits)::value;
+            hipLaunchKernelGGL((route_lanes_backward_kernel<T, L, V>), tokens_grid((a.tokens + 256 / L - 1) / (256 / L)),
+                               dim3(256), 0, s, a);
+        }))
+        hipLaunchKernelGGL(route_backward_kernel<T>, tokens_grid(a.tokens), dim3(64), 4 * a.num_experts, s, a);
+    return hipGetLastError();
+}
+
 } // namespace
 
 hipError_t launch_route_top_k(const moe_ep_route_args &a, hipStream_t s)
 {
-    if (a.row_type == MOE_EP_BF16_ROWS)
-        hipLaunchKernelGGL(route_kernel<Bf16>, tokens_grid(a.tokens), dim3(64), 4 * a.num_experts, s, a);
-    else
-        hipLaunchKernelGGL(route_kernel<Fp32>, tokens_grid(a.tokens), dim3(64), 4 * a.num_experts, s, a);
-    return hipGetLastError();
+    return a.row_type == MOE_EP_BF16_ROWS ? route_launch<Bf16>(a, s) : route_launch<Fp32>(a, s);
 }
 
 hipError_t launch_route_top_k_backward(const moe_ep_route_grad_args &a, hipStream_t s)
 {
-    if (a.row_type == MOE_EP_BF16_ROWS)
-        hipLaunchKernelGGL(route_backward_kernel<Bf16>, tokens_grid(a.tokens), dim3(64), 4 * a.num_experts, s, a);
-    else
-        hipLaunchKernelGGL(route_backward_kernel<Fp32>, tokens_grid(a.tokens), dim3(64), 4 * a.num_experts, s, a);
-    return hipGetLastError();
+    return a.row_type == MOE_EP_BF16_ROWS ? route_backward_launch<Bf16>(a, s) : route_backward_launch<Fp32>(a, s);
 }
 
 } // namespace moe_ep

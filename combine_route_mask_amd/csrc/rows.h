@@ -119,6 +119,18 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x)
     return max(x, (uint32_t)__shfl_xor((int)x, 32));
 }
 
+// Largest value of the four lanes l % 16, + 16, + 32, + 48, in all of them, without LDS.
+__device__ __forceinline__ uint32_t max_of_rows(uint32_t x)
+{
+#if defined(__HIP_DEVICE_COMPILE__) // the host compiler does not know the exchanges
+    const auto s = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    x = max(s[0], s[1]);
+    const auto t = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    x = max(t[0], t[1]);
+#endif
+    return x;
+}
+
 __device__ __forceinline__ int wave_add(int x)
 {
     x += (int)dpp<kDppXor1>((uint32_t)x);
