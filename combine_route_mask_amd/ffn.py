@@ -83,6 +83,11 @@ def _out(out, name, dev, dtype, shape):
     return out
 
 
+def _as(t, dtype):
+    """Bytes as what they hold."""
+    return t.view(dtype) if t.dtype == torch.uint8 else t
+
+
 def _save_code(checkpoint, *widths):
     code = _SAVES.get(checkpoint)
     if code is None:
@@ -115,8 +120,9 @@ def checkpoint_rows(x, *, out=None, out_scales=None, stream=None) -> MxRows:
 
 
 def restore_rows(rows, scales, *, dtype=None, out=None, stream=None):
-    """MXFP8 rows (a checkpoint, or a dispatch's payload) as bf16 or fp32
-    rows, ``out``'s type or bf16; bf16 holds code * scale exactly."""
+    """MXFP8 rows as bf16 or fp32 rows, ``out``'s type or bf16; bf16 holds
+    code * scale exactly.  ``rows`` and ``scales`` are a checkpoint's, or the
+    bytes (uint8) of an MXFP8 dispatch's payload as the sort leaves them."""
     _no_grad(out)
     if out is not None and dtype not in (None, out.dtype):
         _refuse(f"out is {out.dtype}, the result's dtype {dtype}")
@@ -124,6 +130,7 @@ def restore_rows(rows, scales, *, dtype=None, out=None, stream=None):
     if stream is not None or dev.index != _device_now():
         with _On(dev, stream):
             return restore_rows(rows, scales, dtype=dtype, out=out)
+    rows, scales = _as(rows, _CODES), _as(scales, _SCALES)
     M, H = _rows2(rows, "rows", dev, _CODES)
     if H < 32 or H % 32:
         _refuse(f"MXFP8 rows need a width that is a multiple of 32, got {H}")
