@@ -697,13 +697,15 @@ hipError_t product_shape(const Job &a, hipStream_t s)
     }
 }
 
-// Rows from the last expert's last on become zeros.
+// Rows before the first expert's first and from the last one's last on become
+// zeros.
 __global__ __launch_bounds__(256) void zero_rest_kernel(Job a)
 {
-    const int64_t last = a.offsets ? min(max((int64_t)a.offsets[a.num_experts], (int64_t)0), a.num_rows) : a.num_rows;
-    const int64_t units = a.num_rows * (a.n / 8);
-    for (int64_t i = last * (a.n / 8) + (int64_t)blockIdx.x * 256 + threadIdx.x; i < units; i += (int64_t)gridDim.x * 256)
-        reinterpret_cast<u32x4 *>(a.out)[i] = u32x4{0, 0, 0, 0};
+    const int64_t first = min(max((int64_t)a.offsets[0], (int64_t)0), a.num_rows);
+    const int64_t last = min(max((int64_t)a.offsets[a.num_experts], first), a.num_rows);
+    const int64_t units = a.n / 8, held = (last - first) * units, rest = a.num_rows * units - held;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rest; i += (int64_t)gridDim.x * 256)
+        reinterpret_cast<u32x4 *>(a.out)[i < first * units ? i : i + held] = u32x4{0, 0, 0, 0};
 }
 
 // ------------------------------------------------------------ the weights' gradient

@@ -5,7 +5,10 @@ what its backward pass reads, and products with 4-bit weights for serving.
 ``expert_ffn`` takes the rows of ``experts.expert_sort`` (bf16) and its
 ``offsets`` and gives the rows that ``experts.expert_unsort`` takes back; with
 dense weights and no offsets it is a shared expert.  Streams, allocations,
-errors and gradients follow the rules of ``experts``.
+errors and gradients follow the rules of ``experts``.  In a HIP graph capture
+the explicit calls (``expert_ffn_forward``, ``expert_ffn_backward``): torch
+ends the process when autograd's backward pass is captured while an eager
+graph of the same leaves lives.
 """
 from __future__ import annotations
 
@@ -123,7 +126,7 @@ def restore_rows(rows, scales, *, dtype=None, out=None, stream=None):
     """MXFP8 rows as bf16 or fp32 rows, ``out``'s type or bf16; bf16 holds
     code * scale exactly.  ``rows`` and ``scales`` are a checkpoint's, or the
     bytes (uint8) of an MXFP8 dispatch's payload as the sort leaves them."""
-    _no_grad(out)
+    _no_grad(rows, out)
     if out is not None and dtype not in (None, out.dtype):
         _refuse(f"out is {out.dtype}, the result's dtype {dtype}")
     dev = _device(rows, "rows")
@@ -362,6 +365,9 @@ class _FfnFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w1, w2, offsets, checkpoint):
         y, saved = expert_ffn_forward(x, w1, w2, offsets=offsets, checkpoint=checkpoint)
+        if saved.x_scales is None and x.untyped_storage().nbytes() != x.numel() * x.element_size():
+            # a part of a workspace, which the next dispatch overwrites unseen by autograd
+            saved = saved._replace(x=x.clone())
         ctx.save_for_backward(w1, w2, offsets, *saved)
         return y
 

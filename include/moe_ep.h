@@ -593,8 +593,8 @@ int moe_ep_restore_rows(const moe_ep_checkpoint_args *args, void *stream);
  *  out[m][j] = sum over i of x[m][i] * w[e][j][i]   (transposed = 0, w [E][n][k])
  *  out[m][j] = sum over i of x[m][i] * w[e][i][j]   (transposed = 1, w [E][k][n])
  * in fp32, rounded once to bf16.  The order of the sum depends on the shape
- * alone.  n and k multiples of 8, at most 131072.  zero_rest = 1: rows from
- * the last expert's last on become zeros.
+ * alone.  n and k multiples of 8, at most 131072.  zero_rest = 1: rows outside
+ * offsets[0] .. offsets[E] - 1 become zeros.
  */
 typedef struct moe_ep_product_args {
     const void *x;               /* [num_rows][k] bf16                       */

@@ -436,6 +436,25 @@ def test_offsets_out_of_range(M):
     assert torch.equal(F.expert_matmul_mxfp4(x, codes, scales, offsets=bad), F.expert_matmul_mxfp4(x, codes, scales, offsets=good))
 
 
+def test_rows_outside_the_experts(M):
+    """Under autograd rows before the first and behind the last expert's are zeros, in the result and the gradient."""
+    F = M.F
+    x, (w1, w2) = _normal(1, 50, 64), _weights(2, 2, 64, 32)
+    off = torch.tensor([7, 20, 41], dtype=torch.int32, device="cuda")
+    leaves = [t.clone().requires_grad_() for t in (x, w1, w2)]
+    y = F.expert_ffn(*leaves, offsets=off)
+    gx, = torch.autograd.grad(y.sum(), leaves[:1])
+    for t in (y.detach(), gx):
+        assert not bool(t[:7].any() or t[41:].any()) and bool(t[7:41].any(dim=1).all())
+    # rows that lie in a larger buffer are kept as they were in the forward pass
+    space = torch.cat([x, x])
+    part = space[:50].requires_grad_()
+    y = F.expert_ffn(part, leaves[1], leaves[2], offsets=off)
+    space.data.fill_(7.0)  # as a kernel writes: unseen by autograd
+    want = F.expert_ffn(x.clone().requires_grad_(), leaves[1], leaves[2], offsets=off)
+    assert _same(torch.autograd.grad(y.sum(), leaves[1:]), torch.autograd.grad(want.sum(), leaves[1:]))
+
+
 def test_empty_calls(M):
     F, R = M.F, M.R
     (w1, w2), off = _weights(1, 2, 64, 32), torch.zeros(3, dtype=torch.int32, device="cuda")
