@@ -83,11 +83,20 @@ __device__ __forceinline__ void store_logits(void *base, int64_t row, int i, int
             store_logit<T>(base, row + i + v, x[v]);
 }
 
-// Over the LANES (16 or 64) lanes of a token, in all of them.
+// Over the LANES (16 or 64) lanes of a token, in all of them.  Of a wave: rows of
+// 16 hand theirs to the next, and the last lane has it; no LDS, whose latency
+// each round would wait for.
 template <int LANES>
 __device__ __forceinline__ uint32_t token_max(uint32_t x)
 {
-    return LANES == 64 ? wave_max(x) : max16(x);
+    x = max16(x);
+    if (LANES == 64) {
+        constexpr int kBroadcast15 = 0x142, kBroadcast31 = 0x143;
+        x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kBroadcast15, 0xA, 0xF, false));
+        x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kBroadcast31, 0xC, 0xF, false));
+        x = (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+    }
+    return x;
 }
 
 template <int LANES>
@@ -168,13 +177,14 @@ __global__ __launch_bounds__(256) void route_lanes_kernel(moe_ep_route_args a)
                 kept = best;
                 place = best ? chosen : E;
             }
-            const bool pop = lane == winner;
+            // bit by bit: selects of neighbours would become selects of their places
+            const uint32_t pop = lane == winner ? 0xFFFFFFFFu : 0;
 #pragma unroll
             for (int v = 0; v + 1 < V; ++v) {
-                key[v] = pop ? key[v + 1] : key[v];
-                id[v] = pop ? id[v + 1] : id[v];
+                key[v] = (key[v + 1] & pop) | (key[v] & ~pop);
+                id[v] = (int)(((uint32_t)id[v + 1] & pop) | ((uint32_t)id[v] & ~pop));
             }
-            key[V - 1] = pop ? 0 : key[V - 1];
+            key[V - 1] &= ~pop;
         }
         const float peak = value_of(top);
         const float e = kept ? expf(value_of(kept) - peak) : 0.0f;
