@@ -37,6 +37,7 @@ struct Job {
     uint16_t *grad_pre;
     int64_t num_rows;
     int num_experts, n, k, save;
+    bool zero_rest;
 };
 
 // A workgroup takes BN channels and BM rows, 64 elements of k at a time,
@@ -581,12 +582,25 @@ using Finder = typename Heights<S...>::Finder;
 
 constexpr float kEdgeRows = 24.0f; // a tile's beginning and end take as long as this many of its rows
 
+// Rows before the first expert's first and from the last one's last on become
+// zeros, a part of them by each workgroup.
+__device__ __forceinline__ void zero_rest(const Job &a)
+{
+    const int64_t first = min(max((int64_t)a.offsets[0], (int64_t)0), a.num_rows);
+    const int64_t last = min(max((int64_t)a.offsets[a.num_experts], first), a.num_rows);
+    const int64_t units = a.n / 8, held = (last - first) * units, rest = a.num_rows * units - held;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < rest; i += (int64_t)gridDim.x * blockDim.x)
+        reinterpret_cast<u32x4 *>(a.out)[i < first * units ? i : i + held] = u32x4{0, 0, 0, 0};
+}
+
 // A workgroup takes the tiles `slot`, slot + (workgroups of the XCD), ... of
 // its XCD's run, and sends off the next one's first stages before it stores.
 template <int EPI, bool ACROSS, typename S, typename... MORE>
 __global__ __launch_bounds__(S::THREADS, 2) void product_kernel(Job a, int ntiles)
 {
     __shared__ __align__(256) uint8_t lds[largest(S::STAGES * S::BYTES, (MORE::STAGES * MORE::BYTES)...)];
+    if (EPI == kStore && a.zero_rest)
+        zero_rest(a);
     const Finder<S, MORE...> find(a, ntiles, kEdgeRows);
     int slot = (int)(blockIdx.x >> 3);
     Tile t = find.tile(a, slot);
@@ -695,17 +709,6 @@ hipError_t product_shape(const Job &a, hipStream_t s)
         return product_launch<EPI, ACROSS, TileShape<4, 2, 4, 2, 2>, TileShape<4, 2, 4, 4, 2>, TileShape<2, 4, 8, 3, 2>,
                               TileShape<2, 4, 8, 4, 2>, TileShape<2, 4, 8, 5, 2>>(a, s);
     }
-}
-
-// Rows before the first expert's first and from the last one's last on become
-// zeros.
-__global__ __launch_bounds__(256) void zero_rest_kernel(Job a)
-{
-    const int64_t first = min(max((int64_t)a.offsets[0], (int64_t)0), a.num_rows);
-    const int64_t last = min(max((int64_t)a.offsets[a.num_experts], first), a.num_rows);
-    const int64_t units = a.n / 8, held = (last - first) * units, rest = a.num_rows * units - held;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rest; i += (int64_t)gridDim.x * 256)
-        reinterpret_cast<u32x4 *>(a.out)[i < first * units ? i : i + held] = u32x4{0, 0, 0, 0};
 }
 
 // ------------------------------------------------------------ the weights' gradient
@@ -822,11 +825,8 @@ hipError_t launch_expert_product(const moe_ep_product_args &a, hipStream_t s)
     j.num_experts = a.num_experts;
     j.n = a.n;
     j.k = a.k;
-    const hipError_t e = a.transposed ? product_shape<kStore, true>(j, s) : product_shape<kStore, false>(j, s);
-    if (e != hipSuccess || !a.zero_rest || !a.offsets)
-        return e;
-    hipLaunchKernelGGL(zero_rest_kernel, dim3(256), dim3(256), 0, s, j);
-    return hipGetLastError();
+    j.zero_rest = a.zero_rest && a.offsets;
+    return a.transposed ? product_shape<kStore, true>(j, s) : product_shape<kStore, false>(j, s);
 }
 
 hipError_t launch_gated_product(const moe_ep_gated_args &a, hipStream_t s)
