@@ -52,13 +52,13 @@ int check_route(int64_t tokens, int32_t num_experts, int32_t top_k, int32_t reno
 // What a gated block keeps of its first product; `needed`: of an input.
 int check_saved(int32_t save, int32_t inter_size, const void *pre, const void *pre_scales, bool needed)
 {
-    if (save != MOE_EP_SAVE_BF16 && save != MOE_EP_SAVE_MXFP8 && (needed || save != MOE_EP_SAVE_NONE))
+    if (save != MOE_EP_SAVE_HALF && save != MOE_EP_SAVE_MXFP8 && (needed || save != MOE_EP_SAVE_NONE))
         return fail(MOE_EP_ERR_UNSUPPORTED, "unknown save");
     if (save == MOE_EP_SAVE_MXFP8 && inter_size % 32)
         return bad("an MXFP8 checkpoint needs an inter_size that is a multiple of 32");
     if (save != MOE_EP_SAVE_NONE && !good(pre, 16))
         return bad("pre must be a 16-byte aligned device pointer");
-    if (save == MOE_EP_SAVE_MXFP8 && !pre_scales)
+    if (save != MOE_EP_SAVE_NONE && !pre_scales)
         return bad("pre_scales is NULL");
     return MOE_EP_OK;
 }

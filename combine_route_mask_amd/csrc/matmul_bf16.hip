@@ -368,18 +368,29 @@ __device__ __forceinline__ void store8_nt(uint16_t *to, const float *f)
 }
 
 // Eight channels `at` of the first product's row as the backward pass reads
-// them; the four lanes of a row hold a block of 32.
+// them: fp16 over a power of two of their own, or MXFP8, whose blocks of 32 the
+// four lanes of a row hold.
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
 __device__ __forceinline__ void save8(const Job &a, int64_t at, const float *f, bool in)
 {
-    if (a.save == MOE_EP_SAVE_BF16) {
-        if (in)
-            store8(static_cast<uint16_t *>(a.pre) + at, f);
-        return;
-    }
     uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         top = max(top, magnitude(f[i]));
+    if (a.save == MOE_EP_SAVE_HALF) {
+        const uint32_t b = top >= kInfinity ? 127 : min(max(top >> 23, 1u), 253u);
+        const float by = __uint_as_float((254 - b) << 23);
+        f16x8 v;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = (_Float16)(f[i] * by);
+        if (in) {
+            *reinterpret_cast<f16x8 *>(static_cast<uint16_t *>(a.pre) + at) = v;
+            a.pre_scales[at / 8] = (uint8_t)b;
+        }
+        return;
+    }
     top = max_of_rows(top);
     uint8_t scale;
     const u32x2 codes = mx_codes(f, top, scale);
@@ -390,30 +401,39 @@ __device__ __forceinline__ void save8(const Job &a, int64_t at, const float *f, 
         a.pre_scales[at / 32] = scale;
 }
 
-// Eight gate and eight up values of the first product as they were saved: bf16,
-// or codes and in the third word their scale.
+// Eight gate and eight up values of the first product as they were saved.
 struct Saved {
-    u32x4 gate, up;
+    u32x4 gate, up;            // MXFP8: the first two words
+    uint32_t gate_scale, up_scale;
     __device__ __forceinline__ void load(const Job &a, int64_t at, int I)
     {
-        if (a.save == MOE_EP_SAVE_BF16) {
+        if (a.save == MOE_EP_SAVE_HALF) {
             gate = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.pre) + at);
             up = *reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(a.pre) + at + I);
+            gate_scale = a.pre_scales[at / 8];
+            up_scale = a.pre_scales[(at + I) / 8];
         } else {
             const uint8_t *p = static_cast<const uint8_t *>(a.pre) + at;
             const u32x2 g = *reinterpret_cast<const u32x2 *>(p), u = *reinterpret_cast<const u32x2 *>(p + I);
-            gate = u32x4{g[0], g[1], a.pre_scales[at / 32], 0};
-            up = u32x4{u[0], u[1], a.pre_scales[(at + I) / 32], 0};
+            gate = u32x4{g[0], g[1], 0, 0};
+            up = u32x4{u[0], u[1], 0, 0};
+            gate_scale = a.pre_scales[at / 32];
+            up_scale = a.pre_scales[(at + I) / 32];
         }
     }
     __device__ __forceinline__ void values(const Job &a, float *g, float *u) const
     {
-        if (a.save == MOE_EP_SAVE_BF16) {
-            RowType<Bf16>::unpack(gate, g);
-            RowType<Bf16>::unpack(up, u);
+        const float gs = e8m0_value(gate_scale), us = e8m0_value(up_scale);
+        if (a.save == MOE_EP_SAVE_HALF) {
+            const f16x8 gv = __builtin_bit_cast(f16x8, gate), uv = __builtin_bit_cast(f16x8, up);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                g[i] = (float)gv[i] * gs;
+                u[i] = (float)uv[i] * us;
+            }
         } else {
-            mx_values(u32x2{gate[0], gate[1]}, e8m0_value(gate[2]), g);
-            mx_values(u32x2{up[0], up[1]}, e8m0_value(up[2]), u);
+            mx_values(u32x2{gate[0], gate[1]}, gs, g);
+            mx_values(u32x2{up[0], up[1]}, us, u);
         }
     }
 };

@@ -20,9 +20,10 @@ import torch
 from .experts import (_call, _device, _device_now, _empty, _flat, _no_grad, _On, _refuse, _row_type, _whole, _written)
 from .moe_ep import _need, lib
 
-SAVE_NONE, SAVE_BF16, SAVE_MXFP8 = 0, 1, 2
-_SAVES = {"bf16": SAVE_BF16, "mxfp8": SAVE_MXFP8}
+SAVE_NONE, SAVE_HALF, SAVE_MXFP8 = 0, 1, 2
+_SAVES = {"bf16": SAVE_HALF, "mxfp8": SAVE_MXFP8}
 _BF16, _CODES, _SCALES = torch.bfloat16, torch.float8_e4m3fn, torch.float8_e8m0fnu
+_PRE = {SAVE_HALF: (torch.float16, 8), SAVE_MXFP8: (_CODES, 32)}  # the saved product's type, elements of a scale
 
 # The argument blocks of include/moe_ep.h in native layout.
 _CHECKPOINT = struct.Struct("@PPPqii")
@@ -40,12 +41,13 @@ class MxRows(NamedTuple):
 
 
 class FfnCheckpoint(NamedTuple):
-    """What the backward pass of ``expert_ffn`` reads: its input and the
-    first product (gate, then up), in bf16 or as MXFP8 codes with scales."""
+    """What the backward pass of ``expert_ffn`` reads: its input, as it is or
+    as MXFP8 codes with scales, and the first product (gate, then up) in fp16
+    with an e8m0 scale for eight, or as MXFP8."""
     x: torch.Tensor
     x_scales: Optional[torch.Tensor]
     pre: torch.Tensor
-    pre_scales: Optional[torch.Tensor]
+    pre_scales: torch.Tensor
 
 
 def _ptr(t):
@@ -178,8 +180,10 @@ def _product(x, weight, offsets, transposed, out, stream, zero_rest):
 def gated_product(x, weight, *, offsets=None, checkpoint: Optional[str] = None, out=None, stream=None):
     """silu(gate) * up of bf16 rows [M, K] with each expert's weights
     [E, 2 I, K], gate channels first, in one kernel: (rows [M, I], pre,
-    pre_scales).  ``checkpoint`` "bf16" or "mxfp8" also gives the products
-    themselves [M, 2 I] in that form, for ``gated_product_backward``; else
+    pre_scales).  ``checkpoint`` also gives the products themselves [M, 2 I]
+    for ``gated_product_backward``: "bf16" in fp16 with an e8m0 scale for
+    eight (11 significant bits; bf16's eight would cost the gradients half
+    their accuracy again), "mxfp8" as e4m3 codes with a scale for 32; else
     pre is None.  Rows as in ``expert_product``."""
     _no_grad(x, weight, out)
     dev = _device(x, "x")
@@ -195,18 +199,17 @@ def gated_product(x, weight, *, offsets=None, checkpoint: Optional[str] = None, 
     out = _out(out, "out", dev, _BF16, (M, I))
     pre = scales = None
     if save:
-        pre = _empty((M, N), (N, 1), _CODES if save == SAVE_MXFP8 else _BF16, dev)
-        if save == SAVE_MXFP8:
-            scales = _empty((M, N // 32), (N // 32, 1), _SCALES, dev)
+        dtype, block = _PRE[save]
+        pre, scales = _empty((M, N), (N, 1), dtype, dev), _empty((M, N // block), (N // block, 1), _SCALES, dev)
     _call(lib.moe_ep_gated_product, _GATED, dev, x.data_ptr(), weight.data_ptr(), _ptr(offsets), out.data_ptr(), _ptr(pre),
           _ptr(scales), M, E, I, K, save)
     return out, pre, scales
 
 
-def gated_product_backward(grad_out, weight, pre, pre_scales=None, *, offsets=None, need_rows: bool = True, stream=None):
+def gated_product_backward(grad_out, weight, pre, pre_scales, *, offsets=None, need_rows: bool = True, stream=None):
     """The gradient grad_out [M, N] of the block's second product, weights
-    [E, N, I], taken through it and the activation: (grad_pre [M, 2 I], the
-    activation rows [M, I] again or None)."""
+    [E, N, I], taken through it and the activation at ``gated_product``'s
+    pre: (grad_pre [M, 2 I], the activation rows [M, I] again or None)."""
     _no_grad(grad_out, weight, pre)
     dev = _device(grad_out, "grad_out")
     if stream is not None or dev.index != _device_now():
@@ -216,12 +219,12 @@ def gated_product_backward(grad_out, weight, pre, pre_scales=None, *, offsets=No
     E, n, I = _experts(weight, "weight", dev, _BF16, offsets)
     if n != N:
         _refuse(f"grad_out is [M, {N}], the weight {list(weight.shape)}")
-    save = SAVE_BF16 if pre_scales is None else SAVE_MXFP8
-    _flat(pre, "pre", dev, _BF16 if pre_scales is None else _CODES, (M, 2 * I))
-    if pre_scales is not None:
-        if I % 32:
-            _refuse(f"an MXFP8 checkpoint needs a width that is a multiple of 32, got {I}")
-        _flat(pre_scales, "pre_scales", dev, _SCALES, (M, I // 16))
+    save = SAVE_HALF if pre.dtype == torch.float16 else SAVE_MXFP8
+    dtype, block = _PRE[save]
+    if I % block:
+        _refuse(f"this checkpoint needs a width that is a multiple of {block}, got {I}")
+    _flat(pre, "pre", dev, dtype, (M, 2 * I))
+    _flat(pre_scales, "pre_scales", dev, _SCALES, (M, 2 * I // block))
     grad_pre = _empty((M, 2 * I), (2 * I, 1), _BF16, dev)
     rows = _empty((M, I), (I, 1), _BF16, dev) if need_rows else None
     _call(lib.moe_ep_gated_product_backward, _GATED_GRAD, dev, grad_out.data_ptr(), weight.data_ptr(), _ptr(offsets),
@@ -297,8 +300,9 @@ def expert_ffn(x, w1, w2, *, offsets=None, checkpoint: str = "bf16", out=None, s
     Differentiable in ``x``, ``w1`` and ``w2`` (without ``out`` or
     ``stream``); the rows outside the experts' ranges are then zeros, and
     their gradients too.  ``checkpoint`` says what the backward pass keeps of
-    x and of the first product: "bf16", or "mxfp8" (half the memory, H and I
-    multiples of 32; the gradients are then those at the rounded values)."""
+    x and of the first product: "bf16", x itself and the product in 16 bits, or
+    "mxfp8" (half the memory, H and I multiples of 32; the gradients are then
+    those at the rounded values)."""
     _no_grad(out)
     if torch.is_grad_enabled() and (x.requires_grad or w1.requires_grad or w2.requires_grad):
         _need(out is None and stream is None, "only a block into a new tensor, on the current stream, has a gradient")

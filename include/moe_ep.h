@@ -613,7 +613,7 @@ typedef struct moe_ep_product_args {
 int moe_ep_expert_product(const moe_ep_product_args *args, void *stream);
 
 #define MOE_EP_SAVE_NONE 0
-#define MOE_EP_SAVE_BF16 1   /* pre [num_rows][2 I] bf16                    */
+#define MOE_EP_SAVE_HALF 1   /* pre [num_rows][2 I] fp16, pre_scales [num_rows][2 I / 8] */
 #define MOE_EP_SAVE_MXFP8 2  /* pre [num_rows][2 I] e4m3, pre_scales [num_rows][2 I / 32] */
 
 /*
@@ -621,8 +621,12 @@ int moe_ep_expert_product(const moe_ep_product_args *args, void *stream);
  * [E][2 I][k] (gate channels first), gate = pre[:I], up = pre[I:],
  *  out = silu(gate) * up
  * in fp32 from the unrounded sums, rounded once to bf16.  save: pre as the
- * backward pass reads it, rounded to bf16 or as an 8-bit checkpoint (as
- * moe_ep_checkpoint_rows makes of the unrounded sums; I a multiple of 32).
+ * backward pass reads it, as an 8-bit checkpoint (as moe_ep_checkpoint_rows
+ * makes of the unrounded sums; I a multiple of 32), or in 16 bits: for eight
+ * elements whose largest magnitude is in [2^e, 2^(e+1)) the scale 2^e, as e8m0
+ * (b in 1..253; 127 where an element is no finite number), and value / scale
+ * rounded to fp16.  That keeps 11 significant bits: with bf16's eight the
+ * gradients are half as far off again.
  * I and k multiples of 8, at most 65536 and 131072.
  */
 typedef struct moe_ep_gated_args {
@@ -631,7 +635,7 @@ typedef struct moe_ep_gated_args {
     const int32_t *offsets;      /* [E + 1] or NULL                          */
     void *out;                   /* [num_rows][I] bf16                       */
     void *pre;                   /* as `save` says, or NULL                  */
-    uint8_t *pre_scales;         /* MXFP8 only                               */
+    uint8_t *pre_scales;         /* as `save` says, or NULL                  */
     int64_t num_rows;
     int32_t num_experts;
     int32_t inter_size;          /* I                                        */
@@ -654,14 +658,14 @@ typedef struct moe_ep_gated_grad_args {
     const void *w;               /* [E][n][I] bf16                           */
     const int32_t *offsets;      /* [E + 1] or NULL                          */
     const void *pre;             /* as `save` says                           */
-    const uint8_t *pre_scales;   /* MXFP8 only                               */
+    const uint8_t *pre_scales;   /* as `save` says                           */
     void *grad_pre;              /* [num_rows][2 * I] bf16                   */
     void *out;                   /* [num_rows][I] bf16, or NULL              */
     int64_t num_rows;
     int32_t num_experts;
     int32_t inter_size;          /* I                                        */
     int32_t n;
-    int32_t save;                /* MOE_EP_SAVE_BF16 or _MXFP8               */
+    int32_t save;                /* MOE_EP_SAVE_HALF or _MXFP8               */
 } moe_ep_gated_grad_args;
 
 int moe_ep_gated_product_backward(const moe_ep_gated_grad_args *args, void *stream);

@@ -124,6 +124,19 @@ def mx_round(x, exponent):
     return (torch.round(v / step) * step * scale).view(x.shape)
 
 
+def half_values(rows, scales):
+    """What fp16 rows with a scale for eight hold, in float64."""
+    s = torch.exp2(scales.cpu().view(torch.uint8).double() - 127)
+    return (rows.cpu().double().view(rows.shape[0], -1, 8) * s[:, :, None]).view(rows.shape)
+
+
+def half_step(pre, off):
+    """How far fp16 with a scale for eight may be from `pre` known to `off`: 2^-11 of the value, or half of fp16's
+    least step, 2^-24, of a scale that the largest of the eight is below twice of."""
+    top = (pre.abs() + off).view(pre.shape[0], -1, 8).amax(2, keepdim=True).expand(-1, -1, 8).reshape(pre.shape)
+    return off + 2.0 ** -11 * (pre.abs() + off) + 2.0 ** -24 * top + 2.0 ** -149
+
+
 def mx_values(rows, scales):
     """What MXFP8 codes and scales hold, in float64."""
     s = torch.exp2(scales.cpu().view(torch.uint8).double() - 127)

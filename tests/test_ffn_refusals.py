@@ -90,6 +90,7 @@ BAD += [
     ("moe_ep_gated_product", dict(inter_size=40), ARG), ("moe_ep_gated_product", dict(k=20), ARG),
     ("moe_ep_gated_product", dict(save=3), UNSUP), ("moe_ep_gated_product", dict(pre=0), ARG),
     ("moe_ep_gated_product", dict(pre_scales=0), ARG), ("moe_ep_gated_product", dict(save=1, pre=A + 8), ARG),
+    ("moe_ep_gated_product", dict(save=1, pre_scales=0), ARG),
     ("moe_ep_gated_product", dict(out=0), ARG),
     ("moe_ep_gated_product_backward", dict(save=0), UNSUP), ("moe_ep_gated_product_backward", dict(save=7), UNSUP),
     ("moe_ep_gated_product_backward", dict(inter_size=40), ARG), ("moe_ep_gated_product_backward", dict(n=12), ARG),
@@ -143,12 +144,13 @@ def _calls(F, R, make=lambda t: t):
     q, s = torch.zeros(2, 32, dtype=torch.float8_e4m3fn), torch.zeros(2, 1, dtype=torch.uint8).view(torch.float8_e8m0fnu)
     codes, scales = torch.zeros(8, 16, dtype=torch.uint8), torch.zeros(8, 1, dtype=torch.uint8).view(torch.float8_e8m0fnu)
     ids, w = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 2)
-    saved = F.FfnCheckpoint(x, None, torch.zeros(2, 64, dtype=BF), None)
+    saved = F.FfnCheckpoint(x, None, torch.zeros(2, 64, dtype=torch.float16),
+                            torch.zeros(2, 8, dtype=torch.uint8).view(torch.float8_e8m0fnu))
     return {
         "checkpoint_rows": lambda: F.checkpoint_rows(make(x)), "restore_rows": lambda: F.restore_rows(q, s),
         "expert_product": lambda: F.expert_product(make(x), w2),
         "gated_product": lambda: F.gated_product(make(x), w1),
-        "gated_product_backward": lambda: F.gated_product_backward(make(x), w2, saved.pre),
+        "gated_product_backward": lambda: F.gated_product_backward(make(x), w2, saved.pre, saved.pre_scales),
         "product_weight_grad": lambda: F.product_weight_grad(make(x), x),
         "expert_matmul_mxfp4": lambda: F.expert_matmul_mxfp4(make(x), codes, scales),
         "expert_ffn": lambda: F.expert_ffn(x, w1, w2),

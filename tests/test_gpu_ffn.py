@@ -79,7 +79,9 @@ def test_gated_product(F, M, E, I, K, kind, checkpoint):
     if checkpoint is None:
         assert kept is None and scales is None
     elif checkpoint == "bf16":
-        U.close(kept.cpu()[held], pre[held], U.rounded(poff, pre)[held], "pre")
+        assert kept.dtype == torch.float16 and scales.shape == (M, 2 * I // 8)
+        if bool(held.any()):
+            U.close(U.half_values(kept, scales)[held], pre[held], U.half_step(pre[held], poff[held]), "pre")
     elif bool(held.any()):
         p, q = pre[held], poff[held]
         exponent = scales.cpu()[held].view(torch.uint8).double() - 127
@@ -102,11 +104,13 @@ def test_gated_product_backward(F, M, E, I, N, kind, checkpoint):
     dy, w = U.bf16(rng, M, N), _weight(rng, E, N, I)
     pre = U.bf16(rng, M, 2 * I, size=3.0)
     d, doff, held = U.product(dy, w, o, transposed=True)
-    scales = None
-    given = pre.cuda()
     if checkpoint == "mxfp8":
-        given, scales = F.checkpoint_rows(given)
+        given, scales = F.checkpoint_rows(pre.cuda())
         pre = U.mx_values(given, scales)
+    else:
+        given = pre.half().cuda()
+        scales = torch.from_numpy(rng.integers(124, 130, (M, 2 * I // 8), dtype=np.uint8)).view(torch.float8_e8m0fnu).cuda()
+        pre = U.half_values(given, scales)
     ref, bound, rows, rbound = U.gated_backward(d, doff, pre.double())
     got, again = F.gated_product_backward(dy.cuda(), w.cuda(), given, scales, offsets=off)
     U.close(got.cpu()[held], ref[held], U.rounded(bound, ref)[held], "grad_pre")
@@ -126,6 +130,21 @@ def test_weight_grad(F, M, E, N, K, kind):
         dy[o[-1]:], x[o[-1]:] = float("nan"), float("nan")
     got = F.product_weight_grad(dy.cuda(), x.cuda(), offsets=off)
     U.close(got.cpu().view(ref.shape), ref, U.rounded(bound, ref), "grad_w")
+
+
+def test_saved_products_of_extremes(F):
+    """Large, small and unequal products keep 11 bits beside their largest; what is no finite number stays so."""
+    w = torch.eye(16, dtype=BF).repeat(2, 1)  # gate = up = x
+    x = torch.ones(6, 16, dtype=BF)
+    x[0], x[1], x[2, 3], x[3, 9] = 2.0 ** 127, 2.0 ** -126, float("inf"), float("nan")
+    x[4, :8] = torch.tensor([1, 2.0 ** -8, 2.0 ** -13, 0, -3, 100, -2.0 ** -9, 7], dtype=BF)
+    x[5] = 0
+    _, pre, scales = F.gated_product(x.cuda(), w.cuda(), checkpoint="bf16")
+    got = U.half_values(pre, scales)[:, :16]
+    want = x.double() @ w[:16].double().t()  # 0 times an infinity or NaN is NaN in the other channels
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got.isinf(), want.isinf())
+    fine = want.isfinite()
+    assert torch.equal(got[fine], want[fine])  # each is a bf16 number within 2^-14 of its eight's largest
 
 
 def _pieces(F, x, w1, w2, off, checkpoint, dy):

@@ -37,7 +37,7 @@ def _weights(seed, E, H, I):
 
 
 def _same(a, b):
-    return all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+    return all(torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8)) for x, y in zip(a, b))
 
 
 # ----------------------------------------------------------------------------
@@ -330,7 +330,7 @@ def test_large_tiles(M, counts, N, K):
         got, kept, scales = F.gated_product(x, w, offsets=off, checkpoint=checkpoint)
         U.close(got[held.cuda()], ref[held], U.rounded(bound, ref)[held], "gated")
         if checkpoint == "bf16":
-            U.close(kept[held.cuda()], pre[held], U.rounded(poff, pre)[held], "pre")
+            U.close(U.half_values(kept, scales)[held], pre[held], U.half_step(pre[held], poff[held]), "pre")
         else:
             v = U.mx_values(kept, scales)
             exponent = scales.cpu().view(torch.uint8).double() - 127
@@ -341,7 +341,7 @@ def test_large_tiles(M, counts, N, K):
         I = N // 2
         w2, go = _normal(5, E, K, I, size=I ** -0.5), _normal(6, rows, K)
         d, doff, _ = _product_gpu(go, w2, o, True)
-        values = kept.cpu().double() if scales is None else U.mx_values(kept, scales)
+        values = (U.half_values if checkpoint == "bf16" else U.mx_values)(kept, scales)
         gref, gbound, act, abound = U.gated_backward(d, doff, values)
         gp, again = F.gated_product_backward(go, w2, kept, scales, offsets=off)
         U.close(gp[held.cuda()], gref[held], U.rounded(gbound, gref)[held], "grad_pre")
@@ -489,7 +489,8 @@ def test_binding_refusals(M):
                  lambda: F.expert_product(x.view(-1)[8:8 + 4 * 64].view(4, 64)[:, :32], w1, offsets=off),
                  lambda: F.expert_product(x.view(-1)[4:4 + 4 * 64].view(4, 64), w1, offsets=off),
                  lambda: F.gated_product(x, w1[:, :31].contiguous(), offsets=off),
-                 lambda: F.gated_product_backward(x, w2, saved.pre[:5], offsets=off),
+                 lambda: F.gated_product_backward(x, w2, saved.pre[:5], saved.pre_scales, offsets=off),
+                 lambda: F.gated_product_backward(x, w2, saved.pre.to(BF), saved.pre_scales, offsets=off),
                  lambda: F.gated_product_backward(x, w2, saved.pre, scales, offsets=off),
                  lambda: F.product_weight_grad(x, y[:5], offsets=off), lambda: F.product_weight_grad(x, y, offsets=off[:1]),
                  lambda: F.expert_ffn_backward(y, saved._replace(x=x[:, :32].contiguous()), w1, w2, offsets=off),
