@@ -12,6 +12,15 @@
 // along k (an operand's row after another, k next to k) or across it (a k
 // after another).  An operand across k goes into LDS as it lies and is turned
 // by the transposing LDS read.
+//
+// The matrix cores bound large calls: 8192^3 takes 772 us along k, 784 across
+// (rows times weights) and 786 (weights' gradient), 1.4 PFLOP/s, with the
+// cores busy two thirds of the cycles at 1.8 GHz and no LDS bank conflict.
+// Ragged experts lose a fifth of that to whole tiles of 256 CUs, the weights'
+// gradient of few rows to its stores; memory bounds a few rows an expert (5.9
+// TB/s of weights). Two workgroups a CU of 256 x 128 tiles, 32 of k a stage in
+// three of them, overlap one's stores with the other's products, but take 926
+// to 1080 us for 8192^3 and no less for the gradient of 32 experts of 512 rows.
 #include <algorithm>
 #include <cmath>
 
@@ -600,7 +609,11 @@ struct Heights<S, A, B, MORE...> {
 template <typename... S>
 using Finder = typename Heights<S...>::Finder;
 
-constexpr float kEdgeRows = 24.0f; // a tile's beginning and end take as long as this many of its rows
+// A tile's beginning and end take as long as about this many of its rows (one
+// round of 4096^3, 103 us, is as long as a quarter of the four rounds of 8192 x
+// 8192 x 4096).  Heights of up to 320 rows against 256 only: 8191 rows over 8
+// experts, gated backward 178 us against 261, forward 279 against 314.
+constexpr float kEdgeRows = 24.0f;
 
 // Rows before the first expert's first and from the last one's last on become
 // zeros, a part of them by each workgroup.

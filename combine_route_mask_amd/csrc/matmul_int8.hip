@@ -329,6 +329,7 @@ __global__ __launch_bounds__(S::THREADS, 2) void matmul_tile_kernel(moe_ep_matmu
     // this tile's and the next one's
     __shared__ __align__(16) uint8_t scales[2][tile_scales<S, MORE...>()];
     constexpr int TALL = largest(S::BM, MORE::BM...), BM = TALL > 256 ? 256 : TALL;
+    // a tile's beginning and end take about as long as 76 rows
     const std::conditional_t<BM == TALL, TileFinder<BM>, TileFinder<BM, TALL>> find(a, ntiles, 76.0f);
     int slot = (int)(blockIdx.x >> 3);
     Tile t = find.tile(a, slot);
