@@ -165,7 +165,6 @@ int check_params(const moe_ep_params *pp, Layout *lay)
     return MOE_EP_OK;
 }
 
-
 bool live_handle(const moe_ep_handle *h)
 {
     std::lock_guard<std::mutex> lk(g_handles_mu);

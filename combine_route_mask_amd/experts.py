@@ -154,6 +154,11 @@ def _empty(shape, strides, dtype, dev):
     return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
 
 
+def _new(shape, dtype, dev):
+    """A contiguous tensor of any shape."""
+    return _empty(shape, (shape[1], 1), dtype, dev) if len(shape) == 2 else torch.empty(shape, dtype=dtype, device=dev)
+
+
 _device_now = torch._C._cuda_getDevice
 _stream_now = torch._C._cuda_getCurrentRawStream
 

@@ -17,7 +17,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .experts import (_call, _device, _device_now, _empty, _flat, _no_grad, _On, _refuse, _row_type, _whole, _written)
+from .experts import (_call, _device, _device_now, _empty, _flat, _new, _no_grad, _On, _refuse, _row_type, _whole,
+                      _written)
 from .moe_ep import _need, lib
 
 SAVE_NONE, SAVE_HALF, SAVE_MXFP8 = 0, 1, 2
@@ -82,7 +83,7 @@ def _experts(weight, name, dev, dtype, offsets):
 def _out(out, name, dev, dtype, shape):
     """A given output, checked, or a new one."""
     if out is None:
-        return _empty(shape, (shape[1], 1), dtype, dev) if len(shape) == 2 else torch.empty(shape, dtype=dtype, device=dev)
+        return _new(shape, dtype, dev)
     _flat(out, name, dev, dtype, shape)
     _written(out)
     return out

@@ -7,13 +7,12 @@ follow the rules of ``experts``.
 """
 from __future__ import annotations
 
-import math
 import struct
 from typing import NamedTuple
 
 import torch
 
-from .experts import _call, _device, _device_now, _empty, _flat, _no_grad, _On, _refuse, _row_type, _whole, _written
+from .experts import _call, _device, _device_now, _flat, _new, _no_grad, _On, _refuse, _row_type, _whole, _written
 from .moe_ep import _need, lib
 
 MAX_ROUTED_EXPERTS = 4096  # MOE_EP_MAX_ROUTED_EXPERTS
@@ -55,7 +54,7 @@ def _shape(logits, top_k):
         _refuse(f"experts must be in [1, {MAX_ROUTED_EXPERTS}], got {E}")
     if not 1 <= top_k <= min(64, E):
         _refuse(f"top_k must be in [1, 64] and at most the {E} experts, got {top_k}")
-    return E, math.prod(logits.shape[:-1]), (*logits.shape[:-1], top_k)
+    return E, logits.numel() // E, (*logits.shape[:-1], top_k)
 
 
 def _route(logits, top_k, renormalize, scale, ids, weights, stream):
@@ -67,12 +66,12 @@ def _route(logits, top_k, renormalize, scale, ids, weights, stream):
     E, T, shape = _shape(logits, top_k)
     _flat(logits, "logits", dev, logits.dtype, logits.shape)
     if ids is None:
-        ids = torch.empty(shape, dtype=torch.int32, device=dev)
+        ids = _new(shape, torch.int32, dev)
     else:
         _flat(ids, "ids", dev, torch.int32, shape)
         _written(ids)
     if weights is None:
-        weights = torch.empty(shape, dtype=torch.float32, device=dev)
+        weights = _new(shape, torch.float32, dev)
     else:
         _flat(weights, "weights", dev, torch.float32, shape)
         _written(weights)
@@ -84,8 +83,8 @@ def _route(logits, top_k, renormalize, scale, ids, weights, stream):
 def route_top_k_backward(logits, ids, grad_weights, *, renormalize: bool = True, scale: float = 1.0, out=None,
                          stream=None):
     """Gradient of ``route_top_k``'s weights for the logits [..., E], in
-    their type; ``ids`` as the router chose them, ``grad_weights`` fp32
-    [..., k]."""
+    their type; ``ids`` as the router chose them (an id once a token),
+    ``grad_weights`` fp32 [..., k]."""
     _no_grad(logits, grad_weights, out)
     dev = _device(logits, "logits")
     if stream is not None or dev.index != _device_now():
@@ -100,7 +99,7 @@ def route_top_k_backward(logits, ids, grad_weights, *, renormalize: bool = True,
     _flat(ids, "ids", dev, torch.int32, shape)
     _flat(grad_weights, "grad_weights", dev, torch.float32, shape)
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        out = _new(logits.shape, logits.dtype, dev)
     else:
         _flat(out, "out", dev, logits.dtype, logits.shape)
         _written(out)
