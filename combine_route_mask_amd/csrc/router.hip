@@ -1,8 +1,10 @@
 // gfx950 kernels of the router: the largest logits of each token with their
 // softmax weights, and the gradient of the weights for the logits.  Up to 512
-// experts 16 or 64 lanes hold a token's logits in registers, a few consecutive
-// ones each; beyond, a wave holds them in LDS.  Instructions bound large calls
-// (a round for each place), the launch small ones.
+// experts 16 lanes (more than 16 places: 64) hold a token's logits in registers;
+// beyond, a wave holds them in LDS.  Instructions bound large calls (a sort of
+// each lane's, then a round for each place: 32768 tokens of 256 experts, 8
+// places, fp32 12.1 us, bf16 8.5; the gradient 9.7, 3.5 TB/s), the launch small
+// ones.
 #include <type_traits>
 
 #include "ffn_internal.h"
@@ -83,6 +85,60 @@ __device__ __forceinline__ void store_logits(void *base, int64_t row, int i, int
             store_logit<T>(base, row + i + v, x[v]);
 }
 
+// Logit v of a lane where LANES lanes share a token's: fours in turn.
+template <int LANES, int V>
+__device__ __forceinline__ int spread(int lane, int v)
+{
+    return V < 4 ? lane : 4 * (v / 4 * LANES + lane) + v % 4;
+}
+
+template <typename T, int LANES, int V>
+__device__ __forceinline__ void load_spread(const void *base, int64_t row, int lane, int E, float other, float (&x)[V])
+{
+    static_assert(V == 1 || V % 4 == 0);
+    constexpr int N = V < 4 ? 1 : 4;
+#pragma unroll
+    for (int v = 0; v < V; v += N) {
+        float f[N];
+        load_logits<T, N>(base, row, spread<LANES, V>(lane, v), E, other, f);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            x[v + i] = f[i];
+    }
+}
+
+template <typename T, int LANES, int V>
+__device__ __forceinline__ void store_spread(void *base, int64_t row, int lane, int E, const float (&x)[V])
+{
+    constexpr int N = V < 4 ? 1 : 4;
+#pragma unroll
+    for (int v = 0; v < V; v += N) {
+        float f[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            f[i] = x[v + i];
+        store_logits<T, N>(base, row, spread<LANES, V>(lane, v), E, f);
+    }
+}
+
+// A wave's accesses of LDS before are done before those behind.
+__device__ __forceinline__ void wave_order()
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#endif
+}
+
+// Smallest value of each 16 consecutive lanes, in all of them.
+__device__ __forceinline__ uint32_t min16(uint32_t x)
+{
+    x = min(x, dpp<kDppXor1>(x));
+    x = min(x, dpp<kDppXor2>(x));
+    x = min(x, dpp<kDppMirror8>(x));
+    return min(x, dpp<kDppMirror16>(x));
+}
+
 // Over the LANES (16 or 64) lanes of a token, in all of them.  Of a wave: rows of
 // 16 hand theirs to the next, and the last lane has it; no LDS, whose latency
 // each round would wait for.
@@ -110,15 +166,6 @@ __device__ __forceinline__ float token_sum(float x)
     return x + dpp<kDppMirror16>(x);
 }
 
-// The value of the token's lane j.
-template <int LANES, typename X>
-__device__ __forceinline__ X of_lane(X x, int j)
-{
-    if (LANES == 64) // j is the same in all lanes
-        return __builtin_bit_cast(X, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), j));
-    return __shfl(x, j, 16);
-}
-
 // A logit as a number that orders like it, 0 where it is never chosen.
 __device__ __forceinline__ uint32_t order_of(float x)
 {
@@ -131,14 +178,14 @@ __device__ __forceinline__ float value_of(uint32_t k)
     return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// Each lane sorts its V logits once (neighbours change places only where the
+// More than 16 places: each lane sorts its V logits once (neighbours change places only where the
 // later one is larger, so that equal ones keep their order); in a round the
 // lanes' first ones compete, the lowest lane wins of equal ones and moves up.
 // Lane j keeps place j.
-template <typename T, int LANES, int V>
+template <typename T, int V>
 __global__ __launch_bounds__(256) void route_lanes_kernel(moe_ep_route_args a)
 {
-    constexpr int PER = 256 / LANES;
+    constexpr int LANES = 64, PER = 256 / LANES;
     const int E = a.num_experts, lane = threadIdx.x % LANES;
     for (int64_t t0 = (int64_t)blockIdx.x * PER; t0 < a.tokens; t0 += (int64_t)gridDim.x * PER) {
         const int64_t mine = t0 + threadIdx.x / LANES, t = min(mine, a.tokens - 1); // lanes without a token do the last's again
@@ -169,8 +216,8 @@ __global__ __launch_bounds__(256) void route_lanes_kernel(moe_ep_route_args a)
         for (int j = 0; j < a.top_k; ++j) {
             const uint32_t best = token_max<LANES>(key[0]);
             const uint64_t ties = __ballot(key[0] == best);
-            const int winner = __builtin_ctzll(LANES == 64 ? ties : ties >> (threadIdx.x & 48));
-            const int chosen = of_lane<LANES>(id[0], winner);
+            const int winner = __builtin_ctzll(ties);
+            const int chosen = __builtin_amdgcn_readlane(id[0], winner);
             if (j == 0)
                 top = best;
             if (lane == j) {
@@ -204,11 +251,160 @@ __global__ __launch_bounds__(256) void route_lanes_kernel(moe_ep_route_args a)
     }
 }
 
+// A logit and its expert as one number, so that the larger one wins: of equal
+// logits the lower expert's.  0 where it is never chosen.  fp32: a double in
+// [1, 2) with the logit's order in the first 32 bits of its fraction, of which
+// one instruction takes the larger; across lanes 32 bits at a time, the order
+// and then the expert, cost less.  (32768 tokens of 256 experts: 12.0 us;
+// doubles across lanes too 12.2, pairs of words in the sort too 14.2.)
+template <typename T>
+struct Ranked {
+    double w;
+    struct Head {
+        uint32_t order, id;
+        __device__ __forceinline__ bool any() const { return order != 0; }
+        __device__ __forceinline__ bool operator==(const Head &o) const { return order == o.order && id == o.id; }
+        __device__ __forceinline__ Head best() const
+        {
+            const uint32_t k = max16(order);
+            return {k, min16(order == k ? id : 0xFFFFFFFFu)};
+        }
+        __device__ __forceinline__ int expert() const { return (int)id; }
+        __device__ __forceinline__ float value() const { return value_of(order); }
+    };
+    static __device__ __forceinline__ Ranked of(float x, int id)
+    {
+        const uint32_t k = order_of(x);
+        const uint64_t u = (uint64_t)(0x3FF00000u | k >> 12) << 32 | (k << 20 | (0xFFFFFu - (uint32_t)id));
+        return {k ? __builtin_bit_cast(double, u) : 0.0};
+    }
+    __device__ __forceinline__ Head head() const
+    {
+        const uint64_t u = __builtin_bit_cast(uint64_t, w);
+        return {(uint32_t)(u >> 20), 0xFFFFFu - ((uint32_t)u & 0xFFFFFu)};
+    }
+    __device__ __forceinline__ Ranked larger(const Ranked &o) const
+    {
+        double y; // the builtin would first turn signalling NaNs into quiet ones
+        asm("v_max_f64 %0, %1, %2" : "=v"(y) : "v"(w), "v"(o.w));
+        return {y};
+    }
+    __device__ __forceinline__ Ranked smaller(const Ranked &o) const
+    {
+        double y;
+        asm("v_min_f64 %0, %1, %2" : "=v"(y) : "v"(w), "v"(o.w));
+        return {y};
+    }
+};
+
+template <>
+struct Ranked<Bf16> { // order and expert, 16 bits each
+    uint32_t w;
+    struct Head {
+        uint32_t w;
+        __device__ __forceinline__ bool any() const { return w != 0; }
+        __device__ __forceinline__ bool operator==(const Head &o) const { return w == o.w; }
+        __device__ __forceinline__ Head best() const { return {max16(w)}; }
+        __device__ __forceinline__ int expert() const { return (int)(0xFFFFu - (w & 0xFFFFu)); }
+        __device__ __forceinline__ float value() const { return __uint_as_float(__float_as_uint(value_of(w)) & 0xFFFF0000u); }
+    };
+    static __device__ __forceinline__ Ranked of(float x, int id)
+    {
+        const uint32_t k = order_of(x) & 0xFFFF0000u; // not 0 for a number
+        return {k ? k | (0xFFFFu - (uint32_t)id) : 0};
+    }
+    __device__ __forceinline__ Head head() const { return {w}; }
+    __device__ __forceinline__ Ranked larger(const Ranked &o) const { return {max(w, o.w)}; }
+    __device__ __forceinline__ Ranked smaller(const Ranked &o) const { return {min(w, o.w)}; }
+};
+
+// Batcher's network, largest first.
+template <int V, typename R>
+__device__ __forceinline__ void sort_down(R (&r)[V])
+{
+#pragma unroll
+    for (int p = 1; p < V; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int i = 0; i + k < V; ++i)
+                if (i >= k % p && (i - k % p) / k % 2 == 0 && i / (2 * p) == (i + k) / (2 * p)) {
+                    const R a = r[i], b = r[i + k];
+                    r[i] = a.larger(b);
+                    r[i + k] = a.smaller(b);
+                }
+}
+
+// Sixteen lanes a token, four tokens a wave.  A lane sorts its logits once and
+// keeps them in LDS, in its own column; in a round the lanes' first ones
+// compete, and the winner's lane reads its next.  Lane j keeps place j.  (A lane
+// of 64 with four or eight logits, sorted and moved up in registers, as for
+// more places: 32768 tokens of 256 experts 17.6 us against 12.1, bf16 17.3
+// against 8.5; 16384 of 384 bf16 16.0 / 9.2; only one place of 384 is faster so,
+// 8.7 / 11.7.)
+template <typename T, int V>
+__global__ __launch_bounds__(256) void route_sorted_kernel(moe_ep_route_args a)
+{
+    typedef Ranked<T> R;
+    __shared__ typename R::Head list[V + 1][256];
+    const int E = a.num_experts, lane = threadIdx.x & 15;
+    for (int64_t t0 = (int64_t)blockIdx.x * 16; t0 < a.tokens; t0 += (int64_t)gridDim.x * 16) {
+        const int64_t mine = t0 + threadIdx.x / 16, t = min(mine, a.tokens - 1); // lanes without a token do the last's again
+        float x[V];
+        load_spread<T, 16, V>(a.logits, t * E, lane, E, -INFINITY, x);
+        R r[V];
+        uint32_t bad = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            r[v] = R::of(x[v], spread<16, V>(lane, v));
+            bad |= x[v] != x[v];
+        }
+        sort_down<V>(r);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            list[v][threadIdx.x] = r[v].head();
+        list[V][threadIdx.x] = {}; // never chosen
+        auto head = r[0].head();
+        decltype(head) top = {}, kept = {};
+        int at = 0;
+        for (int j = 0; j < a.top_k; ++j) {
+            const auto best = head.best();
+            if (j == 0)
+                top = best;
+            if (lane == j)
+                kept = best;
+            at += head.any() && head == best; // no further than the last
+            head = list[at][threadIdx.x];
+        }
+        const int place = kept.any() ? kept.expert() : E;
+        const float peak = top.value();
+        const float e = kept.any() ? expf(kept.value() - peak) : 0.0f;
+        float total = e;
+        if (!a.renormalize) {
+            total = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                total += expf(x[v] - peak);
+        }
+        total = token_sum<16>(total);
+        const bool nan = token_max<16>(bad) != 0;
+        if (lane < a.top_k && mine < a.tokens) {
+            a.ids[t * a.top_k + lane] = place;
+            a.weights[t * a.top_k + lane] = place == E ? 0.0f : nan ? nan_value() : a.scale * (e / total);
+        }
+    }
+}
+
+// The chosen experts' places go through LDS, a wave's own part of it.  (32768
+// tokens of 256 experts, 8 places: 9.7 us, a wave a token 12.9; over all experts
+// 14.5, with the places compared in registers 18.5.)
 template <typename T, int LANES, int V>
 __global__ __launch_bounds__(256) void route_lanes_backward_kernel(moe_ep_route_grad_args a)
 {
     constexpr int PER = 256 / LANES;
+    __shared__ __align__(16) float places[256 * V];
     const int E = a.num_experts, lane = threadIdx.x % LANES;
+    float *place = places + threadIdx.x / LANES * (LANES * V);
     for (int64_t t0 = (int64_t)blockIdx.x * PER; t0 < a.tokens; t0 += (int64_t)gridDim.x * PER) {
         const int64_t mine = t0 + threadIdx.x / LANES, t = min(mine, a.tokens - 1);
         int id = E;
@@ -222,11 +418,14 @@ __global__ __launch_bounds__(256) void route_lanes_backward_kernel(moe_ep_route_
         float x[V];
         float top = chosen;
         if (!a.renormalize) {
-            load_logits<T, V>(a.logits, t * E, lane * V, E, -INFINITY, x);
+            load_spread<T, LANES, V>(a.logits, t * E, lane, E, -INFINITY, x);
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 top = fmaxf(top, x[v]);
         }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            place[spread<LANES, V>(lane, v)] = 0.0f;
         const uint32_t peak_key = token_max<LANES>(order_of(top));
         const float peak = peak_key ? value_of(peak_key) : 0.0f;
         const float e = held ? expf(chosen - peak) : 0.0f;
@@ -243,24 +442,20 @@ __global__ __launch_bounds__(256) void route_lanes_backward_kernel(moe_ep_route_
         const float by = total != 0.0f ? 1.0f / total : 0.0f;
         const float mean = token_sum<LANES>(held ? e * by * g : 0.0f);
         // what an expert's place gives: the gradient, or its part of it
-        const float gives = a.renormalize ? a.scale * (e * by) * (g - mean) : g;
+        wave_order();
+        if (held)
+            place[id] = a.renormalize ? a.scale * (e * by) * (g - mean) : g;
+        wave_order();
         float d[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            d[v] = 0.0f;
-        for (int j = 0; j < a.top_k; ++j) {
-            const int at = of_lane<LANES>(id, j) - lane * V;
-            const float y = of_lane<LANES>(gives, j);
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                d[v] = at == v ? y : d[v];
-        }
-        if (!a.renormalize)
-#pragma unroll
-            for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
+            d[v] = place[spread<LANES, V>(lane, v)];
+            if (!a.renormalize)
                 d[v] = a.scale * (x[v] * by) * (d[v] - mean);
+        }
         if (mine < a.tokens)
-            store_logits<T, V>(a.grad_logits, t * E, lane * V, E, d);
+            store_spread<T, LANES, V>(a.grad_logits, t * E, lane, E, d);
+        wave_order();
     }
 }
 
@@ -391,11 +586,15 @@ template <typename F>
 bool with_lanes(int experts, int top_k, F f)
 {
     using std::integral_constant;
-    if (experts <= 64 && top_k <= 16) {
+    if (experts <= 512 && top_k <= 16) {
         if (experts <= 16)
             f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-        else
+        else if (experts <= 64)
             f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+        else if (experts <= 256)
+            f(integral_constant<int, 16>{}, integral_constant<int, 16>{});
+        else
+            f(integral_constant<int, 16>{}, integral_constant<int, 32>{});
     } else if (experts <= 64) {
         f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
     } else if (experts <= 256) {
@@ -413,7 +612,11 @@ hipError_t route_launch(const moe_ep_route_args &a, hipStream_t s)
 {
     if (!with_lanes(a.num_experts, a.top_k, [&](auto lanes, auto logits) {
             constexpr int L = decltype(lanes)::value, V = decltype(logits)::value;
-            hipLaunchKernelGGL((route_lanes_kernel<T, L, V>), tokens_grid((a.tokens + 256 / L - 1) / (256 / L)), dim3(256), 0, s, a);
+            const dim3 grid = tokens_grid((a.tokens + 256 / L - 1) / (256 / L));
+            if constexpr (L == 16)
+                hipLaunchKernelGGL((route_sorted_kernel<T, V>), grid, dim3(256), 0, s, a);
+            else
+                hipLaunchKernelGGL((route_lanes_kernel<T, V>), grid, dim3(256), 0, s, a);
         }))
         hipLaunchKernelGGL(route_kernel<T>, tokens_grid(a.tokens), dim3(64), 4 * a.num_experts, s, a);
     return hipGetLastError();
@@ -422,11 +625,7 @@ hipError_t route_launch(const moe_ep_route_args &a, hipStream_t s)
 template <typename T>
 hipError_t route_backward_launch(const moe_ep_route_grad_args &a, hipStream_t s)
 {
-    // Over the chosen experts alone little is computed, and a wave's LDS takes the
-    // few places sooner than registers do (32768 tokens, 256 experts, 8 places:
-    // 13.0 / 15.1 us; over all experts 26.3 / 18.7).
-    const bool lds = a.renormalize && a.num_experts > 64;
-    if (lds || !with_lanes(a.num_experts, a.top_k, [&](auto lanes, auto logits) {
+    if (!with_lanes(a.num_experts, a.top_k, [&](auto lanes, auto logits) {
             constexpr int L = decltype(lanes)::value, V = decltype(logits)::value;
             hipLaunchKernelGGL((route_lanes_backward_kernel<T, L, V>), tokens_grid((a.tokens + 256 / L - 1) / (256 / L)),
                                dim3(256), 0, s, a);
