@@ -1,10 +1,10 @@
 // gfx950 kernels of the router: the largest logits of each token with their
 // softmax weights, and the gradient of the weights for the logits.  Up to 512
-// experts 16 lanes (more than 16 places: 64) hold a token's logits in registers;
-// beyond, a wave holds them in LDS.  Instructions bound large calls (a sort of
-// each lane's, then a round for each place: 32768 tokens of 256 experts, 8
-// places, fp32 12.1 us, bf16 8.5; the gradient 9.7, 3.5 TB/s), the launch small
-// ones.
+// experts 16 lanes (more than 16 places, or few tokens: 64) hold a token's logits
+// in registers; beyond, a wave holds them in LDS.  Instructions bound large
+// calls (a sort of each lane's, then a round for each place: 32768 tokens of 256
+// experts, 8 places, fp32 12.1 us, bf16 8.5; the gradient 9.7, 3.5 TB/s), the
+// launch small ones.
 #include <type_traits>
 
 #include "ffn_internal.h"
@@ -178,10 +178,10 @@ __device__ __forceinline__ float value_of(uint32_t k)
     return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// More than 16 places: each lane sorts its V logits once (neighbours change places only where the
-// later one is larger, so that equal ones keep their order); in a round the
-// lanes' first ones compete, the lowest lane wins of equal ones and moves up.
-// Lane j keeps place j.
+// More than 16 places, or few tokens: each lane sorts its V logits once
+// (neighbours change places only where the later one is larger, so that equal
+// ones keep their order); in a round the lanes' first ones compete, the lowest
+// lane wins of equal ones and moves up.  Lane j keeps place j.
 template <typename T, int V>
 __global__ __launch_bounds__(256) void route_lanes_kernel(moe_ep_route_args a)
 {
@@ -582,11 +582,15 @@ inline dim3 tokens_grid(int64_t tokens)
 }
 
 // Calls f(lanes, logits a lane) for the kernels in registers, or returns false.
+// A few tokens of many experts leave SIMDs without a wave: 64 lanes a token then
+// (in a graph, 64 lanes / 16, 256 experts fp32: one token 2.8 / 3.8 us, 2048
+// 3.5 / 4.1, 4096 4.3 / 4.1, 8192 6.2 / 4.8; 384 bf16: 3.4 / 4.7, 4.8 / 5.1, 6.5 /
+// 5.1, 9.8 / 6.1; 64 fp32: 2.3 / 2.4, 2.9 / 2.7, 3.4 / 2.8, 4.6 / 2.9).
 template <typename F>
-bool with_lanes(int experts, int top_k, F f)
+bool with_lanes(int64_t tokens, int experts, int top_k, F f)
 {
     using std::integral_constant;
-    if (experts <= 512 && top_k <= 16) {
+    if (experts <= 512 && top_k <= 16 && (experts <= 64 || tokens > 2048)) {
         if (experts <= 16)
             f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
         else if (experts <= 64)
@@ -610,7 +614,7 @@ bool with_lanes(int experts, int top_k, F f)
 template <typename T>
 hipError_t route_launch(const moe_ep_route_args &a, hipStream_t s)
 {
-    if (!with_lanes(a.num_experts, a.top_k, [&](auto lanes, auto logits) {
+    if (!with_lanes(a.tokens, a.num_experts, a.top_k, [&](auto lanes, auto logits) {
             constexpr int L = decltype(lanes)::value, V = decltype(logits)::value;
             const dim3 grid = tokens_grid((a.tokens + 256 / L - 1) / (256 / L));
             if constexpr (L == 16)
@@ -625,7 +629,7 @@ hipError_t route_launch(const moe_ep_route_args &a, hipStream_t s)
 template <typename T>
 hipError_t route_backward_launch(const moe_ep_route_grad_args &a, hipStream_t s)
 {
-    if (!with_lanes(a.num_experts, a.top_k, [&](auto lanes, auto logits) {
+    if (!with_lanes(a.tokens, a.num_experts, a.top_k, [&](auto lanes, auto logits) {
             constexpr int L = decltype(lanes)::value, V = decltype(logits)::value;
             hipLaunchKernelGGL((route_lanes_backward_kernel<T, L, V>), tokens_grid((a.tokens + 256 / L - 1) / (256 / L)),
                                dim3(256), 0, s, a);

@@ -70,7 +70,8 @@ def _error(logits, E):
 
 SHAPES = [(1, 1, 1), (1, 256, 8), (5, 4, 4), (3, 7, 2), (64, 64, 64), (33, 65, 6), (100, 130, 8), (17, 512, 16),
           (9, 1000, 3), (4, 4096, 64), (1025, 32, 4), (3000, 8, 2), (2, 257, 1),
-          (5, 200, 40), (7, 500, 17), (18, 260, 16), (16, 256, 16), (31, 16, 16), (6, 17, 17)]
+          (5, 200, 40), (7, 500, 17), (18, 260, 16), (16, 256, 16), (31, 16, 16), (6, 17, 17),
+          (2051, 130, 8), (2049, 300, 16)]
 
 
 @pytest.mark.parametrize("renormalize", [True, False])
