@@ -16,7 +16,8 @@ stream must be ordered by the caller.  Calls may be captured into a HIP
 graph.  A refused call raises ``MoeEpArgError`` (or ``MoeEpError`` with the
 library's code) and launches nothing.  Under grad mode an input that asks for
 a gradient is refused where the operator has none for it, and so is a given
-output that does.
+output that does.  No operator has a forward-mode derivative: a tensor with a
+tangent is refused, also under ``torch.no_grad()``, which leaves tangents on.
 """
 from __future__ import annotations
 
@@ -25,6 +26,7 @@ import struct
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from .moe_ep import ERR_INVALID_ARG, MoeEpArgError, _check, _need, lib
 
@@ -131,8 +133,17 @@ def _row_type(t, name):
 _written = torch.autograd.graph.increment_version  # of a given output: autograd then knows what it saved is gone
 
 
+def _no_tangent(*tensors):
+    """A dual tensor does not ask for a gradient, and its tangent would be lost."""
+    if forward_ad._current_level >= 0:  # a dual level; outside one unpack_dual alone takes 0.7 us a tensor
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                _refuse("this call has no forward-mode derivative: unpack its dual tensors")
+
+
 def _no_grad(*tensors):
     """Without a gradient of its own, an operator refuses to drop one."""
+    _no_tangent(*tensors)
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
@@ -219,6 +230,7 @@ def expert_sort(ids, rows, experts_per_rank: int, *, scales=None, capacity: Opti
     Differentiable in ``rows`` (bf16 or fp32; not with ``quantize``, ``out``
     or ``stream``: autograd orders its work by the current stream); the rows
     behind the last pair are then zeros.  ``scales`` have no gradient."""
+    _no_tangent(rows)
     _no_grad(scales, out, out_scales)
     if rows.requires_grad and torch.is_grad_enabled():
         _need(not quantize and out is None and stream is None and rows.dtype in _ROW_TYPES,
@@ -330,6 +342,7 @@ def expert_unsort(position, rows, weights=None, *, out=None, keep_empty: bool = 
 
     Differentiable in ``rows`` and ``weights`` (without ``out`` or
     ``stream``)."""
+    _no_tangent(rows, weights)
     _no_grad(out)
     if (rows.requires_grad or (weights is not None and weights.requires_grad)) and torch.is_grad_enabled():
         _need(out is None and not keep_empty and stream is None,

@@ -17,8 +17,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .experts import (_call, _device, _device_now, _empty, _flat, _new, _no_grad, _On, _refuse, _row_type, _whole,
-                      _written)
+from .experts import (_call, _device, _device_now, _empty, _flat, _new, _no_grad, _no_tangent, _On, _refuse, _row_type,
+                      _whole, _written)
 from .moe_ep import _need, lib
 
 SAVE_NONE, SAVE_HALF, SAVE_MXFP8 = 0, 1, 2
@@ -304,6 +304,7 @@ def expert_ffn(x, w1, w2, *, offsets=None, checkpoint: str = "bf16", out=None, s
     x and of the first product: "bf16", x itself and the product in 16 bits, or
     "mxfp8" (half the memory, H and I multiples of 32; the gradients are then
     those at the rounded values)."""
+    _no_tangent(x, w1, w2)
     _no_grad(out)
     if torch.is_grad_enabled() and (x.requires_grad or w1.requires_grad or w2.requires_grad):
         _need(out is None and stream is None, "only a block into a new tensor, on the current stream, has a gradient")

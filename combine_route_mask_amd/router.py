@@ -12,7 +12,8 @@ from typing import NamedTuple
 
 import torch
 
-from .experts import _call, _device, _device_now, _flat, _new, _no_grad, _On, _refuse, _row_type, _whole, _written
+from .experts import (_call, _device, _device_now, _flat, _new, _no_grad, _no_tangent, _On, _refuse, _row_type, _whole,
+                      _written)
 from .moe_ep import _need, lib
 
 MAX_ROUTED_EXPERTS = 4096  # MOE_EP_MAX_ROUTED_EXPERTS
@@ -38,6 +39,7 @@ def route_top_k(logits, top_k: int, *, renormalize: bool = True, scale: float = 
     weight 0.  A row with a NaN or +infinity has NaN weights.
 
     Differentiable in ``logits`` (without given outputs or ``stream``)."""
+    _no_tangent(logits)
     _no_grad(weights)
     if logits.requires_grad and torch.is_grad_enabled():
         _need(ids is None and weights is None and stream is None,
