@@ -211,6 +211,8 @@ def gated_product_backward(grad_out, weight, pre, pre_scales, *, offsets=None, n
     """The gradient grad_out [M, N] of the block's second product, weights
     [E, N, I], taken through it and the activation at ``gated_product``'s
     pre: (grad_pre [M, 2 I], the activation rows [M, I] again or None)."""
+    if pre is None or pre_scales is None:
+        _refuse("pre and pre_scales are what gated_product gives with a checkpoint, and without one it keeps none")
     _no_grad(grad_out, weight, pre)
     dev = _device(grad_out, "grad_out")
     if stream is not None or dev.index != _device_now():
