@@ -21,10 +21,8 @@
 // TB/s of weights). Two workgroups a CU of 256 x 128 tiles, 32 of k a stage in
 // three of them, overlap one's stores with the other's products, but take 926
 // to 1080 us for 8192^3 and no less for the gradient of 32 experts of 512 rows.
-#include <algorithm>
-#include <cmath>
-
 #include "ffn_internal.h"
+#include "product_shapes.h"
 #include "rows.h"
 #include "tiles.h"
 
@@ -671,64 +669,10 @@ hipError_t product_launch(const Job &a, hipStream_t s)
     return hipGetLastError();
 }
 
-// Which shape: the one that a model of the time of the busiest CU finds fastest,
-// from the number of tiles on 256 CUs and of 64-deep steps.  A step takes a
-// shape's workgroup `first` us alone on its CU (waits of LDS and barriers),
-// `more` us of a CU's time with others, `all` us of one of 256 where all
-// CUs are busy (the clock falls); a tile's beginning and end take `edge` us.
-// Fitted to, and checked against, each shape's time (us, best of the four and
-// the model's choice; rows x hidden x inter):
-//  - products: 1023 x 2064 x 1032 gated 26.2 (64 x 64) / 26.9 (128 x 64), down
-//    12.3 / 12.3 (128 x 128), through w1 23.6 / 23.6 (128 x 64); 64 x 4096 x 2048
-//    down 9.3 / 9.3 (64 x 64), others 12.7, 12.8, 19; 4000 x 4096 x 1024 through w1
-//    57 / 57 (256 x 256), others 117, 92, 69; 2000 rows over 16 experts x 2048 x 768
-//    gated 24.5 / 24.5 (128 x 64), others 30, 31, 33;
-//  - weights' gradient: 4000 rows of 2048 x 4096 66 / 66 (128 x 128), 256 x 256 85;
-//    8191 rows over 8 experts of 4096 x 4096 254 / 254 (256 x 256), 128 x 128 303;
-//    2000 rows over 16 of 2048 x 768 18 / 18 (128 x 128), 256 x 256 23, 64 x 64 30.
-// One to three more stages for the smaller shapes change nothing where a CU has
-// one workgroup and cost where it could have several.
-enum Shape { kTile64, kTile128x64, kTile128, kTile256 };
-
-struct ShapeTime {
-    int channels, rows;
-    float first, more, all, edge;
-};
-
-constexpr ShapeTime kShapeTimes[] = {{64, 64, 0.3f, 0.25f, 0.0f, 1.0f},
-                                     {128, 64, 0.42f, 0.365f, 0.0f, 1.5f},
-                                     {128, 128, 0.75f, 0.52f, 0.0f, 2.5f},
-                                     {256, 256, 1.0f, 1.0f, 1.65f, 9.0f}};
-
-// `tiles(shape)` are its tiles, `steps` those of one.
-template <typename F>
-Shape fastest_shape(float steps, F tiles)
-{
-    Shape best = kTile64;
-    float least = 0.0f;
-    for (const Shape s : {kTile64, kTile128x64, kTile128, kTile256}) {
-        const ShapeTime &t = kShapeTimes[s];
-        const float n = tiles(t), turns = std::ceil(n / 256.0f);
-        const float step = std::max(turns > 1.0f ? turns * t.more : t.first, t.all * n / 256.0f);
-        const float time = steps * step + turns * t.edge;
-        if (s == kTile64 || time < least) {
-            best = s;
-            least = time;
-        }
-    }
-    return best;
-}
-
 template <int EPI, bool ACROSS>
 hipError_t product_shape(const Job &a, hipStream_t s)
 {
-    const float rows = (float)a.num_rows / (float)a.num_experts;
-    // ragged experts have some tiles more than experts of the average
-    const float more = a.num_experts > 1 ? 1.1f : 1.0f;
-    const Shape shape = fastest_shape((float)((a.k + 63) / 64), [&](const ShapeTime &t) {
-        return more * (float)a.num_experts * std::ceil(rows / (float)t.rows) * (float)channel_tiles(a.n, t.channels);
-    });
-    switch (shape) {
+    switch (product_shape_of(a.num_rows, a.num_experts, a.n, a.k)) {
     case kTile64:
         if constexpr (EPI == kGated) // a wave needs two fragments of either half
             return product_launch<EPI, ACROSS, TileShape<1, 2, 4, 1, 4>, TileShape<1, 2, 4, 2, 3>>(a, s);
@@ -899,11 +843,7 @@ hipError_t launch_gated_product_backward(const moe_ep_gated_grad_args &a, hipStr
 
 hipError_t launch_product_weight_grad(const moe_ep_weight_grad_args &a, hipStream_t s)
 {
-    const float rows = (float)a.num_rows / (float)a.num_experts;
-    const Shape shape = fastest_shape(std::ceil(rows / 64.0f), [&](const ShapeTime &t) {
-        return (float)a.num_experts * (float)channel_tiles(a.n, t.rows) * (float)channel_tiles(a.k, t.channels);
-    });
-    switch (shape) {
+    switch (weight_grad_shape_of(a.num_rows, a.num_experts, a.n, a.k)) {
     case kTile64: return weight_grad_launch<TileShape<2, 2, 2, 2, 3>>(a, s);
     case kTile128x64: return weight_grad_launch<TileShape<2, 2, 4, 2, 3>>(a, s);
     case kTile128: return weight_grad_launch<TileShape<2, 2, 4, 4, 2>>(a, s);

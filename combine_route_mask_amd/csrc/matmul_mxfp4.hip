@@ -8,6 +8,7 @@
 #include <algorithm>
 
 #include "ffn_internal.h"
+#include "product_shapes.h"
 #include "rows.h"
 #include "tiles.h"
 
@@ -345,24 +346,15 @@ hipError_t four_bit_launch(const moe_ep_four_bit_args &a, hipStream_t s)
     return hipGetLastError();
 }
 
-// Times in us, other side behind the stroke.  With at most two workgroups for
-// each CU four stages of two resident ones, else three of three: 8 rows over 8 of
-// 32 experts of 4096 x 7168 (512 workgroups) 27.5 / 35.8, 64 rows over 32 of
-// 4096 x 2048 28.5 / 32.5, 64 over 64 of 2048 x 1024 16.7 / 19.9.  For 17 rows or
-// more stages of 64 (one workgroup a CU).  Where 64 channels a workgroup leave
-// CUs without one, 16 channels straight into registers: 16 rows, dense 7168 x
-// 2048, 7.9 / 10.
 template <typename T, bool GATED>
 hipError_t four_bit_shape(const moe_ep_four_bit_args &a, hipStream_t s)
 {
-    const int64_t rows = (a.num_rows + a.num_experts - 1) / a.num_experts, busy = std::min<int64_t>(a.num_rows, a.num_experts);
-    if (rows > 16)
-        return four_bit_launch<T, GATED, Stage<64, 3>>(a, s);
-    const int64_t groups = busy * channel_tiles(a.n, 64);
-    if (groups > 512)
-        return four_bit_launch<T, GATED, Stage<16, 3>>(a, s);
-    if (groups >= 256)
-        return four_bit_launch<T, GATED, Stage<16, 4>>(a, s);
+    switch (four_bit_shape_of(a.num_rows, a.num_experts, a.n)) {
+    case kRows64: return four_bit_launch<T, GATED, Stage<64, 3>>(a, s);
+    case kRows16Stages3: return four_bit_launch<T, GATED, Stage<16, 3>>(a, s);
+    case kRows16Stages4: return four_bit_launch<T, GATED, Stage<16, 4>>(a, s);
+    case kFew: break;
+    }
     const int ntiles = channel_tiles(GATED ? a.n / 2 : a.n, 16);
     const int64_t tiles = (int64_t)ntiles * a.num_experts;
     if (tiles > INT32_MAX)
