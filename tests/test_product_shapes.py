@@ -32,3 +32,45 @@ def test_choices(shapes):
     assert shapes.four_bit(128, 32, 4096) == "16 rows, 3 stages"
     assert shapes.four_bit(1, 0, 4096) == "few channels"
     assert shapes.four_bit(300, 4, 100) == "64 rows"
+
+
+def _row_tiles(counts, n):
+    """Heights of the row tiles of 256 channels that the device takes: of 128 to 320 rows at most what the CUs are done
+    with first, each expert's of even height in units of 64."""
+    channels, best = -(-n // 256), None
+    for most in (128, 192, 256, 320):
+        tiles = sum(-(-c // most) for c in counts)
+        time = (tiles * channels + 255) // 256 * (24 + sum(counts) / tiles)
+        if best is None or time < best[0]:
+            best = time, most
+    heights = set()
+    for c in filter(None, counts):
+        tiles, units = -(-c // best[1]), -(-c // 64)
+        for row in range(tiles):
+            heights.add(units // tiles + (row < units % tiles))
+    return heights
+
+
+def test_sizes_of_the_tile_tests(shapes):
+    """The GPU tests' sizes choose what they are there for."""
+    from tests import test_gpu_product_tiles as T
+    for counts, n, k in T.BF16_TILES:
+        rows, E = sum(counts) + T.BEFORE + T.BEHIND, len(counts)
+        assert shapes.product(rows, E, n, k) == shapes.product(rows, E, n // 64 * 64, k) == "256 x 256"
+        assert k // 64 > 2 * 2  # the loop over the two stages goes round
+    assert _row_tiles(T.BF16_TILES[0][0], T.BF16_TILES[0][1]) == {1, 2, 3, 4, 5}
+    taken = {(shapes.four_bit(M, E, N), K % 128 == 0) for M, E, N, K, _ in T.FOUR_BIT_TILES}
+    assert taken >= {(s, words) for s in ("16 rows, 4 stages", "16 rows, 3 stages") for words in (False, True)}
+
+
+def test_every_tile_has_a_test(shapes):
+    """The GPU tests together reach every tile of every product."""
+    from tests import test_gpu_ffn as A, test_gpu_matmul_mxfp4 as Q, test_gpu_product_tiles as T
+    bf16 = [(M, E, n, k) for M, E, n, k, _ in A.SHAPES]
+    bf16 += [(sum(c) + T.BEFORE + T.BEHIND, len(c), n, k) for c, n, k in T.BF16_TILES]
+    every = {"64 x 64", "128 x 64", "128 x 128", "256 x 256"}
+    assert {shapes.product(*s) for s in bf16} == every                                   # either order, the backward
+    assert {shapes.product(M, E, 2 * n, k) for M, E, n, k in bf16[:len(A.SHAPES)]} | {"256 x 256"} == every  # gated
+    assert {shapes.weight_grad(*s) for s in bf16} == every
+    four = {shapes.four_bit(M, E, N) for M, E, N, *_ in Q.SHAPES + T.FOUR_BIT_TILES}
+    assert four == {"few channels", "16 rows, 4 stages", "16 rows, 3 stages", "64 rows"}
