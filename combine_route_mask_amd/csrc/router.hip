@@ -395,6 +395,8 @@ __global__ __launch_bounds__(256) void route_sorted_kernel(moe_ep_route_args a)
     }
 }
 
+// Over the chosen experts the others' logits are not read (half of the bytes), so
+// a NaN among them does not reach the gradient.
 // The chosen experts' places go through LDS, a wave's own part of it.  (32768
 // tokens of 256 experts, 8 places: 9.7 us, a wave a token 12.9; over all experts
 // 14.5, with the places compared in registers 18.5.)

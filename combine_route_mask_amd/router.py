@@ -86,7 +86,9 @@ def route_top_k_backward(logits, ids, grad_weights, *, renormalize: bool = True,
                          stream=None):
     """Gradient of ``route_top_k``'s weights for the logits [..., E], in
     their type; ``ids`` as the router chose them (an id once a token),
-    ``grad_weights`` fp32 [..., k]."""
+    ``grad_weights`` fp32 [..., k].  With ``renormalize`` only the chosen
+    logits are read: a NaN among the others has no part in it.  Without, a
+    NaN or +infinity makes its row's gradient NaN."""
     _no_grad(logits, grad_weights, out)
     dev = _device(logits, "logits")
     if stream is not None or dev.index != _device_now():

@@ -551,6 +551,11 @@ int moe_ep_route_top_k(const moe_ep_route_args *args, void *stream);
  * 0 outside the softmax.  Places whose id is outside [0, num_experts) have no
  * part in it.  An id may appear once a token.  fp32 sums in an order that the
  * shape alone fixes, rounded once.
+ * NaN and +infinity: over the chosen experts (renormalize = 1) only the chosen
+ * logits are read.  A chosen +infinity makes the chosen ones' gradients NaN; a
+ * NaN, which is never chosen, has no part, though the router gave its row NaN
+ * weights (what the caller makes of those comes back as grad_weights).  Over all
+ * experts either makes the row's whole gradient NaN.
  */
 typedef struct moe_ep_route_grad_args {
     const void *logits;          /* [tokens][num_experts] row_type           */
