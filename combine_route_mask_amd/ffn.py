@@ -126,9 +126,11 @@ def checkpoint_rows(x, *, out=None, out_scales=None, stream=None) -> MxRows:
 
 
 def restore_rows(rows, scales, *, dtype=None, out=None, stream=None):
-    """MXFP8 rows as bf16 or fp32 rows, ``out``'s type or bf16; bf16 holds
-    code * scale exactly.  ``rows`` and ``scales`` are a checkpoint's, or the
-    bytes (uint8) of an MXFP8 dispatch's payload as the sort leaves them."""
+    """MXFP8 rows as bf16 or fp32 rows, ``out``'s type or bf16.  fp32 holds
+    code * scale exactly, and so does bf16 for scale bytes 3 to 246; for
+    smaller ones it rounds to its least step, 2^-133.  ``rows`` and
+    ``scales`` are a checkpoint's, or the bytes (uint8) of an MXFP8
+    dispatch's payload as the sort leaves them."""
     _no_grad(rows, out)
     if out is not None and dtype not in (None, out.dtype):
         _refuse(f"out is {out.dtype}, the result's dtype {dtype}")

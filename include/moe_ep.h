@@ -578,7 +578,9 @@ int moe_ep_route_top_k_backward(const moe_ep_route_grad_args *args, void *stream
  * e8m0 scale 2^(b - 127) for 32 elements, the smallest power of two that
  * keeps the block's magnitudes within 448; b = 0 for zeros, b = 255 and codes
  * 0x7F for a block with a NaN or an infinity), and back.  restore: code *
- * scale, which bf16 and fp32 hold exactly down to 2^-126.
+ * scale rounded to nearest even: exact in fp32, and in bf16 for b in 3..246
+ * (smaller products are below bf16's least step, 2^-133); what passes the
+ * largest number, from b = 247 on, is infinity.
  * hidden_size a multiple of 32, at most 2^20.
  */
 typedef struct moe_ep_checkpoint_args {
