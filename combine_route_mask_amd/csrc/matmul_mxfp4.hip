@@ -103,8 +103,11 @@ __device__ __forceinline__ void load_word(const uint8_t *base, uint32_t offset, 
 #endif
 }
 
-// WORDS: a row's scales are whole aligned words, else their bytes are read one
-// by one.
+// WORDS: a row's scales are whole aligned words and go through LDS with the stage,
+// else their bytes are read one by one where they are used, and the wait for them
+// is a wait for every stage on its way: 128 rows over 32 experts of 4096 x 7200
+// take 155 us against 106 of 4096 x 7168, of 5760 x 2880 80 against 55 of 5760 x
+// 2816 (3.3 to 3.6 against 4.8 to 5.0 TB/s).
 template <typename T, bool GATED, bool WORDS, typename S>
 __global__ __launch_bounds__(64 * kWaves) void four_bit_kernel(moe_ep_four_bit_args a, int ntiles)
 {

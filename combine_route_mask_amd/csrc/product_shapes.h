@@ -100,7 +100,9 @@ inline Shape weight_grad_shape_of(int64_t num_rows, int num_experts, int n, int 
 // 4096 x 2048 28.5 / 32.5, 64 over 64 of 2048 x 1024 16.7 / 19.9.  For 17 rows or
 // more stages of 64 (one workgroup a CU).  Where 64 channels a workgroup leave
 // CUs without one, 16 channels straight into registers: 16 rows, dense 7168 x
-// 2048, 7.9 / 10.
+// 2048, 7.9 / 10.  The rows an expert are the average, which is what the host
+// knows: with 16 rows a workgroup an expert of more has its weights read again
+// for every 16.
 enum FourBitShape { kFew, kRows16Stages4, kRows16Stages3, kRows64 };
 
 inline FourBitShape four_bit_shape_of(int64_t num_rows, int num_experts, int n)

@@ -44,7 +44,7 @@ class MxRows(NamedTuple):
 class FfnCheckpoint(NamedTuple):
     """What the backward pass of ``expert_ffn`` reads: its input, as it is or
     as MXFP8 codes with scales, and the first product (gate, then up) in fp16
-    with an e8m0 scale for eight, or as MXFP8."""
+    with an e8m0 scale for eight (17 bits an element), or as MXFP8."""
     x: torch.Tensor
     x_scales: Optional[torch.Tensor]
     pre: torch.Tensor
@@ -270,7 +270,9 @@ def expert_matmul_mxfp4(x, weight, weight_scales, *, offsets=None, gated: bool =
     codes a byte, the even element in the low half, ``weight_scales`` e8m0
     [E, N, K / 32] (MXFP4).  ``gated``: N = 2 I channels, gate first, and the
     result is silu(gate) * up [M, I].  Rows, dense weights and ``dtype`` (bf16
-    or fp32) as in ``experts.expert_matmul``."""
+    or fp32) as in ``experts.expert_matmul``.  Fastest for K a multiple of
+    128 and scales that begin on 4 bytes (other calls take 1.4 times as
+    long), and for up to 16 rows an expert."""
     if out is not None and dtype not in (None, out.dtype):
         _refuse(f"out is {out.dtype}, the result's dtype {dtype}")
     _no_grad(x, out)
@@ -305,9 +307,16 @@ def expert_ffn(x, w1, w2, *, offsets=None, checkpoint: str = "bf16", out=None, s
     Differentiable in ``x``, ``w1`` and ``w2`` (without ``out`` or
     ``stream``); the rows outside the experts' ranges are then zeros, and
     their gradients too.  ``checkpoint`` says what the backward pass keeps of
-    x and of the first product: "bf16", x itself and the product in 16 bits, or
-    "mxfp8" (half the memory, H and I multiples of 32; the gradients are then
-    those at the rounded values)."""
+    x and of the first product: "bf16", x itself (a copy where x is a part of
+    a larger buffer, such as a slice of a batch: the next dispatch would
+    overwrite it unseen) and the product in 17 bits an element (fp16, a
+    scale for eight), or "mxfp8", both in 8.25 (H and I multiples of 32; the
+    gradients are then those at the rounded values).
+
+    Sums are fp32, and what passes from one product to the next is bf16, the
+    operand of the matrix cores: the activation and y in the forward pass,
+    the gradient of the first product, the activation again and grad_x in
+    the backward pass, each rounded once."""
     _no_tangent(x, w1, w2)
     _no_grad(out)
     if torch.is_grad_enabled() and (x.requires_grad or w1.requires_grad or w2.requires_grad):
@@ -336,7 +345,8 @@ def _check_ffn(x, w1, w2, offsets):
 
 def expert_ffn_forward(x, w1, w2, *, offsets=None, checkpoint: str = "bf16", stream=None):
     """(y, FfnCheckpoint) of ``expert_ffn``, for ``expert_ffn_backward``.
-    Rows outside the experts' ranges are zeros in y."""
+    Rows outside the experts' ranges are zeros in y.  A "bf16" checkpoint
+    holds x itself, no copy: leave it as it is until the backward pass."""
     _no_grad(x, w1, w2)
     dev = _device(x, "x")
     if stream is not None or dev.index != _device_now():
