@@ -397,11 +397,12 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ void save8(const Job &a, int64_t at, const float *f, bool in)
 {
     uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        top = max(top, magnitude(f[i]));
     if (a.save == MOE_EP_SAVE_HALF) {
-        const uint32_t b = top >= kInfinity ? 127 : min(max(top >> 23, 1u), 253u);
+        // of the finite ones: an infinity or NaN stays what it is at any scale
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            top = max(top, magnitude(f[i]) < kInfinity ? magnitude(f[i]) : 0);
+        const uint32_t b = min(max(top >> 23, 1u), 253u);
         const float by = __uint_as_float((254 - b) << 23);
         f16x8 v;
 #pragma unroll
@@ -413,6 +414,9 @@ __device__ __forceinline__ void save8(const Job &a, int64_t at, const float *f, 
         }
         return;
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        top = max(top, magnitude(f[i]));
     top = max_of_rows(top);
     uint8_t scale;
     const u32x2 codes = mx_codes(f, top, scale);

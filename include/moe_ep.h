@@ -630,10 +630,10 @@ int moe_ep_expert_product(const moe_ep_product_args *args, void *stream);
  * in fp32 from the unrounded sums, rounded once to bf16.  save: pre as the
  * backward pass reads it, as an 8-bit checkpoint (as moe_ep_checkpoint_rows
  * makes of the unrounded sums; I a multiple of 32), or in 16 bits: for eight
- * elements whose largest magnitude is in [2^e, 2^(e+1)) the scale 2^e, as e8m0
- * (b in 1..253; 127 where an element is no finite number), and value / scale
- * rounded to fp16.  That keeps 11 significant bits: with bf16's eight the
- * gradients are half as far off again.
+ * elements whose largest finite magnitude is in [2^e, 2^(e+1)) the scale 2^e, as
+ * e8m0 (b in 1..253), and value / scale rounded to fp16 (infinities and NaN
+ * stay).  That keeps 11 significant bits: with bf16's eight the gradients are half
+ * as far off again.
  * I and k multiples of 8, at most 65536 and 131072.
  */
 typedef struct moe_ep_gated_args {
