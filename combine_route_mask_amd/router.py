@@ -38,7 +38,9 @@ def route_top_k(logits, top_k: int, *, renormalize: bool = True, scale: float = 
     id E, which a dispatch routes nowhere and a sort passes over, and the
     weight 0.  A row with a NaN or +infinity has NaN weights.
 
-    Differentiable in ``logits`` (without given outputs or ``stream``)."""
+    Differentiable in ``logits`` (without given outputs or ``stream``); the
+    backward pass keeps them, a copy where they are a part of a larger
+    buffer, such as a dispatch's workspace."""
     _no_tangent(logits)
     _no_grad(weights)
     if logits.requires_grad and torch.is_grad_enabled():
@@ -116,6 +118,9 @@ class _RouteFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top_k, renormalize, scale):
         r = _route(logits, top_k, renormalize, scale, None, None, None)
+        if logits.untyped_storage().nbytes() != logits.numel() * logits.element_size():
+            # a part of a workspace, which the next dispatch overwrites unseen by autograd
+            logits = logits.clone()
         ctx.save_for_backward(logits, r.ids)
         ctx.rule = renormalize, scale
         ctx.mark_non_differentiable(r.ids)
